@@ -12,6 +12,10 @@ Entry points (same names as the C ABI):
   kda_decode_multi(cfg, q, ..., state_pool, conv_pool, slots=, n_commit=)
   kda_decode_step_gated / kda_decode_multi_gated   the same, output epilogue fused
   kda_output_gate(cfg, o, gate, o_norm_weight)     the output epilogue alone
+  kda_add_rmsnorm(cfg, x, residual, weight)        the norm in front of a layer, and its residual's addition
+  kda_add_rmsnorm_fp8 / kda_output_gate_fp8        the norm / the epilogue with e4m3 rows and block scales
+  kda_add_rmsnorm_backward / kda_output_gate_backward
+  kda_fp8_matmul(cfg, a, a_scale, w, w_scale)      a projection of e4m3 rows
   kda_prefill_workspace_bytes / kda_varlen_workspace_bytes / kda_prefill_slab_workspace_bytes
 """
 from __future__ import annotations
@@ -42,13 +46,20 @@ FLAG_RAW_GATE = 1 << 2
 FLAG_RAW_BETA = 1 << 3
 FLAG_BETA_X2 = 1 << 4
 
-STAGES = ("chunk_table", "chunk_prep", "chunk_scan", "conv_state", "decode", "output_gate", "backward")
+STAGES = ("chunk_table", "chunk_prep", "chunk_scan", "conv_state", "decode", "output_gate", "backward", "norm",
+          "matmul")
 NUM_STAGES = len(STAGES)
 
 EXPORTED = ("kda_version", "kda_status_string", "kda_prefill_workspace_bytes", "kda_prefill",
             "kda_varlen_workspace_bytes", "kda_varlen_prefill", "kda_decode_step", "kda_decode_multi",
             "kda_decode_step_gated", "kda_decode_multi_gated", "kda_output_gate", "kda_varlen_prefill_noalloc",
-            "kda_varlen_backward_workspace_bytes", "kda_varlen_backward", "kda_prefill_slab_workspace_bytes")
+            "kda_varlen_backward_workspace_bytes", "kda_varlen_backward", "kda_prefill_slab_workspace_bytes",
+            "kda_add_rmsnorm", "kda_add_rmsnorm_fp8", "kda_add_rmsnorm_backward_workspace_bytes",
+            "kda_add_rmsnorm_backward", "kda_output_gate_fp8", "kda_output_gate_backward_workspace_bytes",
+            "kda_output_gate_backward", "kda_fp8_matmul")
+
+# consecutive values of an e4m3 row that share a scale
+SCALE_BLOCK = 128
 
 # the fixed scratch behind kda_varlen_prefill_noalloc (KDA_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 256 << 20
@@ -119,6 +130,23 @@ def _load_library():
                                            ctypes.c_float, vp, vp, vp]
     lib.kda_output_gate.restype = ctypes.c_int
     lib.kda_output_gate.argtypes = [cfgp, ctypes.c_int64, vp, vp, vp, ctypes.c_float, vp, vp]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.kda_add_rmsnorm.restype = ctypes.c_int
+    lib.kda_add_rmsnorm.argtypes = [cfgp, i64, i32, vp, vp, vp, f32, vp, vp, vp]
+    lib.kda_add_rmsnorm_fp8.restype = ctypes.c_int
+    lib.kda_add_rmsnorm_fp8.argtypes = [cfgp, i64, i32, vp, vp, vp, f32, vp, vp, vp, vp]
+    lib.kda_add_rmsnorm_backward_workspace_bytes.restype = sz
+    lib.kda_add_rmsnorm_backward_workspace_bytes.argtypes = [cfgp, i64, i32]
+    lib.kda_add_rmsnorm_backward.restype = ctypes.c_int
+    lib.kda_add_rmsnorm_backward.argtypes = [cfgp, i64, i32, vp, vp, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_output_gate_fp8.restype = ctypes.c_int
+    lib.kda_output_gate_fp8.argtypes = [cfgp, i64, vp, vp, vp, f32, vp, vp, vp]
+    lib.kda_output_gate_backward_workspace_bytes.restype = sz
+    lib.kda_output_gate_backward_workspace_bytes.argtypes = [cfgp, i64]
+    lib.kda_output_gate_backward.restype = ctypes.c_int
+    lib.kda_output_gate_backward.argtypes = [cfgp, i64, vp, vp, vp, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_fp8_matmul.restype = ctypes.c_int
+    lib.kda_fp8_matmul.argtypes = [cfgp, i64, i32, i32, vp, vp, vp, vp, vp, vp]
     return lib
 
 
@@ -401,4 +429,181 @@ def kda_output_gate(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, *, y
     st = _lib.kda_output_gate(ctypes.byref(cfg.c_struct()), n_tokens, _ptr(o), _ptr(gate), _ptr(o_norm_weight),
                               float(eps), _ptr(y), _stream(stream))
     _check(st, "kda_output_gate")
+    return y
+
+
+# ---- the operators around the core -----------------------------------------
+# These take their device and default stream from their tensors, check shapes
+# and types, and allocate what they return on the stream that they run on.
+
+class _On:
+    """The device of a call's tensors made current, and the call's stream:
+    `stream`, or that device's current one."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("tensors must be on the GPU")
+        if stream is not None and stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.other = torch.cuda.device(self.device) if torch.cuda.current_device() != self.device.index else None
+        if self.other is not None:
+            self.other.__enter__()
+        self.inner = torch.cuda.stream(self.stream) if self.stream is not None else None
+        if self.inner is not None:
+            self.inner.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+
+def _want(name, t, shape, dtype, device):
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}, "
+                         f"not {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+
+
+def _scale_blocks(k: int) -> int:
+    return (k + SCALE_BLOCK - 1) // SCALE_BLOCK
+
+
+def _add_rmsnorm(name, cfg, x, residual, weight, eps, h, y, y_scale, stream, fp8):
+    hidden, dev = x.shape[-1], x.device
+    n = x.numel() // hidden if x.numel() else 0
+    out = torch.float8_e4m3fn if fp8 else cfg.out_dtype
+    blocks = (*x.shape[:-1], _scale_blocks(hidden))
+    _want("x", x, x.shape, cfg.io_dtype, dev)
+    _want("residual", residual, x.shape, cfg.io_dtype, dev)
+    _want("weight", weight, (hidden,), torch.float32, dev)
+    _want("h", h, x.shape, cfg.io_dtype, dev)
+    _want("y", y, x.shape, out, dev)
+    _want("y_scale", y_scale, blocks, torch.float32, dev)
+    with _On(dev, stream) as st:
+        if h is None and residual is not None:
+            h = torch.empty_like(x)
+        if y is None:
+            y = torch.empty(x.shape, dtype=out, device=dev)
+        args = [ctypes.byref(cfg.c_struct()), n, hidden, _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(h),
+                _ptr(y)]
+        if fp8:
+            if y_scale is None:
+                y_scale = torch.empty(blocks, dtype=torch.float32, device=dev)
+            args.append(_ptr(y_scale))
+        _check(getattr(_lib, name)(*args, st), name)
+    return y, y_scale, x if h is None else h
+
+
+def kda_add_rmsnorm(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=None, y=None, stream=None):
+    """h = x + residual and y = h / sqrt(mean(h^2) + eps) * weight per row:
+    x, residual [..., hidden] io dtype (residual may be None), weight [hidden]
+    fp32.  Returns (y, h), y in the out dtype, h in the io dtype (x itself
+    without a residual or h).  h=x or h=residual works in place."""
+    y, _, h = _add_rmsnorm("kda_add_rmsnorm", cfg, x, residual, weight, eps, h, y, None, stream, False)
+    return y, h
+
+
+def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=None, y=None, y_scale=None,
+                        stream=None):
+    """kda_add_rmsnorm with y as e4m3 rows.  Returns (y, y_scale, h): y
+    [..., hidden] float8_e4m3fn, y_scale [..., ceil(hidden / 128)] fp32."""
+    return _add_rmsnorm("kda_add_rmsnorm_fp8", cfg, x, residual, weight, eps, h, y, y_scale, stream, True)
+
+
+def kda_add_rmsnorm_backward(cfg: Config, h, weight, dy, d_h=None, eps: float = 1e-6, *, dx=None, workspace=None,
+                             stream=None):
+    """Gradients of kda_add_rmsnorm: h as it returned it, dy [..., hidden] in
+    the out dtype, d_h the gradient that reaches h otherwise (fp32) or None.
+    Returns (dx [..., hidden], dweight [hidden]), fp32; dx is the gradient of x
+    and of residual alike.  dx=d_h works in place."""
+    hidden, dev = h.shape[-1], h.device
+    n = h.numel() // hidden if h.numel() else 0
+    _want("h", h, h.shape, cfg.io_dtype, dev)
+    _want("weight", weight, (hidden,), torch.float32, dev)
+    _want("dy", dy, h.shape, cfg.out_dtype, dev)
+    _want("d_h", d_h, h.shape, torch.float32, dev)
+    _want("dx", dx, h.shape, torch.float32, dev)
+    with _On(dev, stream) as st:
+        if dx is None:
+            dx = torch.empty(h.shape, dtype=torch.float32, device=dev)
+        dw = torch.empty((hidden,), dtype=torch.float32, device=dev)
+        c = ctypes.byref(cfg.c_struct())
+        ws = _workspace(int(_lib.kda_add_rmsnorm_backward_workspace_bytes(c, n, hidden)), dev, workspace)
+        _check(_lib.kda_add_rmsnorm_backward(c, n, hidden, _ptr(h), _ptr(weight), float(eps), _ptr(dy), _ptr(d_h),
+                                             _ptr(dx), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(), st),
+               "kda_add_rmsnorm_backward")
+    return dx, dw
+
+
+def kda_output_gate_fp8(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, *, y=None, y_scale=None, stream=None):
+    """kda_output_gate with its output as e4m3 rows: o [..., H, dv] out dtype,
+    gate the same shape in the io dtype.  Returns (y [..., H * dv]
+    float8_e4m3fn, y_scale [..., ceil(H * dv / 128)] fp32)."""
+    H, dv, dev = cfg.num_heads, cfg.head_v_dim, o.device
+    lead = tuple(o.shape[:-2])
+    _want("o", o, (*lead, H, dv), cfg.out_dtype, dev)
+    _want("gate", gate, (*lead, H, dv), cfg.io_dtype, dev)
+    _want("o_norm_weight", o_norm_weight, (dv,), torch.float32, dev)
+    _want("y", y, (*lead, H * dv), torch.float8_e4m3fn, dev)
+    _want("y_scale", y_scale, (*lead, _scale_blocks(H * dv)), torch.float32, dev)
+    with _On(dev, stream) as st:
+        if y is None:
+            y = torch.empty((*lead, H * dv), dtype=torch.float8_e4m3fn, device=dev)
+        if y_scale is None:
+            y_scale = torch.empty((*lead, _scale_blocks(H * dv)), dtype=torch.float32, device=dev)
+        _check(_lib.kda_output_gate_fp8(ctypes.byref(cfg.c_struct()), o.numel() // (H * dv), _ptr(o), _ptr(gate),
+                                        _ptr(o_norm_weight), float(eps), _ptr(y), _ptr(y_scale), st),
+               "kda_output_gate_fp8")
+    return y, y_scale
+
+
+def kda_output_gate_backward(cfg: Config, o, gate, o_norm_weight, dy, eps: float = 1e-6, *, workspace=None,
+                             stream=None):
+    """Gradients of kda_output_gate: o, dy [..., H, dv] out dtype, gate the
+    same shape in the io dtype.  Returns (d_o in the out dtype, as
+    kda_varlen_backward takes it, d_gate fp32, d_weight [dv] fp32)."""
+    H, dv, dev = cfg.num_heads, cfg.head_v_dim, o.device
+    lead = tuple(o.shape[:-2])
+    _want("o", o, (*lead, H, dv), cfg.out_dtype, dev)
+    _want("gate", gate, (*lead, H, dv), cfg.io_dtype, dev)
+    _want("o_norm_weight", o_norm_weight, (dv,), torch.float32, dev)
+    _want("dy", dy, (*lead, H, dv), cfg.out_dtype, dev)
+    n = o.numel() // (H * dv)
+    with _On(dev, stream) as st:
+        d_o = torch.empty_like(o)
+        d_gate = torch.empty(gate.shape, dtype=torch.float32, device=dev)
+        dw = torch.empty((dv,), dtype=torch.float32, device=dev)
+        c = ctypes.byref(cfg.c_struct())
+        ws = _workspace(int(_lib.kda_output_gate_backward_workspace_bytes(c, n)), dev, workspace)
+        _check(_lib.kda_output_gate_backward(c, n, _ptr(o), _ptr(gate), _ptr(o_norm_weight), float(eps), _ptr(dy),
+                                             _ptr(d_o), _ptr(d_gate), _ptr(dw), _ptr(ws),
+                                             ws.numel() * ws.element_size(), st),
+               "kda_output_gate_backward")
+    return d_o, d_gate, dw
+
+
+def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
+    """y = a w^T of e4m3 operands: a [..., K] float8_e4m3fn with a_scale
+    [..., ceil(K / 128)] fp32 (as kda_add_rmsnorm_fp8 and kda_output_gate_fp8
+    return them), w [N, K] float8_e4m3fn with w_scale [ceil(N / 128),
+    ceil(K / 128)] fp32.  Returns y [..., N] in the out dtype."""
+    (N, K), dev = w.shape, a.device
+    lead = tuple(a.shape[:-1])
+    _want("a", a, (*lead, K), torch.float8_e4m3fn, dev)
+    _want("a_scale", a_scale, (*lead, _scale_blocks(K)), torch.float32, dev)
+    _want("w", w, (N, K), torch.float8_e4m3fn, dev)
+    _want("w_scale", w_scale, (_scale_blocks(N), _scale_blocks(K)), torch.float32, dev)
+    _want("y", y, (*lead, N), cfg.out_dtype, dev)
+    with _On(dev, stream) as st:
+        if y is None:
+            y = torch.empty((*lead, N), dtype=cfg.out_dtype, device=dev)
+        _check(_lib.kda_fp8_matmul(ctypes.byref(cfg.c_struct()), math.prod(lead), N, K, _ptr(a), _ptr(a_scale),
+                                   _ptr(w), _ptr(w_scale), _ptr(y), st), "kda_fp8_matmul")
     return y

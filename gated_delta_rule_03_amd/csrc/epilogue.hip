@@ -11,77 +11,13 @@
 // the rows.
 #include "kda_device.h"
 #include "kda_internal.h"
-#include "mfma.h"
+#include "vec_io.h"
 
 namespace kda {
 
 namespace {
 
 constexpr int kEpiThreads = 256;
-
-// EPL consecutive io elements (EPL in {1, 2, 4, 8}) at index i of a bf16 or
-// fp32 tensor, as floats, with the widest aligned loads.
-template <bool BF16, int EPL>
-__device__ __forceinline__ void load_n(const void* p, size_t i, float (&x)[EPL]) {
-  if constexpr (BF16) {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
-    uint32_t w[(EPL + 1) / 2];
-    if constexpr (EPL == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q);
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else if constexpr (EPL == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(q);
-      w[0] = v.x; w[1] = v.y;
-    } else if constexpr (EPL == 2) {
-      w[0] = *reinterpret_cast<const uint32_t*>(q);
-    } else {
-      w[0] = *q;
-    }
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) x[e] = __uint_as_float((e & 1) ? (w[e / 2] & 0xffff0000u) : (w[e / 2] << 16));
-  } else {
-    const float* q = static_cast<const float*>(p) + i;
-#pragma unroll
-    for (int e = 0; e < EPL; e += (EPL >= 4 ? 4 : EPL)) {
-      if constexpr (EPL >= 4) {
-        const float4 v = *reinterpret_cast<const float4*>(q + e);
-        x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
-      } else if constexpr (EPL == 2) {
-        const float2 v = *reinterpret_cast<const float2*>(q);
-        x[0] = v.x; x[1] = v.y;
-      } else {
-        x[0] = *q;
-      }
-    }
-  }
-}
-
-template <bool BF16, int EPL>
-__device__ __forceinline__ void store_n(void* p, size_t i, const float (&x)[EPL]) {
-  if constexpr (BF16) {
-    uint16_t* q = static_cast<uint16_t*>(p) + i;
-    if constexpr (EPL == 1) {
-      *q = static_cast<uint16_t>(pack_bf16x2(x[0], 0.f));
-    } else {
-      uint32_t w[EPL / 2];
-#pragma unroll
-      for (int e = 0; e < EPL / 2; ++e) w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-      if constexpr (EPL == 8) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-      else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(q) = w[0];
-    }
-  } else {
-    float* q = static_cast<float*>(p) + i;
-    if constexpr (EPL >= 4) {
-#pragma unroll
-      for (int e = 0; e < EPL; e += 4) *reinterpret_cast<float4*>(q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-    } else if constexpr (EPL == 2) {
-      *reinterpret_cast<float2*>(q) = make_float2(x[0], x[1]);
-    } else {
-      *q = x[0];
-    }
-  }
-}
 
 }  // namespace
 
@@ -137,6 +73,175 @@ hipError_t launch_output_gate(int D, int64_t rows, const void* o, const void* ga
     case 128: return launch_output_gate_d<128>(rows, o, gate, w, eps, y, o_bf16, g_bf16, st);
     default: return hipErrorInvalidValue;
   }
+}
+
+// The epilogue with its output in e4m3, the operand of the out projection: a
+// token's heads side by side are one row of H * dv channels, in blocks of 128
+// (whole heads: dv divides 128) with one scale each.  16 lanes hold a block,
+// 8 channels a lane, so dv / 8 lanes sum a head's squares and all 16 the
+// block's largest value, all in DPP steps.
+template <int DV, bool O_BF16, bool G_BF16>
+__global__ __launch_bounds__(kEpiThreads) void output_gate_fp8_kernel(int64_t units, int row, const void* o,
+                                                                      const void* gate, const float* __restrict__ w,
+                                                                      float eps, uint8_t* __restrict__ y,
+                                                                      float* __restrict__ scale) {
+  const int l16 = threadIdx.x & 15;
+  const int nblk = (row + kScaleBlock - 1) / kScaleBlock;
+  const int64_t step = (static_cast<int64_t>(gridDim.x) * kEpiThreads) >> 4;
+  float wv[8];
+  load_n<false, 8>(w, (l16 * 8) % DV, wv);
+  // uniform over the wave, so every lane takes part in its group's DPP steps
+  for (int64_t u0 = (static_cast<int64_t>(blockIdx.x) * kEpiThreads + (threadIdx.x & ~63)) >> 4; u0 < units; u0 += step) {
+    const int64_t u = u0 + ((threadIdx.x & 63) >> 4);
+    // with whole blocks only, unit u of the tensor starts at element 128 u
+    int64_t token = 0;
+    int blk = 0, left = kScaleBlock;
+    size_t base = static_cast<size_t>(u) * kScaleBlock;
+    if (row % kScaleBlock) {
+      token = u / nblk;
+      blk = static_cast<int>(u - token * nblk);
+      left = row - blk * kScaleBlock;
+      base = static_cast<size_t>(token) * row + static_cast<size_t>(blk) * kScaleBlock;
+    }
+    const bool mine = u < units && l16 * 8 < left;
+    float ov[8] = {}, gv[8] = {};
+    if (mine) {
+      load_n<O_BF16, 8>(o, base + l16 * 8, ov);
+      load_n<G_BF16, 8>(gate, base + l16 * 8, gv);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(ov[e], ov[e], ss);
+    ss = dpp_group_sum<DV / 8>(ss);
+    float inv = 1.0f / sqrtf(ss * (1.0f / DV) + eps);
+    // heads narrower than a block have norms of their own inside it, and lanes
+    // past the row's end none (with eps = 0 it would be infinite)
+    const float each = DV == kScaleBlock ? 1.0f : (mine ? inv : 0.0f);
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = ov[e] * wv[e] * sigmoidf_(gv[e]) * each;
+    float s;
+    const uint2 q = quantise_block8(t, DV == kScaleBlock ? inv : 1.0f, &s);
+    if (mine) {
+      *reinterpret_cast<uint2*>(y + base + l16 * 8) = q;
+      if (l16 == 0) scale[u] = s;
+    }
+  }
+}
+
+// The epilogue's backward pass, with n = o / sqrt(mean o^2 + eps) per head,
+// s = sigmoid(gate) and g = dy * w * s:
+//   d_o = (g - n * mean(g * n)) / sqrt(mean o^2 + eps)
+//   dgate = dy * w * n * s (1 - s),  dw = sum over tokens and heads of dy * n * s
+// One pass over the rows, 8 channels a lane.  A lane keeps its channels for
+// the whole launch, so dw gathers in registers; a workgroup joins its lanes
+// in LDS and leaves one row of `part`.  The order of every sum is fixed.
+template <int DV, bool O_BF16, bool G_BF16>
+__global__ __launch_bounds__(kEpiThreads) void output_gate_bwd_kernel(int64_t chunks, const void* __restrict__ o,
+                                                                      const void* __restrict__ gate,
+                                                                      const float* __restrict__ w, float eps,
+                                                                      const void* __restrict__ dy,
+                                                                      void* __restrict__ d_o,
+                                                                      float* __restrict__ dgate,
+                                                                      float* __restrict__ part) {
+  constexpr int kLanes = DV / 8;   // lanes of a head's row
+  __shared__ float red[kEpiThreads][8];
+  float wv[8], dw[8] = {};
+  load_n<false, 8>(w, (threadIdx.x % kLanes) * 8, wv);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kEpiThreads;
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kEpiThreads + (threadIdx.x & ~63); c0 < chunks; c0 += step) {
+    const int64_t c = c0 + (threadIdx.x & 63);
+    const bool mine = c < chunks;   // all or none of a head's lanes
+    const size_t base = static_cast<size_t>(c) * 8;
+    float ov[8] = {}, gv[8] = {}, dv[8] = {};
+    if (mine) {
+      load_n<O_BF16, 8>(o, base, ov);
+      load_n<G_BF16, 8>(gate, base, gv);
+      load_n<O_BF16, 8>(dy, base, dv);
+    }
+    float ss = 0.f, sg = 0.f, sig[8], off[8];   // off = 1 - sigmoid, exact also where the sigmoid is near 1
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = exp_fast(-gv[e]);
+      sig[e] = rcp_fast(1.0f + x);
+      off[e] = fminf(x, 1e38f) * sig[e];   // (an infinite x has sigmoid 0)
+      ss = fmaf(ov[e], ov[e], ss);
+      sg = fmaf(dv[e] * wv[e] * sig[e], ov[e], sg);
+    }
+    ss = dpp_group_sum<kLanes>(ss);
+    sg = dpp_group_sum<kLanes>(sg);
+    const float inv = 1.0f / sqrtf(ss * (1.0f / DV) + eps);
+    const float k = sg * (1.0f / DV) * inv * inv;   // n * mean(g n) = o * k
+    float a[8], b[8];
+    if (mine) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = ov[e] * inv, ds = dv[e] * sig[e];
+        dw[e] = fmaf(ds, n, dw[e]);
+        a[e] = inv * fmaf(-ov[e], k, ds * wv[e]);
+        b[e] = ds * wv[e] * n * off[e];
+      }
+      store_n<O_BF16, 8>(d_o, base, a);
+      store_n<false, 8>(dgate, base, b);
+    }
+  }
+  store_n<false, 8>(&red[threadIdx.x][0], 0, dw);
+  __syncthreads();
+  if (threadIdx.x < DV) {
+    float s = 0.f;
+    for (int t = threadIdx.x / 8; t < kEpiThreads; t += kLanes) s += red[t][threadIdx.x & 7];
+    part[static_cast<size_t>(blockIdx.x) * DV + threadIdx.x] = s;
+  }
+}
+
+// Calls f with the head size and the two types as constants.
+template <class F>
+static hipError_t with_gate_types(int D, bool o_bf16, bool g_bf16, F&& f) {
+  auto by_type = [&](auto d) {
+    if (o_bf16 && g_bf16) f(d, std::true_type{}, std::true_type{});
+    else if (o_bf16) f(d, std::true_type{}, std::false_type{});
+    else if (g_bf16) f(d, std::false_type{}, std::true_type{});
+    else f(d, std::false_type{}, std::false_type{});
+    return hipGetLastError();
+  };
+  switch (D) {
+    case 16: return by_type(std::integral_constant<int, 16>{});
+    case 32: return by_type(std::integral_constant<int, 32>{});
+    case 64: return by_type(std::integral_constant<int, 64>{});
+    case 128: return by_type(std::integral_constant<int, 128>{});
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_output_gate_fp8(int D, int64_t n_tokens, int row, const void* o, const void* gate, const float* w,
+                                  float eps, uint8_t* y, float* scale, bool o_bf16, bool g_bf16, hipStream_t st) {
+  const int64_t units = n_tokens * ((row + kScaleBlock - 1) / kScaleBlock);
+  const int64_t blocks = (units + kEpiThreads / 16 - 1) / (kEpiThreads / 16);
+  const dim3 grid(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)));
+  return with_gate_types(D, o_bf16, g_bf16, [&](auto d, auto ob, auto gb) {
+    output_gate_fp8_kernel<decltype(d)::value, decltype(ob)::value, decltype(gb)::value>
+        <<<grid, kEpiThreads, 0, st>>>(units, row, o, gate, w, eps, y, scale);
+  });
+}
+
+// Workgroups of the backward, each with a row of partial sums.
+int output_gate_bwd_parts(int D, int64_t rows) {
+  const int64_t blocks = (rows * (D / 8) + kEpiThreads - 1) / kEpiThreads;
+  return static_cast<int>(blocks < 2048 ? blocks : 2048);
+}
+
+hipError_t launch_output_gate_bwd(int D, int64_t rows, const void* o, const void* gate, const float* w, float eps,
+                                  const void* dy, void* d_o, float* dgate, float* dw, float* part, bool o_bf16,
+                                  bool g_bf16, hipStream_t st) {
+  const int parts = output_gate_bwd_parts(D, rows);
+  if (parts > 0) {
+    const hipError_t e = with_gate_types(D, o_bf16, g_bf16, [&](auto d, auto ob, auto gb) {
+      output_gate_bwd_kernel<decltype(d)::value, decltype(ob)::value, decltype(gb)::value>
+          <<<dim3(parts), kEpiThreads, 0, st>>>(rows * (D / 8), o, gate, w, eps, dy, d_o, dgate, part);
+    });
+    if (e != hipSuccess) return e;
+  }
+  return launch_column_sums(parts, D, part, dw, st);
 }
 
 }  // namespace kda

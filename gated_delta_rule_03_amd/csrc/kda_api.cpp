@@ -5,15 +5,17 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "api_util.h"
 #include "kda_internal.h"
 
 namespace {
 
+using kda::align_up;
 using kda::ChunkTable;
 using kda::Params;
 using kda::PrefillIO;
+using kda::stage;
 
-constexpr size_t kAlign = 256;
 constexpr uint32_t kKnownFlags = KDA_FLAG_SKIP_CONV | KDA_FLAG_SKIP_L2NORM | KDA_FLAG_RAW_GATE |
                                  KDA_FLAG_RAW_BETA | KDA_FLAG_BETA_X2;
 // Sub-block decay factors e^{-P} of 16 tokens stay finite in fp32 when every
@@ -21,8 +23,6 @@ constexpr uint32_t kKnownFlags = KDA_FLAG_SKIP_CONV | KDA_FLAG_SKIP_L2NORM | KDA
 // it (down to -inf, no clamp) routes a prefill to the recurrent form, whose
 // state is only ever multiplied by e^g <= 1.
 constexpr float kChunkedGateFloor = -5.4f;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 kda_status_t check_config(const kda_config_t* cfg, bool chunked) {
   if (!cfg) return KDA_ERR_INVALID_ARGUMENT;
@@ -93,24 +93,6 @@ Layout make_layout(const kda_config_t* cfg, int64_t N, int64_t max_chunks, int64
 
 int64_t chunks_uniform(int64_t B, int64_t T) { return B * ((T + kda::kChunk - 1) / kda::kChunk); }
 int64_t chunks_varlen(int64_t N, int64_t total_T) { return (total_T + kda::kChunk - 1) / kda::kChunk + N; }
-
-kda_status_t hip_status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
-
-// Records the caller's timing event `which` (0 = before, 1 = after) of a stage.
-void mark(const kda_config_t* cfg, int stage, int which, hipStream_t st) {
-  if (!cfg->stage_events) return;
-  void* ev = cfg->stage_events[2 * stage + which];
-  if (ev) (void)hipEventRecord(static_cast<hipEvent_t>(ev), st);
-}
-
-// Runs one stage's launcher between its two timing marks.
-template <class F>
-kda_status_t stage(const kda_config_t* cfg, int s, hipStream_t st, F&& launch) {
-  mark(cfg, s, 0, st);
-  const hipError_t e = launch();
-  mark(cfg, s, 1, st);
-  return hip_status(e);
-}
 
 // The shared prefill pipeline over a packed batch.
 kda_status_t run_prefill(const kda_config_t* cfg, int32_t N, int64_t total_T, int64_t max_chunks,

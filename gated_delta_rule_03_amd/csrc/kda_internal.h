@@ -144,6 +144,39 @@ hipError_t launch_recurrent_scan(const Params& p, const ChunkTable& t, const Pre
 hipError_t launch_output_gate(int D, int64_t rows, const void* o, const void* gate, const float* w, float eps,
                               void* y, bool o_bf16, bool g_bf16, hipStream_t st);
 
+// The same with e4m3 outputs: a token's H * D outputs are one row of `row`
+// channels, in blocks of 128 with one scale each.
+hipError_t launch_output_gate_fp8(int D, int64_t n_tokens, int row, const void* o, const void* gate, const float* w,
+                                  float eps, uint8_t* y, float* scale, bool o_bf16, bool g_bf16, hipStream_t st);
+
+// Its backward pass over `rows` (token, head) rows.  part holds
+// output_gate_bwd_parts rows of D partial sums of dw.
+int output_gate_bwd_parts(int D, int64_t rows);
+hipError_t launch_output_gate_bwd(int D, int64_t rows, const void* o, const void* gate, const float* w, float eps,
+                                  const void* dy, void* d_o, float* dgate, float* dw, float* part, bool o_bf16,
+                                  bool g_bf16, hipStream_t st);
+
+// out[c] = sum over p < parts of part[p][c] (zeros when parts == 0), in a fixed order.
+hipError_t launch_column_sums(int parts, int cols, const float* part, float* out, hipStream_t st);
+
+// The residual's addition and the RMS norm over n rows of `hidden` channels (a
+// multiple of 8, at most kMaxHidden); res and h may be null.  scale picks the
+// e4m3 output, otherwise out_bf16 the type of y.
+constexpr int kMaxHidden = 32768;
+hipError_t launch_add_rmsnorm(int64_t n, int hidden, const void* x, const void* res, const float* w, float eps,
+                              void* h, void* y, float* scale, bool io_bf16, bool out_bf16, hipStream_t st);
+
+// Its backward pass; dh may be null and may be dx.  part holds
+// add_rmsnorm_bwd_parts rows of `hidden` partial sums of dw.
+int add_rmsnorm_bwd_parts(int64_t n);
+hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const float* w, float eps, const void* dy,
+                                  const float* dh, float* dx, float* dw, float* part, bool h_bf16, bool dy_bf16,
+                                  hipStream_t st);
+
+// y [M][N] = a [M][K] w [N][K]^T, e4m3 with scales per 1 x 128 (a) and 128 x 128 (w).
+hipError_t launch_fp8_matmul(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
+                             const float* sw, void* y, bool out_bf16, hipStream_t st);
+
 struct DecodeIO {
   const void* q;
   const void* k;

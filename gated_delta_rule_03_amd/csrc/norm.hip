@@ -1,0 +1,299 @@
+// The norm in front of a KDA layer, with the residual's addition:
+//   h = x + residual (rounded to the io type, as it is stored)
+//   y = h / sqrt(mean_j h[j]^2 + eps) * w[j]
+// in bf16 / fp32, or as e4m3 values with one fp32 scale per 128 channels (the
+// operand of the block-scaled product); and its backward pass, with n = h /
+// sqrt(mean h^2 + eps) and g = dy * w:
+//   dx = (g - n * mean(g * n)) / sqrt(mean h^2 + eps) + d_h
+//   dw = sum over tokens of dy * n
+//
+// HBM-bound: each row is read once and kept in registers between the row's
+// sums and its outputs.  A row belongs to WPR waves, 8 channels a lane and
+// step (16-byte loads in bf16), NV steps; 16 lanes hold one scale block, so
+// its largest value is four DPP steps.
+#include "kda_device.h"
+#include "kda_internal.h"
+#include "vec_io.h"
+
+namespace kda {
+
+namespace {
+
+enum class Out { kBf16, kFp32, kFp8 };
+
+// Sums of A values over the WPR waves of a row, in every lane.  `parity`
+// alternates between the two halves of `red`, so one barrier per call is
+// enough: a wave that writes a half again has passed the barrier of the call
+// in between, which every wave reaches after reading that half.
+template <int WPR, int A>
+__device__ __forceinline__ void row_sums(float (&s)[A], float (*red)[16][A], int wave, int parity) {
+#pragma unroll
+  for (int a = 0; a < A; ++a) {
+    s[a] = lane_group_sum<16>(s[a]);
+    s[a] += __shfl_xor(s[a], 16);
+    s[a] += __shfl_xor(s[a], 32);
+  }
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int a = 0; a < A; ++a) red[parity][wave][a] = s[a];
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) t += red[parity][w][a];
+      s[a] = t;
+    }
+  }
+}
+
+// Waves of a workgroup: one row at a time, or four rows of one wave each.
+constexpr int waves_of(int wpr) { return wpr < 4 ? 4 : wpr; }
+
+}  // namespace
+
+template <bool BF16, Out OUT, int WPR, int NV>
+__global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_kernel(
+    int64_t n_rows, int hidden, const void* x, const void* res, const float* __restrict__ w, float eps, void* h,
+    void* y, float* __restrict__ scale) {
+  constexpr int kRows = waves_of(WPR) / WPR;   // rows at a time
+  __shared__ float red[2][16][1];
+  const int lane = threadIdx.x & 63;
+  const int wave = (threadIdx.x >> 6) % WPR;
+  const int nvec = hidden >> 3;
+  const int nblk = (hidden + kScaleBlock - 1) / kScaleBlock;
+  const float rcp = 1.0f / static_cast<float>(hidden);
+  float wv[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = (i * WPR + wave) * 64 + lane;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wv[i][e] = 0.f;
+    if (v < nvec) load_n<false, 8>(w, static_cast<size_t>(v) * 8, wv[i]);
+  }
+  int parity = 0;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + (WPR == 1 ? threadIdx.x >> 6 : 0); r < n_rows;
+       r += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
+    const size_t base = static_cast<size_t>(r) * hidden;
+    float hv[NV][8];
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = (i * WPR + wave) * 64 + lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) hv[i][e] = 0.f;
+      if (v < nvec) {
+        load_n<BF16, 8>(x, base + static_cast<size_t>(v) * 8, hv[i]);
+        if (res) {
+          float rv[8];
+          load_n<BF16, 8>(res, base + static_cast<size_t>(v) * 8, rv);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) hv[i][e] += rv[e];
+          if constexpr (BF16) {   // the norm is of the stored sum
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const uint32_t p = pack_bf16x2(hv[i][e], hv[i][e + 1]);
+              hv[i][e] = __uint_as_float(p << 16);
+              hv[i][e + 1] = __uint_as_float(p & 0xffff0000u);
+            }
+          }
+        }
+        if (h) store_n<BF16, 8>(h, base + static_cast<size_t>(v) * 8, hv[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss[0] = fmaf(hv[i][e], hv[i][e], ss[0]);
+      }
+    }
+    row_sums<WPR, 1>(ss, red, wave, parity);
+    const float inv = 1.0f / sqrtf(ss[0] * rcp + eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = (i * WPR + wave) * 64 + lane;
+      float t[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = hv[i][e] * wv[i][e];
+      if constexpr (OUT == Out::kFp8) {
+        float s;
+        const uint2 q = quantise_block8(t, inv, &s);   // all 64 lanes: zeros past the row's end
+        if (v < nvec) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(y) + base + static_cast<size_t>(v) * 8) = q;
+          if ((lane & 15) == 0) scale[static_cast<size_t>(r) * nblk + (v >> 4)] = s;
+        }
+      } else if (v < nvec) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = hv[i][e] * inv * wv[i][e];
+        store_n<OUT == Out::kBf16, 8>(y, base + static_cast<size_t>(v) * 8, t);
+      }
+    }
+  }
+}
+
+// dx of a row and the lanes' sums of dy * n over the workgroup's rows, one
+// row of `part` per workgroup.  Rows go to the workgroups by a rule on the
+// sizes alone and the sums are joined in a fixed order, so dw is the same in
+// every run.
+template <bool H_BF16, bool DY_BF16, int WPR, int NV>
+__global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_bwd_kernel(
+    int64_t n_rows, int hidden, const void* __restrict__ h, const float* __restrict__ w, float eps,
+    const void* __restrict__ dy, const float* dh, float* dx, float* __restrict__ part) {
+  constexpr int kRows = waves_of(WPR) / WPR;
+  __shared__ float red[2][16][2];
+  __shared__ float join[WPR == 1 ? 4 * 512 : 1];
+  const int lane = threadIdx.x & 63;
+  const int wave = (threadIdx.x >> 6) % WPR;
+  const int nvec = hidden >> 3;
+  const float rcp = 1.0f / static_cast<float>(hidden);
+  float wv[NV][8], dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = (i * WPR + wave) * 64 + lane;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wv[i][e] = dw[i][e] = 0.f;
+    if (v < nvec) load_n<false, 8>(w, static_cast<size_t>(v) * 8, wv[i]);
+  }
+  int parity = 0;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + (WPR == 1 ? threadIdx.x >> 6 : 0); r < n_rows;
+       r += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
+    const size_t base = static_cast<size_t>(r) * hidden;
+    float hv[NV][8], gv[NV][8];
+    float s[2] = {0.f, 0.f};   // sum h^2, sum g h
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = (i * WPR + wave) * 64 + lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) hv[i][e] = gv[i][e] = 0.f;
+      if (v < nvec) {
+        load_n<H_BF16, 8>(h, base + static_cast<size_t>(v) * 8, hv[i]);
+        load_n<DY_BF16, 8>(dy, base + static_cast<size_t>(v) * 8, gv[i]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[0] = fmaf(hv[i][e], hv[i][e], s[0]);
+        s[1] = fmaf(gv[i][e] * wv[i][e], hv[i][e], s[1]);
+      }
+    }
+    row_sums<WPR, 2>(s, red, wave, parity);
+    const float inv = 1.0f / sqrtf(s[0] * rcp + eps);
+    const float c = s[1] * rcp * inv * inv;   // n * mean(g n) = h * c
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = (i * WPR + wave) * 64 + lane;
+      if (v < nvec) {
+        float t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[i][e] = fmaf(gv[i][e], hv[i][e] * inv, dw[i][e]);
+          t[e] = inv * fmaf(-hv[i][e], c, gv[i][e] * wv[i][e]);
+        }
+        if (dh) {
+          float d[8];
+          load_n<false, 8>(dh, base + static_cast<size_t>(v) * 8, d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] += d[e];
+        }
+        store_n<false, 8>(dx, base + static_cast<size_t>(v) * 8, t);
+      }
+    }
+  }
+  if constexpr (WPR == 1) {   // the four waves' rows joined
+    float* mine = join + (threadIdx.x >> 6) * 512 + lane * 8;
+    store_n<false, 8>(mine, 0, dw[0]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < hidden; c += 256)
+      part[static_cast<size_t>(blockIdx.x) * hidden + c] = (join[c] + join[512 + c]) + (join[1024 + c] + join[1536 + c]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = (i * WPR + wave) * 64 + lane;
+      if (v < nvec) store_n<false, 8>(part, static_cast<size_t>(blockIdx.x) * hidden + static_cast<size_t>(v) * 8, dw[i]);
+    }
+  }
+}
+
+// out[c] = sum over p of part[p][c]: 64 columns a workgroup, 16 waves over the
+// partial rows.
+__global__ __launch_bounds__(1024) void column_sums_kernel(int parts, int cols, const float* __restrict__ part,
+                                                           float* __restrict__ out) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < cols)
+    for (int p = wave; p < parts; p += 16) s += part[static_cast<size_t>(p) * cols + c];
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += red[i][lane];
+    out[c] = t;
+  }
+}
+
+hipError_t launch_column_sums(int parts, int cols, const float* part, float* out, hipStream_t st) {
+  column_sums_kernel<<<dim3((cols + 63) / 64), 1024, 0, st>>>(parts, cols, part, out);
+  return hipGetLastError();
+}
+
+// Calls f with the waves per row and the steps of 64 x 8 channels per wave
+// that hold a row of `hidden` channels in registers.
+template <class F>
+static hipError_t with_row_shape(int hidden, F&& f) {
+  using std::integral_constant;
+  if (hidden <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  if (hidden <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  if (hidden <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  if (hidden <= 8192) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (hidden <= 16384) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+}
+
+hipError_t launch_add_rmsnorm(int64_t n, int hidden, const void* x, const void* res, const float* w, float eps,
+                              void* h, void* y, float* scale, bool io_bf16, bool out_bf16, hipStream_t st) {
+  return with_row_shape(hidden, [&](auto wpr, auto nv) {
+    constexpr int WPR = decltype(wpr)::value, NV = decltype(nv)::value;
+    constexpr int kRows = waves_of(WPR) / WPR;
+    const int64_t blocks = (n + kRows - 1) / kRows;
+    const dim3 grid(static_cast<unsigned>(blocks < 65536 ? blocks : 65536));
+    const dim3 block(64 * waves_of(WPR));
+    auto go = [&](auto bf, auto out) {
+      add_rmsnorm_kernel<decltype(bf)::value, decltype(out)::value, WPR, NV>
+          <<<grid, block, 0, st>>>(n, hidden, x, res, w, eps, h, y, scale);
+    };
+    auto by_out = [&](auto bf) {
+      if (scale) go(bf, std::integral_constant<Out, Out::kFp8>{});
+      else if (out_bf16) go(bf, std::integral_constant<Out, Out::kBf16>{});
+      else go(bf, std::integral_constant<Out, Out::kFp32>{});
+    };
+    if (io_bf16) by_out(std::true_type{});
+    else by_out(std::false_type{});
+    return hipGetLastError();
+  });
+}
+
+// Workgroups of the backward, each with a row of partial sums.
+int add_rmsnorm_bwd_parts(int64_t n) { return static_cast<int>(n < 1024 ? n : 1024); }
+
+hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const float* w, float eps, const void* dy,
+                                  const float* dh, float* dx, float* dw, float* part, bool h_bf16, bool dy_bf16,
+                                  hipStream_t st) {
+  const int parts = add_rmsnorm_bwd_parts(n);
+  if (parts > 0) {
+    const hipError_t e = with_row_shape(hidden, [&](auto wpr, auto nv) {
+      constexpr int WPR = decltype(wpr)::value, NV = decltype(nv)::value;
+      auto go = [&](auto hb, auto db) {
+        add_rmsnorm_bwd_kernel<decltype(hb)::value, decltype(db)::value, WPR, NV>
+            <<<dim3(parts), dim3(64 * waves_of(WPR)), 0, st>>>(n, hidden, h, w, eps, dy, dh, dx, part);
+      };
+      if (h_bf16 && dy_bf16) go(std::true_type{}, std::true_type{});
+      else if (h_bf16) go(std::true_type{}, std::false_type{});
+      else if (dy_bf16) go(std::false_type{}, std::true_type{});
+      else go(std::false_type{}, std::false_type{});
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  return launch_column_sums(parts, hidden, part, dw, st);
+}
+
+}  // namespace kda

@@ -30,8 +30,12 @@
  * kda_decode_multi (K tokens per sequence through state / conv-history pools,
  * with commit counts for speculative decoding); kda_decode_step_gated and
  * kda_decode_multi_gated (the same with the output epilogue fused);
- * kda_output_gate (the layer's o_norm x sigmoid output epilogue); plus the
- * workspace queries, the version and status strings.
+ * kda_output_gate (the layer's o_norm x sigmoid output epilogue).  Around the
+ * core: kda_add_rmsnorm (the residual's addition and the norm in front of the
+ * layer), kda_fp8_matmul (its projections, e4m3 operands with block scales),
+ * kda_add_rmsnorm_fp8 and kda_output_gate_fp8 (the producers of such operands),
+ * kda_add_rmsnorm_backward and kda_output_gate_backward.  Plus the workspace
+ * queries, the version and status strings.
  *
  * Conventions for every entry point:
  *  - All tensor pointers are DEVICE pointers, contiguous, row-major in the
@@ -93,7 +97,9 @@ typedef enum kda_stage {
     KDA_STAGE_DECODE = 4,       /* the decode step kernel (also kda_decode_multi)             */
     KDA_STAGE_OUTPUT_GATE = 5,  /* the o_norm + sigmoid output-gate epilogue                  */
     KDA_STAGE_BACKWARD = 6,     /* the backward pass's kernels (after its chunk table)        */
-    KDA_NUM_STAGES = 7
+    KDA_STAGE_NORM = 7,         /* the residual's addition and the RMS norm                   */
+    KDA_STAGE_MATMUL = 8,       /* the block-scaled e4m3 product                              */
+    KDA_NUM_STAGES = 9
 } kda_stage_t;
 
 typedef struct kda_config {
@@ -380,6 +386,135 @@ kda_status_t kda_output_gate(const kda_config_t *cfg, int64_t n_tokens,
                              const void *o, const void *gate,
                              const float *o_norm_weight, float eps,
                              void *y, void *stream);
+
+/*
+ * ---- The operators around the core ---------------------------------------
+ *
+ * A KDA layer adds its input to the residual stream, normalises it, projects
+ * it to q, k, v, alpha, b and the output gate, runs the core and the output
+ * epilogue, and projects back.  The entry points below are those steps, in
+ * bf16 / fp32 or with 8-bit matrix operands:
+ *
+ *   e4m3 rows: K values of 1 byte (OCP e4m3: 3 mantissa bits, at most 448, no
+ *   infinity) with one fp32 scale for every 128 consecutive values, the last
+ *   block of a row being short when 128 does not divide K:  KB = ceil(K / 128),
+ *   value k of a row stands for q[k] * scale[k / 128].  A row is written from
+ *   fp32 values v as  scale = max(max|v| over the block, 1e-30) / 448,
+ *   q = v / scale rounded to nearest even.  A NaN or an infinity in a block
+ *   makes its scale NaN or infinite.
+ *
+ * Pointers are 16-byte aligned as everywhere (e4m3 outputs 8-byte, scales
+ * 4-byte); one that is not is KDA_ERR_INVALID_ARGUMENT here.
+ */
+
+/*
+ * The norm in front of a layer, with the residual's addition:
+ *   h[t] = x[t] + residual[t], rounded to io_dtype
+ *   y[t][j] = h[t][j] / sqrt(mean_j' h[t][j']^2 + eps) * weight[j]
+ *   x, residual    [n_tokens][hidden] io_dtype; residual NULL: h = x
+ *   weight         [hidden] fp32
+ *   eps            >= 0 (NaN or negative: KDA_ERR_INVALID_ARGUMENT); with 0 a
+ *                  row of zeros gives NaN
+ *   h              [n_tokens][hidden] io_dtype, or NULL if not wanted; may
+ *                  alias x or residual (in place)
+ *   y              [n_tokens][hidden] out_dtype; with h NULL it may alias x
+ *                  when both have the same type
+ *   hidden         a multiple of 8, 8 .. 32768 (else KDA_ERR_UNSUPPORTED)
+ * No other aliasing.  Only io_dtype, out_dtype and stage_events of cfg are
+ * used.  Needs no workspace.  n_tokens == 0 is a no-op.
+ */
+kda_status_t kda_add_rmsnorm(const kda_config_t *cfg, int64_t n_tokens, int32_t hidden,
+                             const void *x, const void *residual, const float *weight, float eps,
+                             void *h, void *y, void *stream);
+
+/*
+ * The same with y as e4m3 rows: y [n_tokens][hidden] e4m3, y_scale
+ * [n_tokens][ceil(hidden / 128)] fp32.  y aliases nothing; out_dtype of cfg
+ * is not used, but has to be a known type.
+ */
+kda_status_t kda_add_rmsnorm_fp8(const kda_config_t *cfg, int64_t n_tokens, int32_t hidden,
+                                 const void *x, const void *residual, const float *weight, float eps,
+                                 void *h, void *y, float *y_scale, void *stream);
+
+/*
+ * Gradient of kda_add_rmsnorm (of kda_add_rmsnorm_fp8 with the rounding taken
+ * as the identity).  With n = h / sqrt(mean h^2 + eps) and g = dy * weight:
+ *   dx = (g - n * mean(g * n)) / sqrt(mean h^2 + eps) + d_h
+ *   dweight[j] = sum over tokens of dy * n
+ *   h              [n_tokens][hidden] io_dtype, as the forward wrote it
+ *   dy             [n_tokens][hidden] out_dtype: dLoss/dy
+ *   d_h            [n_tokens][hidden] fp32: the gradient that reaches h by the
+ *                  residual stream, or NULL (zero)
+ *   dx             [n_tokens][hidden] fp32: the gradient of x, and of residual
+ *                  alike; may alias d_h
+ *   dweight        [hidden] fp32; zeros when n_tokens == 0
+ *   workspace      kda_add_rmsnorm_backward_workspace_bytes(); calls that
+ *                  overlap in time need one each
+ * The same inputs give the same bits on every run.
+ */
+size_t kda_add_rmsnorm_backward_workspace_bytes(const kda_config_t *cfg, int64_t n_tokens, int32_t hidden);
+
+kda_status_t kda_add_rmsnorm_backward(const kda_config_t *cfg, int64_t n_tokens, int32_t hidden,
+                                      const void *h, const float *weight, float eps,
+                                      const void *dy, const float *d_h,
+                                      float *dx, float *dweight,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_output_gate with its output as e4m3 rows, the operand of the projection
+ * that follows: a token's heads are one row of num_heads * head_v_dim values.
+ *   y              [n_tokens][H * dv] e4m3
+ *   y_scale        [n_tokens][ceil(H * dv / 128)] fp32
+ * The other arguments as for kda_output_gate; nothing aliases.
+ */
+kda_status_t kda_output_gate_fp8(const kda_config_t *cfg, int64_t n_tokens,
+                                 const void *o, const void *gate,
+                                 const float *o_norm_weight, float eps,
+                                 void *y, float *y_scale, void *stream);
+
+/*
+ * Gradient of kda_output_gate (of kda_output_gate_fp8 with the rounding taken
+ * as the identity).  Per (token, head) row, with n = o / sqrt(mean o^2 + eps),
+ * s = sigmoid(gate) and g = dy * o_norm_weight * s:
+ *   d_o = (g - n * mean(g * n)) / sqrt(mean o^2 + eps)
+ *   d_gate = dy * o_norm_weight * n * s * (1 - s)
+ *   d_weight[j] = sum over tokens and heads of dy * n * s
+ *   o              [n_tokens][H][dv] out_dtype; gate [n_tokens][H][dv] io_dtype
+ *   dy             [n_tokens][H][dv] out_dtype: dLoss/dy
+ *   d_o            [n_tokens][H][dv] out_dtype, as kda_varlen_backward takes it
+ *   d_gate         [n_tokens][H][dv] fp32, as the other input gradients
+ *   d_weight       [dv] fp32; zeros when n_tokens == 0
+ *   workspace      kda_output_gate_backward_workspace_bytes(); calls that
+ *                  overlap in time need one each
+ * Nothing aliases.  The same inputs give the same bits on every run.
+ */
+size_t kda_output_gate_backward_workspace_bytes(const kda_config_t *cfg, int64_t n_tokens);
+
+kda_status_t kda_output_gate_backward(const kda_config_t *cfg, int64_t n_tokens,
+                                      const void *o, const void *gate,
+                                      const float *o_norm_weight, float eps, const void *dy,
+                                      void *d_o, float *d_gate, float *d_weight,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A projection with 8-bit operands:
+ *   y[m][n] = sum over b of a_scale[m][b] * w_scale[n / 128][b]
+ *                           * sum over k in block b of a[m][k] * w[n][k]
+ * accumulated in fp32 and rounded once to out_dtype.
+ *   a              [M][K] e4m3 rows, a_scale [M][KB] fp32, KB = ceil(K / 128)
+ *   w              [N][K] e4m3 (row n holds the weights of output n)
+ *   w_scale        [ceil(N / 128)][KB] fp32, one scale per 128 x 128 block
+ *   y              [M][N] out_dtype
+ * K is a multiple of 16; K, N up to 2^20, M below 2^31 (else
+ * KDA_ERR_UNSUPPORTED).  M == 0 is a no-op; M == 1 is the single-token form.
+ * A NaN scale or value reaches the outputs of its row (of its 128 columns for
+ * a w_scale).  Only out_dtype and stage_events of cfg are used.  Needs no
+ * workspace.  The same inputs give the same bits on every run.
+ */
+kda_status_t kda_fp8_matmul(const kda_config_t *cfg, int64_t M, int32_t N, int32_t K,
+                            const void *a, const float *a_scale,
+                            const void *w, const float *w_scale,
+                            void *y, void *stream);
 
 #ifdef __cplusplus
 }
