@@ -75,6 +75,23 @@ __device__ __forceinline__ void store_out(void* y, size_t row, int n, int N, con
   }
 }
 
+// Eight consecutive outputs n .. n + 7 of one token, those below N.
+template <bool BF16>
+__device__ __forceinline__ void store_out8(void* y, size_t row, int n, int N, const f32x4& u, const f32x4& v) {
+  if ((N & 7) == 0) {
+    if (n < N) {
+      const float t[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+      store_n<BF16, 8>(y, row + n, t);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n + i < N) st<BF16>(y, row + n + i, u[i]);
+      if (n + 4 + i < N) st<BF16>(y, row + n + 4 + i, v[i]);
+    }
+  }
+}
+
 }  // namespace
 
 // 16 outputs x 16 T tokens a workgroup; its waves share the scale blocks and
@@ -127,19 +144,33 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
   }
 }
 
-// The kernel for many tokens: a TN x TT tile of outputs x tokens per
-// workgroup, WN x WT waves.  Each scale block (128 channels) of the tile's
-// rows goes to LDS straight from memory, 16 bytes a lane, one block ahead of
-// the products in the other of two buffers, so one barrier per block is
-// enough.  A row's eight 16-byte pieces are stored in the order piece ^ (row
-// % 8), which spreads the 16 rows that a product's operand read touches over
-// all banks; the loads read the same 128-byte lines either way.
+// The kernel for many tokens: TN x TT tiles of outputs x tokens, one after
+// the other in each workgroup (one per CU), WN x WT waves.  Each scale block
+// (128 channels) of the tile's rows goes to LDS straight from memory, 16 bytes
+// a lane, one block ahead of the products in the other of two buffers, also
+// from a tile's last block to the next one's first; one barrier per block
+// hands over the buffers.
+//
+// A row's eight 16-byte pieces are stored in the order piece ^ key, with a key
+// of 0 .. 7 from the row's index, which spreads the 16 rows that a product's
+// operand read touches over all banks; the loads read the same 128-byte lines
+// either way.
 //
 // The loads are written in assembly (they have no register output): the
 // compiler's own form of them makes every later LDS read wait for all of
-// them.  Their order against the LDS reads is the barrier below.
-__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t voff, const uint8_t* base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+// them.  Their order against the LDS reads is the barrier below.  m0 is
+// reserved: the compiler keeps nothing in it.  The first form loads where
+// k < end; its branch is inside the assembly so that the products around it
+// stay one block of code, whose registers the compiler can place (with a
+// branch of its own it spills).
+__device__ __forceinline__ void load_lds16_if(int k, int end, uint32_t lds, uint32_t voff, const uint8_t* base) {
+  asm volatile(
+      "s_cmp_ge_i32 %0, %1\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %3, %4\n.Lskip%=:" ::"s"(k),
+      "s"(end), "s"(lds), "v"(voff), "s"(base)
+      : "memory", "scc");
+}
+__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, const void* base) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
 }
 
 // Every load of this wave has landed and its LDS reads are done; then every
@@ -148,16 +179,45 @@ __device__ __forceinline__ void wait_all_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+constexpr int kSteps = 8;   // scale blocks whose scales are loaded together
+
+// LDS of a tile: two buffers of operand rows, of token scales and of weight scales.
+constexpr int tile_lds(int TN, int TT) { return 2 * ((TN + TT) * kScaleBlock + TT * kSteps * 4 + 256); }
+
+// The order of the tiles: workgroups go to the 8 XCDs in turn, so each XCD
+// takes a run of neighbouring tiles, and within it groups of kGroup token
+// tiles wide, so that the tiles running at a time share rows in its L2
+// (8192 x 8192 x 8192: 447 us, 526 us row by row).
+constexpr int kGroup = 4;
+struct TileOrder {
+  int n_tiles, t_tiles, per, turn;   // per: tiles of an XCD, 0 where they are too few to split; turn: workgroups
+  __device__ int count(int wg) const {
+    if (!per) return (n_tiles * t_tiles - wg + turn - 1) / turn;
+    const int left = min(per, n_tiles * t_tiles - (wg & 7) * per) - (wg >> 3);
+    return left <= 0 ? 0 : (left + (turn >> 3) - 1) / (turn >> 3);
+  }
+  __device__ int2 at(int wg, int i) const {   // (output tile, token tile)
+    const int id = per ? (wg & 7) * per + (wg >> 3) + i * (turn >> 3) : wg + i * turn;
+    const int g = id / (kGroup * n_tiles), r = id - g * (kGroup * n_tiles);
+    const int wide = min(kGroup, t_tiles - g * kGroup);
+    return make_int2(r / wide, g * kGroup + r % wide);
+  }
+};
+
 template <int TN, int TT, int WN, int WT, bool OUT_BF16>
 __global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
-    int64_t M, int N, int K, int n_tiles, int64_t tiles, const uint8_t* __restrict__ a, const float* __restrict__ sa,
+    int64_t M, int N, int K, TileOrder order, const uint8_t* __restrict__ a, const float* __restrict__ sa,
     const uint8_t* __restrict__ w, const float* __restrict__ sw, void* __restrict__ y) {
   constexpr int kWaves = WN * WT;
   constexpr int NT = TN / WN / 16, TTW = TT / WT / 16;    // 16 x 16 results of a wave
   constexpr int kRows = TN + TT;
   constexpr int kLoads = kRows / 8 / kWaves;              // 8 rows of 128 bytes a load
+  constexpr int kWLoads = TN / 8 / kWaves;                // those of the weight
   constexpr int kBuf = kRows * kScaleBlock;
-  static_assert(kRows % (8 * kWaves) == 0 && TN / WN <= kScaleBlock && kScaleBlock % (TN / WN) == 0, "tile shape");
+  constexpr int kScaleLoads = TT * kSteps / 64 / kWaves;
+  constexpr int kScaleBuf = TT * kSteps * 4;
+  static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0 && kWaves % 2 == 0, "whole loads");
+  static_assert(TN / WN <= kScaleBlock && kScaleBlock % (TN / WN) == 0 && TN / kScaleBlock <= 64 / kSteps, "scales");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const uint32_t smem0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)smem));
 
@@ -167,52 +227,82 @@ __global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
   const int wn = wave / WT, wt = wave % WT;
   const int KB = (K + kScaleBlock - 1) / kScaleBlock;
 
-  // workgroups go to the 8 XCDs in turn: each XCD takes a run of neighbouring tiles
-  int64_t id = blockIdx.x;
-  {
-    const int64_t per = tiles / 8;
-    if (id < per * 8) id = (id & 7) * per + (id >> 3);
-  }
-  const int tn = static_cast<int>(id % n_tiles);
-  const int64_t tt = id / n_tiles;
-  const int n0 = tn * TN;
-  const int64_t m0 = tt * TT;
-
-  const uint8_t* wbase = w + static_cast<size_t>(n0) * K;
-  const uint8_t* abase = a + static_cast<size_t>(m0) * K;
-  const int nlast = min(TN, N - n0) - 1;
-  const int mlast = static_cast<int>(M - m0 < TT ? M - m0 : TT) - 1;
-
-  // this lane's piece of each load: row 8 i + lane / 8, piece (lane % 8) ^ (row % 8)
-  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;
+  // The tile whose blocks are being loaded.
+  const uint8_t* wbase;
+  const uint8_t* abase;
+  const float* sabase;
+  const float* swbase;
+  int mlast, wrows;
   uint32_t voff[kLoads];
+  // This lane's piece of each load, of row 8 q + lane / 8: the weight's rows
+  // have key (row % 4) + 4 (row / 8 % 2), the tokens' row % 8.
+  const int piece_w = ((lane & 7) ^ (((lane >> 3) & 3) + 4 * (wave & 1))) * 16;
+  const int piece_a = ((lane & 7) ^ (lane >> 3)) * 16;
+  auto set_tile = [&](int2 t) {
+    const int n0 = t.x * TN;
+    const int64_t m0 = static_cast<int64_t>(t.y) * TT;
+    wbase = w + static_cast<size_t>(n0) * K;
+    abase = a + static_cast<size_t>(m0) * K;
+    sabase = sa + static_cast<size_t>(m0) * KB;
+    const int wrow0 = n0 / kScaleBlock;
+    swbase = sw + static_cast<size_t>(wrow0) * KB;
+    wrows = (N - 1) / kScaleBlock - wrow0;
+    const int nlast = min(TN, N - n0) - 1;
+    mlast = static_cast<int>(M - m0 < TT ? M - m0 : TT) - 1;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int row = (i * kWaves + wave) * 8 + (lane >> 3);   // a load is within one operand: TN is a multiple of 8
-    voff[i] = (row < TN ? min(row, nlast) : min(row - TN, mlast)) * static_cast<uint32_t>(K) + piece;
-  }
-  auto issue = [&](int kb, int buf) {
-    const bool past = kb * kScaleBlock + piece >= K;   // beyond a short last block: any byte of the row, masked later
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r0 = (i * kWaves + wave) * 8;
-      const uint8_t* base = (r0 < TN ? wbase : abase) + kb * kScaleBlock;
-      load_lds16(smem0 + buf * kBuf + r0 * kScaleBlock, past ? voff[i] - piece : voff[i], base);
+    for (int i = 0; i < kLoads; ++i) {   // rows past the tile's last are that row again
+      const int row = (i * kWaves + wave) * 8 + (lane >> 3);
+      voff[i] = i < kWLoads ? min(row, nlast) * static_cast<uint32_t>(K) + piece_w
+                            : min(row - TN, mlast) * static_cast<uint32_t>(K) + piece_a;
     }
   };
+  // Loads from .. to - 1 of block kb, if there is one, to a buffer.
+  auto issue = [&](int kb, int end, int buf, int from, int to) {
+    const uint32_t dst = smem0 + buf;
+    // beyond a short last block: any byte of the row, masked later
+    const uint32_t back_w = kb * kScaleBlock + piece_w >= K ? piece_w : 0;
+    const uint32_t back_a = kb * kScaleBlock + piece_a >= K ? piece_a : 0;
+#pragma unroll
+    for (int i = from; i < to; ++i)
+      load_lds16_if(kb, end, dst + (i * kWaves + wave) * 8 * kScaleBlock, voff[i] - (i < kWLoads ? back_w : back_a),
+                    (i < kWLoads ? wbase : abase) + kb * kScaleBlock);
+  };
+  // The scales go to LDS for kSteps blocks at a time, [token][block]: a
+  // token's scales are one run of memory, so a load of 8 tokens touches 8
+  // lines where a load per block would touch one for each token.
+  auto issue_scales = [&](int chunk, int half) {
+    const int kb = min(chunk * kSteps + lane % kSteps, KB - 1);
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) {
+      const int r0 = (i * kWaves + wave) * (64 / kSteps);
+      load_lds4(smem0 + 2 * kBuf + half * kScaleBuf + r0 * (kSteps * 4), (min(r0 + lane / kSteps, mlast) * KB + kb) * 4u,
+                sabase);
+    }
+    if (wave == 0)
+      load_lds4(smem0 + 2 * kBuf + 2 * kScaleBuf + half * 256, (min(lane / kSteps, wrows) * KB + kb) * 4u, swbase);
+  };
 
-  // operand reads: rows l16 of a 16-row group, pieces grp and grp + 4 of the block
-  const int rd0 = l16 * kScaleBlock + ((grp ^ (l16 & 7)) * 16);
-  const int rd1 = l16 * kScaleBlock + (((grp + 4) ^ (l16 & 7)) * 16);
-  auto frag = [&](const uint8_t* rows) {
-    const uint4 lo = *reinterpret_cast<const uint4*>(rows + rd0);
-    const uint4 hi = *reinterpret_cast<const uint4*>(rows + rd1);
+  // Operand reads: 16 rows, pieces grp and grp + 4 of the block.  Two groups
+  // of the weight's rows take turns of four in 32 rows, so that a lane's
+  // results of both are eight neighbouring outputs.
+  const int off0 = (grp ^ (l16 & 7)) * 16, off1 = ((grp + 4) ^ (l16 & 7)) * 16;
+  auto frag = [&](const uint8_t* row) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(row + off0);
+    const uint4 hi = *reinterpret_cast<const uint4*>(row + off1);
     return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
                  static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
   };
+  const int nw = wn * (TN / WN);   // the wave's outputs lie in one scale block
+  const uint8_t* wr = smem + (nw + 8 * (l16 >> 2) + (l16 & 3)) * kScaleBlock;
+  const uint8_t* ar = smem + (TN + wt * (TT / WT) + l16) * kScaleBlock;
+  auto frag_w = [&](int buf, int j) { return frag(wr + buf + (32 * (j >> 1) + 4 * (j & 1)) * kScaleBlock); };
+  auto frag_a = [&](int buf, int t) { return frag(ar + buf + 16 * t * kScaleBlock); };
+  const float* sal = reinterpret_cast<const float*>(smem + 2 * kBuf) + (wt * (TT / WT) + l16) * kSteps;
+  const float* swl = reinterpret_cast<const float*>(smem + 2 * kBuf + 2 * kScaleBuf) + nw / kScaleBlock * kSteps;
   // pieces past K of the last block hold other channels: zeros on both sides
-  auto masked = [&](i32x8 f, int kb) {
-    const bool k0 = kb * kScaleBlock + grp * 16 < K, k1 = kb * kScaleBlock + (grp + 4) * 16 < K;
+  auto masked = [&](i32x8 f) {
+    const int left = K - (KB - 1) * kScaleBlock;
+    const bool k0 = grp * 16 < left, k1 = (grp + 4) * 16 < left;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[i] = k0 ? f[i] : 0;
@@ -221,70 +311,116 @@ __global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
     return f;
   };
 
-  const float* sap[TTW];
-  float sa_next[TTW];
+  // One turn of the loop: the products of the last row group of block kb - 1,
+  // then those of all but the last of block kb.  Each group's rows are read a
+  // group ahead, and block kb's first operands during that leftover group, in
+  // the registers that it has done with, so the matrix cores do not wait for
+  // LDS at the start of a block.  At the top every wave has read all rows of
+  // block kb - 1, whose buffer the loads of the next block take, and the loads
+  // of block kb have landed.  (A tile's first turn has a leftover of zeros.)
+  //
+  // A product's scaled addition follows three products later, so neither
+  // waits for the other; the last three of a turn fall into the next one.  The
+  // fences keep this order: left alone, the compiler puts each addition right
+  // behind its product.
+  constexpr int kLag = 3, kUnits = NT * TTW;
+  constexpr int kEvery = 1, kBatch = 1;   // loads are issued kBatch at every kEvery products
+  static_assert(NT % 2 == 0 && kUnits % (kLag + 1) == 0 && kLag <= TTW, "register slots repeat from turn to turn");
+  i32x8 wf[2], af[TTW];
+  f32x4 acc[NT][TTW], p[kLag + 1];
+  float s[TTW], s_old[TTW];
+  auto add = [&](int q, const float (&by)[TTW]) {   // product q of a block
 #pragma unroll
-  for (int t = 0; t < TTW; ++t) {
-    const int m = min(wt * (TT / WT) + 16 * t + l16, mlast);
-    sap[t] = sa + static_cast<size_t>(m0 + m) * KB;
-    sa_next[t] = sap[t][0];
-  }
-  const int nw = n0 + wn * (TN / WN);   // the wave's outputs lie in one scale block
-  const float* swp = sw + static_cast<size_t>(min(nw, N - 1) / kScaleBlock) * KB;
-
-  f32x4 acc[NT][TTW];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int t = 0; t < TTW; ++t) acc[j][t] = zero4();
-
-  auto step = [&](int kb, auto last_short) {
-    wait_all_barrier();
-    float s[TTW];
-    const float sb = swp[kb];
-#pragma unroll
-    for (int t = 0; t < TTW; ++t) {
-      s[t] = sa_next[t] * sb;
-      asm volatile("" : "+v"(s[t]));   // used up before the loads below are counted
-    }
-    if (kb + 1 < KB) {
-      issue(kb + 1, (kb + 1) & 1);
-#pragma unroll
-      for (int t = 0; t < TTW; ++t) sa_next[t] = sap[t][kb + 1];
-    }
-    const uint8_t* buf = smem + (kb & 1) * kBuf;
-    const uint8_t* wr = buf + wn * (TN / WN) * kScaleBlock;
-    const uint8_t* ar = buf + (TN + wt * (TT / WT)) * kScaleBlock;
-    i32x8 af[TTW];
-#pragma unroll
-    for (int t = 0; t < TTW; ++t) {
-      af[t] = frag(ar + t * 16 * kScaleBlock);
-      if constexpr (decltype(last_short)::value) af[t] = masked(af[t], kb);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      i32x8 wf = frag(wr + j * 16 * kScaleBlock);
-      if constexpr (decltype(last_short)::value) wf = masked(wf, kb);
-#pragma unroll
-      for (int t = 0; t < TTW; ++t) {
-        const f32x4 p = mfma_block<OUT_BF16>(wf, af[t]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][t][i] = fmaf(p[i], s[t], acc[j][t][i]);
-      }
-    }
+    for (int e = 0; e < 4; ++e)
+      acc[q / TTW][q % TTW][e] = fmaf(p[q % (kLag + 1)][e], by[q % TTW], acc[q / TTW][q % TTW][e]);
   };
-  issue(0, 0);
-  const int whole = K / kScaleBlock;
-  for (int kb = 0; kb < whole; ++kb) step(kb, std::false_type{});
-  if (whole < KB) step(whole, std::true_type{});
-
+  int buf = 0, half = 0;   // the block's buffer (byte offset) and its scales'
+  // next, end: the block to load meanwhile, of the tile set by set_tile, if next < end
+  auto turn = [&](int kb, int next, int end, auto is_short) {
+    constexpr bool kShort = decltype(is_short)::value;
+    wait_all_barrier();
+    if (next % kSteps == 0 && next < end) issue_scales(next / kSteps, half ^ 1);
+    const int at = half * (TT * kSteps) + kb % kSteps;
+    wf[0] = frag_w(buf, 0);
+    const float sb = swl[half * 64 + kb % kSteps];
 #pragma unroll
-  for (int t = 0; t < TTW; ++t) {
-    const int m = wt * (TT / WT) + 16 * t + l16;
-    if (m > mlast) continue;
+    for (int t = 0; t < TTW; ++t) s_old[t] = s[t];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int i = (u + kUnits - TTW) % kUnits, j = i / TTW, t = i % TTW;
+      if (u >= TTW && t == 0) {
+        if constexpr (kShort) wf[j & 1] = masked(wf[j & 1]);
+        wf[(j + 1) & 1] = frag_w(buf, j + 1);
+      }
+      if (kShort && u >= TTW && u < 2 * TTW) af[t] = masked(af[t]);
+      if (u % kEvery == 0 && u / kEvery * kBatch < kLoads)
+        issue(next, end, kBuf - buf, u / kEvery * kBatch, min(u / kEvery * kBatch + kBatch, kLoads));
+      __builtin_amdgcn_sched_barrier(0);
+      p[i % (kLag + 1)] = mfma_block<OUT_BF16>(wf[j & 1], af[t]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (u < TTW) {
+        af[t] = frag_a(buf, t);
+        s[t] = sal[at + 16 * t * kSteps] * sb;
+      }
+      const int q = (i + kUnits - kLag) % kUnits;
+      if (u < TTW + kLag) add(q, s_old);
+      else add(q, s);
+    }
+    buf = kBuf - buf;
+    if (next % kSteps == 0) half ^= 1;
+  };
+
+  const int count = order.count(blockIdx.x);
+  if (count <= 0) return;
+  int2 tile = order.at(blockIdx.x, 0);
+  set_tile(tile);
+  issue(0, 1, 0, 0, kLoads);
+  issue_scales(0, 0);
+  for (int it = 0; it < count; ++it) {
+    const int2 here = tile;
+    wf[1] = i32x8{};
+#pragma unroll
+    for (int t = 0; t < TTW; ++t) {
+      af[t] = i32x8{};
+      s[t] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i <= kLag; ++i) p[i] = zero4();
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      store_out<OUT_BF16>(y, static_cast<size_t>(m0 + m) * N, nw + 16 * j + 4 * grp, N, acc[j][t]);
+#pragma unroll
+      for (int t = 0; t < TTW; ++t) acc[j][t] = zero4();
+
+    const int whole = K / kScaleBlock;
+    const int more = it + 1 < count;   // another tile: its first block is loaded during this one's last
+    for (int kb = 0; kb < whole; ++kb) {
+      const bool last = kb + 1 == KB;
+      if (last && more) set_tile(tile = order.at(blockIdx.x, it + 1));
+      turn(kb, last ? 0 : kb + 1, last ? more : KB, std::false_type{});
+    }
+    if (whole < KB) {
+      if (more) set_tile(tile = order.at(blockIdx.x, it + 1));
+      turn(whole, 0, more, std::true_type{});
+      wf[1] = masked(wf[1]);
+    }
+#pragma unroll
+    for (int i = kUnits - TTW; i < kUnits; ++i) {
+      p[i % (kLag + 1)] = mfma_block<OUT_BF16>(wf[1], af[i % TTW]);
+      add(i - kLag, s);
+    }
+#pragma unroll
+    for (int i = kUnits - kLag; i < kUnits; ++i) add(i, s);
+
+    const int n0 = here.x * TN + nw + 8 * grp;
+#pragma unroll
+    for (int t = 0; t < TTW; ++t) {
+      const int64_t m = static_cast<int64_t>(here.y) * TT + wt * (TT / WT) + 16 * t + l16;
+      if (m < M) {
+#pragma unroll
+        for (int j = 0; j < NT; j += 2)
+          store_out8<OUT_BF16>(y, static_cast<size_t>(m) * N, n0 + 16 * j, N, acc[j][t], acc[j + 1][t]);
+      }
+    }
   }
 }
 
@@ -292,20 +428,27 @@ template <int TN, int TT, int WN, int WT, bool OUT_BF16>
 static hipError_t launch_tiles(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                                const float* sw, void* y, hipStream_t st) {
   const auto kernel = fp8_matmul_tile_kernel<TN, TT, WN, WT, OUT_BF16>;
-  constexpr int kLds = 2 * (TN + TT) * kScaleBlock;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  constexpr int kLds = tile_lds(TN, TT);
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                     kLds);
+  int ncu = 0;
+  if (e == hipSuccess) e = device_cus(&ncu);
   if (e != hipSuccess) return e;
-  const int n_tiles = (N + TN - 1) / TN;
-  const int64_t tiles = n_tiles * ((M + TT - 1) / TT);
-  kernel<<<dim3(static_cast<unsigned>(tiles)), 64 * WN * WT, kLds, st>>>(M, N, K, n_tiles, tiles, a, sa, w, sw, y);
+  TileOrder order;
+  order.n_tiles = (N + TN - 1) / TN;
+  order.t_tiles = static_cast<int>((M + TT - 1) / TT);
+  const int64_t tiles = static_cast<int64_t>(order.n_tiles) * order.t_tiles;
+  if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
+  order.turn = static_cast<int>(tiles < ncu ? tiles : ncu);
+  order.per = order.turn % 8 == 0 ? static_cast<int>((tiles + 7) / 8) : 0;
+  kernel<<<dim3(order.turn), 64 * WN * WT, kLds, st>>>(M, N, K, order, a, sa, w, sw, y);
   return hipGetLastError();
 }
 
 template <bool OUT_BF16>
 static hipError_t launch_fp8_matmul_to(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                                        const float* sw, void* y, hipStream_t st) {
-  if (M > 64) return launch_tiles<256, 256, 2, 4, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+  if (M > 64) return launch_tiles<OUT_BF16 ? 256 : 128, 256, 2, 4, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
   const dim3 grid(static_cast<unsigned>((M + 63) / 64), (N + 15) / 16);
   fp8_matmul_rows_kernel<4, 8, OUT_BF16><<<grid, 512, 0, st>>>(M, N, K, a, sa, w, sw, y);
   return hipGetLastError();
