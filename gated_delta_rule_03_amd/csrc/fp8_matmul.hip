@@ -11,6 +11,8 @@
 // 32 * (l / 16) .. + 31; both sides use the same order of channels, so any
 // other assignment of channels to lanes gives the same product.  Result: lane
 // l holds D[4 * (l / 16) + i][l % 16], i < 4.
+#include <algorithm>
+
 #include "kda_device.h"
 #include "kda_internal.h"
 #include "vec_io.h"
@@ -50,16 +52,6 @@ __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
   }
 }
 
-// 32 channels of a row from channel k on, zeros past its end (rows are whole
-// runs of 16).
-__device__ __forceinline__ i32x8 load_frag(const uint8_t* row, int k, int K) {
-  const uint4 z = make_uint4(0, 0, 0, 0);
-  const uint4 lo = k < K ? *reinterpret_cast<const uint4*>(row + k) : z;
-  const uint4 hi = k + 16 < K ? *reinterpret_cast<const uint4*>(row + k + 16) : z;
-  return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
-               static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
-}
-
 // Four consecutive outputs n .. n + 3 of one token, those below N.
 template <bool BF16>
 __device__ __forceinline__ void store_out(void* y, size_t row, int n, int N, const f32x4& v) {
@@ -94,53 +86,101 @@ __device__ __forceinline__ void store_out8(void* y, size_t row, int n, int N, co
 
 }  // namespace
 
-// 16 outputs x 16 T tokens a workgroup; its waves share the scale blocks and
-// join their sums in LDS in a fixed order.
-template <int T, int WAVES, bool OUT_BF16>
+// The kernel for few tokens: 16 J outputs x 16 T tokens a workgroup, the
+// operands straight from memory to registers.  Its waves share the scale
+// blocks, each with U blocks' loads in flight, and join their sums in LDS in
+// a fixed order.
+template <int J, int T, int WAVES, int U, bool OUT_BF16>
 __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
     int64_t M, int N, int K, const uint8_t* __restrict__ a, const float* __restrict__ sa,
     const uint8_t* __restrict__ w, const float* __restrict__ sw, void* __restrict__ y) {
-  __shared__ float4 red[WAVES][T][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float4 red[WAVES][J * T][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, kq = (lane >> 4) * 32;
   const int KB = (K + kScaleBlock - 1) / kScaleBlock;
-  const int n0 = blockIdx.y * 16;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * (16 * T);
-  const uint8_t* wrow = w + static_cast<size_t>(min(n0 + l16, N - 1)) * K;
+  const int n0 = blockIdx.x * (16 * J);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * T);
+  const uint8_t* wrow[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) wrow[j] = w + static_cast<size_t>(min(n0 + 16 * j + l16, N - 1)) * K;
   const float* swrow = sw + static_cast<size_t>(n0 / kScaleBlock) * KB;
-  int64_t tok[T];
-  f32x4 acc[T];
+  const uint8_t* arow[T];
+  const float* sarow[T];
+  f32x4 acc[J][T];
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    const int64_t m = m0 + 16 * t + l16;
-    tok[t] = m < M ? m : M - 1;
-    acc[t] = zero4();
+    const int64_t m = m0 + 16 * t + l16 < M ? m0 + 16 * t + l16 : M - 1;
+    arow[t] = a + static_cast<size_t>(m) * K;
+    sarow[t] = sa + static_cast<size_t>(m) * KB;
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[j][t] = zero4();
   }
-  for (int b = wave; b < KB; b += WAVES) {
-    const int k = b * kScaleBlock + kq;
-    const i32x8 wf = load_frag(wrow, k, K);
-    const float s = swrow[b];
+  // 32 channels from k on; behind the row's end any bytes of it, masked below
+  auto load = [&](const uint8_t* row, int k) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(row + (k < K ? k : 0));
+    const uint4 hi = *reinterpret_cast<const uint4*>(row + (k + 16 < K ? k + 16 : 0));
+    return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
+                 static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+  };
+  auto masked = [&](i32x8 f, int k) {
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const i32x8 af = load_frag(a + static_cast<size_t>(tok[t]) * K, k, K);
-      const float sc = s * sa[static_cast<size_t>(tok[t]) * KB + b];
-      const f32x4 p = mfma_block<OUT_BF16>(wf, af);
+    for (int i = 0; i < 4; ++i) {
+      f[i] = k < K ? f[i] : 0;
+      f[i + 4] = k + 16 < K ? f[i + 4] : 0;
+    }
+    return f;
+  };
+  for (int b0 = wave; b0 < KB; b0 += WAVES * U) {
+    i32x8 wf[U][J], af[U][T];
+    float sc[U][T];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], sc, acc[t][i]);
+    for (int u = 0; u < U; ++u) {
+      const int b = min(b0 + u * WAVES, KB - 1), k = b * kScaleBlock + kq;
+#pragma unroll
+      for (int j = 0; j < J; ++j) wf[u][j] = load(wrow[j], k);
+      const float s = swrow[b];
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        af[u][t] = load(arow[t], k);
+        sc[u][t] = s * sarow[t][b];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * WAVES, k = b * kScaleBlock + kq;
+      if (b >= KB) break;
+      if ((b + 1) * kScaleBlock > K) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) wf[u][j] = masked(wf[u][j], k);
+#pragma unroll
+        for (int t = 0; t < T; ++t) af[u][t] = masked(af[u][t], k);
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const f32x4 p = mfma_block<OUT_BF16>(wf[u][j], af[u][t]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][t][i] = fmaf(p[i], sc[u][t], acc[j][t][i]);
+        }
     }
   }
 #pragma unroll
-  for (int t = 0; t < T; ++t) red[wave][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      red[wave][j * T + t][lane] = make_float4(acc[j][t][0], acc[j][t][1], acc[j][t][2], acc[j][t][3]);
   __syncthreads();
-  for (int t = wave; t < T; t += WAVES) {
-    f32x4 v = zero4();
+  for (int i = wave; i < J * T; i += WAVES) {
+    const int j = i / T, t = i % T;
+    f32x4 sum = zero4();
 #pragma unroll
-    for (int i = 0; i < WAVES; ++i) {
-      const float4 r = red[i][t][lane];
-      v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+    for (int v = 0; v < WAVES; ++v) {
+      const float4 r = red[v][i][lane];
+      sum[0] += r.x; sum[1] += r.y; sum[2] += r.z; sum[3] += r.w;
     }
     const int64_t m = m0 + 16 * t + l16;
-    if (m < M) store_out<OUT_BF16>(y, static_cast<size_t>(m) * N, n0 + 4 * (lane >> 4), N, v);
+    if (m < M) store_out<OUT_BF16>(y, static_cast<size_t>(m) * N, n0 + 16 * j + 4 * (lane >> 4), N, sum);
   }
 }
 
@@ -184,6 +224,13 @@ constexpr int kSteps = 8;   // scale blocks whose scales are loaded together
 // LDS of a tile: two buffers of operand rows, of token scales and of weight scales.
 constexpr int tile_lds(int TN, int TT) { return 2 * ((TN + TT) * kScaleBlock + TT * kSteps * 4 + 256); }
 
+// Waves of a SIMD (by their registers) and workgroups of a CU (also by LDS)
+// that run at a time.
+constexpr int tile_waves(int TN, int TT, int waves) { return TN * TT / waves <= 1024 ? 4 : 2; }
+constexpr int tile_groups(int TN, int TT, int waves) {
+  return std::min(160 * 1024 / tile_lds(TN, TT), 4 * tile_waves(TN, TT, waves) / waves);
+}
+
 // The order of the tiles: workgroups go to the 8 XCDs in turn, so each XCD
 // takes a run of neighbouring tiles, and within it groups of kGroup token
 // tiles wide, so that the tiles running at a time share rows in its L2
@@ -205,7 +252,7 @@ struct TileOrder {
 };
 
 template <int TN, int TT, int WN, int WT, bool OUT_BF16>
-__global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
+__global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8_matmul_tile_kernel(
     int64_t M, int N, int K, TileOrder order, const uint8_t* __restrict__ a, const float* __restrict__ sa,
     const uint8_t* __restrict__ w, const float* __restrict__ sw, void* __restrict__ y) {
   constexpr int kWaves = WN * WT;
@@ -214,10 +261,10 @@ __global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
   constexpr int kLoads = kRows / 8 / kWaves;              // 8 rows of 128 bytes a load
   constexpr int kWLoads = TN / 8 / kWaves;                // those of the weight
   constexpr int kBuf = kRows * kScaleBlock;
-  constexpr int kScaleLoads = TT * kSteps / 64 / kWaves;
+  constexpr int kScaleLoads = (TT * kSteps / 64 + kWaves - 1) / kWaves;
   constexpr int kScaleBuf = TT * kSteps * 4;
   static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0 && kWaves % 2 == 0, "whole loads");
-  static_assert(TN / WN <= kScaleBlock && kScaleBlock % (TN / WN) == 0 && TN / kScaleBlock <= 64 / kSteps, "scales");
+  static_assert(TN / WN <= kScaleBlock && kScaleBlock % (TN / WN) == 0 && (TN + kScaleBlock - 1) / kScaleBlock <= 64 / kSteps, "scales");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const uint32_t smem0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)smem));
 
@@ -275,7 +322,7 @@ __global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
 #pragma unroll
     for (int i = 0; i < kScaleLoads; ++i) {
       const int r0 = (i * kWaves + wave) * (64 / kSteps);
-      load_lds4(smem0 + 2 * kBuf + half * kScaleBuf + r0 * (kSteps * 4), (min(r0 + lane / kSteps, mlast) * KB + kb) * 4u,
+      if (TT * kSteps % (64 * kWaves) == 0 || r0 < TT) load_lds4(smem0 + 2 * kBuf + half * kScaleBuf + r0 * (kSteps * 4), (min(r0 + lane / kSteps, mlast) * KB + kb) * 4u,
                 sabase);
     }
     if (wave == 0)
@@ -323,7 +370,7 @@ __global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
   // waits for the other; the last three of a turn fall into the next one.  The
   // fences keep this order: left alone, the compiler puts each addition right
   // behind its product.
-  constexpr int kLag = 3, kUnits = NT * TTW;
+  constexpr int kLag = TTW < 4 ? 1 : 3, kUnits = NT * TTW;
   constexpr int kEvery = 1, kBatch = 1;   // loads are issued kBatch at every kEvery products
   static_assert(NT % 2 == 0 && kUnits % (kLag + 1) == 0 && kLag <= TTW, "register slots repeat from turn to turn");
   i32x8 wf[2], af[TTW];
@@ -426,32 +473,69 @@ __global__ __launch_bounds__(64 * WN * WT) void fp8_matmul_tile_kernel(
 
 template <int TN, int TT, int WN, int WT, bool OUT_BF16>
 static hipError_t launch_tiles(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
-                               const float* sw, void* y, hipStream_t st) {
+                               const float* sw, void* y, int ncu, hipStream_t st) {
   const auto kernel = fp8_matmul_tile_kernel<TN, TT, WN, WT, OUT_BF16>;
   constexpr int kLds = tile_lds(TN, TT);
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     kLds);
-  int ncu = 0;
-  if (e == hipSuccess) e = device_cus(&ncu);
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
   TileOrder order;
   order.n_tiles = (N + TN - 1) / TN;
   order.t_tiles = static_cast<int>((M + TT - 1) / TT);
   const int64_t tiles = static_cast<int64_t>(order.n_tiles) * order.t_tiles;
   if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
-  order.turn = static_cast<int>(tiles < ncu ? tiles : ncu);
+  const int slots = ncu * tile_groups(TN, TT, WN * WT);
+  order.turn = static_cast<int>(tiles < slots ? tiles : slots);
   order.per = order.turn % 8 == 0 ? static_cast<int>((tiles + 7) / 8) : 0;
   kernel<<<dim3(order.turn), 64 * WN * WT, kLds, st>>>(M, N, K, order, a, sa, w, sw, y);
   return hipGetLastError();
 }
 
+template <int J, int T, int WAVES, int U, bool OUT_BF16>
+static hipError_t launch_rows(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
+                              const float* sw, void* y, hipStream_t st) {
+  const dim3 grid((N + 16 * J - 1) / (16 * J), static_cast<unsigned>((M + 16 * T - 1) / (16 * T)));
+  fp8_matmul_rows_kernel<J, T, WAVES, U, OUT_BF16><<<grid, 64 * WAVES, 0, st>>>(M, N, K, a, sa, w, sw, y);
+  return hipGetLastError();
+}
+
+// Time of a pass over `tiles` tiles, of which `groups` run on a CU at a time:
+// `full` for a full load of the card, `one` for at most one a CU.
+static int64_t tiles_cost(int64_t tiles, int ncu, int groups, int full, int one) {
+  const int64_t slots = static_cast<int64_t>(ncu) * groups, left = tiles % slots;
+  return tiles / slots * full + (left == 0 ? 0 : left <= ncu ? one : full);
+}
+
+// The kernel by the sizes.  us at N = K = 4096, bf16 out, for 16 / 32 / 64 /
+// 128 / 256 / 512 / 1024 / 2048 / 32768 tokens: rows 7.0 / 8.5 / 11.4 / 15.2 /
+// 21, tiles of 64 x 64 20 up to 256 tokens, then 23 / 32 / 59 / 1000, of 128 x
+// 128 25 up to 512, then 28 / 40 / 640, of 256 x 256 47 to 50, then 500.  So
+// few tokens take the rows kernel, unless there are outputs enough to fill
+// half the card with 64 x 64 tiles (64 tokens, 16416 outputs: 28, rows 38),
+// and the others the tile of the least cost, by the measured time of a load
+// of the card.  fp32 outputs have no 256 x 256 tile: with its operands widened
+// in registers 128 x 256 took as long as 128 x 128 (1077, 1118 us).
 template <bool OUT_BF16>
 static hipError_t launch_fp8_matmul_to(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                                        const float* sw, void* y, hipStream_t st) {
-  if (M > 64) return launch_tiles<OUT_BF16 ? 256 : 128, 256, 2, 4, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
-  const dim3 grid(static_cast<unsigned>((M + 63) / 64), (N + 15) / 16);
-  fp8_matmul_rows_kernel<4, 8, OUT_BF16><<<grid, 512, 0, st>>>(M, N, K, a, sa, w, sw, y);
-  return hipGetLastError();
+  int ncu = 0;
+  const hipError_t e = device_cus(&ncu);
+  if (e != hipSuccess) return e;
+  const auto tiles = [&](int64_t of) { return (M + of - 1) / of * ((N + of - 1) / of); };
+  if (M <= 16) return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+  if (M <= 128 && 2 * tiles(64) <= ncu) {
+    if (M <= 32) return launch_rows<2, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    if (M <= 64) return launch_rows<2, 2, 8, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    return launch_rows<4, 2, 8, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+  }
+  const int64_t c64 = tiles_cost(tiles(64), ncu, tile_groups(64, 64, 4), OUT_BF16 ? 29 : 51, OUT_BF16 ? 20 : 29);
+  const int64_t c128 = tiles_cost(tiles(128), ncu, tile_groups(128, 128, 4), OUT_BF16 ? 40 : 71, OUT_BF16 ? 26 : 45);
+  if constexpr (OUT_BF16) {
+    const int64_t c256 = tiles_cost(tiles(256), ncu, tile_groups(256, 256, 8), 62, 50);
+    if (c256 <= c64 && c256 <= c128) return launch_tiles<256, 256, 2, 4, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+  }
+  if (c64 < c128) return launch_tiles<64, 64, 2, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+  return launch_tiles<128, 128, 2, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
 }
 
 hipError_t launch_fp8_matmul(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
