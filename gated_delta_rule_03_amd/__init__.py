@@ -435,70 +435,60 @@ def kda_output_gate(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, *, y
 # ---- the operators around the core -----------------------------------------
 # These take their device and default stream from their tensors, check shapes
 # and types, and allocate what they return on the stream that they run on.
+# They are called once a token and layer, so the binding's own time counts: it
+# does each step once (a kernel launch is ~4 us, the binding 3 to 6).
 
-class _On:
-    """The device of a call's tensors made current, and the call's stream:
-    `stream`, or that device's current one."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("tensors must be on the GPU")
-        if stream is not None and stream.device != device:
+def _run(device, stream, call):
+    """call(stream handle) with the tensors' device current, on `stream` or on
+    that device's current stream, which is also where `call` allocates."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    if stream is not None:
+        if stream.device != device:
             raise ValueError("the stream belongs to another device than the tensors")
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        self.other = torch.cuda.device(self.device) if torch.cuda.current_device() != self.device.index else None
-        if self.other is not None:
-            self.other.__enter__()
-        self.inner = torch.cuda.stream(self.stream) if self.stream is not None else None
-        if self.inner is not None:
-            self.inner.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
-        if self.other is not None:
-            self.other.__exit__(*exc)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if device.index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
 
 
-def _want(name, t, shape, dtype, device):
+def _at(name, t, shape, dtype, device):
+    """The address of a tensor that has to be of this shape and type, or None for None."""
     if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}, "
                          f"not {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace_at(nbytes, device, workspace):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _op_struct(cfg: Config):
+    """The fields of the config that these operators read."""
+    c = KdaConfigC()
+    c.num_heads = cfg.num_heads
+    c.head_v_dim = cfg.head_v_dim
+    c.io_dtype = _dtype_code(cfg.io_dtype)
+    c.out_dtype = _dtype_code(cfg.out_dtype)
+    if cfg.stage_events is not None:
+        c.stage_events = ctypes.cast(cfg.stage_events, ctypes.c_void_p)
+    return ctypes.byref(c)
 
 
 def _scale_blocks(k: int) -> int:
     return (k + SCALE_BLOCK - 1) // SCALE_BLOCK
-
-
-def _add_rmsnorm(name, cfg, x, residual, weight, eps, h, y, y_scale, stream, fp8):
-    hidden, dev = x.shape[-1], x.device
-    n = x.numel() // hidden if x.numel() else 0
-    out = torch.float8_e4m3fn if fp8 else cfg.out_dtype
-    blocks = (*x.shape[:-1], _scale_blocks(hidden))
-    _want("x", x, x.shape, cfg.io_dtype, dev)
-    _want("residual", residual, x.shape, cfg.io_dtype, dev)
-    _want("weight", weight, (hidden,), torch.float32, dev)
-    _want("h", h, x.shape, cfg.io_dtype, dev)
-    _want("y", y, x.shape, out, dev)
-    _want("y_scale", y_scale, blocks, torch.float32, dev)
-    with _On(dev, stream) as st:
-        if h is None and residual is not None:
-            h = torch.empty_like(x)
-        if y is None:
-            y = torch.empty(x.shape, dtype=out, device=dev)
-        args = [ctypes.byref(cfg.c_struct()), n, hidden, _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(h),
-                _ptr(y)]
-        if fp8:
-            if y_scale is None:
-                y_scale = torch.empty(blocks, dtype=torch.float32, device=dev)
-            args.append(_ptr(y_scale))
-        _check(getattr(_lib, name)(*args, st), name)
-    return y, y_scale, x if h is None else h
 
 
 def kda_add_rmsnorm(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=None, y=None, stream=None):
@@ -506,15 +496,47 @@ def kda_add_rmsnorm(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=No
     x, residual [..., hidden] io dtype (residual may be None), weight [hidden]
     fp32.  Returns (y, h), y in the out dtype, h in the io dtype (x itself
     without a residual or h).  h=x or h=residual works in place."""
-    y, _, h = _add_rmsnorm("kda_add_rmsnorm", cfg, x, residual, weight, eps, h, y, None, stream, False)
-    return y, h
+    shape, dev = x.shape, x.device
+    hidden = shape[-1]
+    xp, rp = _at("x", x, shape, cfg.io_dtype, dev), _at("residual", residual, shape, cfg.io_dtype, dev)
+    wp = _at("weight", weight, (hidden,), torch.float32, dev)
+    hp, yp = _at("h", h, shape, cfg.io_dtype, dev), _at("y", y, shape, cfg.out_dtype, dev)
+
+    def call(st):
+        h_ = torch.empty_like(x) if h is None and residual is not None else h
+        y_ = torch.empty_like(x, dtype=cfg.out_dtype) if y is None else y
+        _check(_lib.kda_add_rmsnorm(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
+                                    hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(), st),
+               "kda_add_rmsnorm")
+        return y_, x if h_ is None else h_
+    return _run(dev, stream, call)
 
 
 def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=None, y=None, y_scale=None,
                         stream=None):
     """kda_add_rmsnorm with y as e4m3 rows.  Returns (y, y_scale, h): y
     [..., hidden] float8_e4m3fn, y_scale [..., ceil(hidden / 128)] fp32."""
-    return _add_rmsnorm("kda_add_rmsnorm_fp8", cfg, x, residual, weight, eps, h, y, y_scale, stream, True)
+    shape, dev = x.shape, x.device
+    hidden = shape[-1]
+    blocks = (*shape[:-1], _scale_blocks(hidden))
+    xp, rp = _at("x", x, shape, cfg.io_dtype, dev), _at("residual", residual, shape, cfg.io_dtype, dev)
+    wp = _at("weight", weight, (hidden,), torch.float32, dev)
+    hp, yp = _at("h", h, shape, cfg.io_dtype, dev), _at("y", y, shape, torch.float8_e4m3fn, dev)
+    sp = _at("y_scale", y_scale, blocks, torch.float32, dev)
+
+    def call(st):
+        h_ = torch.empty_like(x) if h is None and residual is not None else h
+        y_ = torch.empty_like(x, dtype=torch.float8_e4m3fn) if y is None else y
+        s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
+        _check(_lib.kda_add_rmsnorm_fp8(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
+                                        hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(),
+                                        sp if s_ is y_scale else s_.data_ptr(), st), "kda_add_rmsnorm_fp8")
+        return y_, s_, x if h_ is None else h_
+    return _run(dev, stream, call)
+
+
+def kda_add_rmsnorm_backward_workspace_bytes(cfg: Config, n_tokens: int, hidden: int) -> int:
+    return int(_lib.kda_add_rmsnorm_backward_workspace_bytes(_op_struct(cfg), n_tokens, hidden))
 
 
 def kda_add_rmsnorm_backward(cfg: Config, h, weight, dy, d_h=None, eps: float = 1e-6, *, dx=None, workspace=None,
@@ -523,45 +545,56 @@ def kda_add_rmsnorm_backward(cfg: Config, h, weight, dy, d_h=None, eps: float = 
     the out dtype, d_h the gradient that reaches h otherwise (fp32) or None.
     Returns (dx [..., hidden], dweight [hidden]), fp32; dx is the gradient of x
     and of residual alike.  dx=d_h works in place."""
-    hidden, dev = h.shape[-1], h.device
-    n = h.numel() // hidden if h.numel() else 0
-    _want("h", h, h.shape, cfg.io_dtype, dev)
-    _want("weight", weight, (hidden,), torch.float32, dev)
-    _want("dy", dy, h.shape, cfg.out_dtype, dev)
-    _want("d_h", d_h, h.shape, torch.float32, dev)
-    _want("dx", dx, h.shape, torch.float32, dev)
-    with _On(dev, stream) as st:
-        if dx is None:
-            dx = torch.empty(h.shape, dtype=torch.float32, device=dev)
-        dw = torch.empty((hidden,), dtype=torch.float32, device=dev)
-        c = ctypes.byref(cfg.c_struct())
-        ws = _workspace(int(_lib.kda_add_rmsnorm_backward_workspace_bytes(c, n, hidden)), dev, workspace)
-        _check(_lib.kda_add_rmsnorm_backward(c, n, hidden, _ptr(h), _ptr(weight), float(eps), _ptr(dy), _ptr(d_h),
-                                             _ptr(dx), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(), st),
+    shape, dev = h.shape, h.device
+    hidden = shape[-1]
+    n = h.numel() // hidden if hidden else 0
+    hp, wp = _at("h", h, shape, cfg.io_dtype, dev), _at("weight", weight, (hidden,), torch.float32, dev)
+    dyp, dhp = _at("dy", dy, shape, cfg.out_dtype, dev), _at("d_h", d_h, shape, torch.float32, dev)
+    dxp = _at("dx", dx, shape, torch.float32, dev)
+
+    def call(st):
+        dx_ = torch.empty_like(h, dtype=torch.float32) if dx is None else dx
+        dw = torch.empty_like(weight)
+        c = _op_struct(cfg)
+        ws, wsp, size = _workspace_at(_lib.kda_add_rmsnorm_backward_workspace_bytes(c, n, hidden), dev, workspace)
+        _check(_lib.kda_add_rmsnorm_backward(c, n, hidden, hp, wp, eps, dyp, dhp,
+                                             dxp if dx_ is dx else dx_.data_ptr(), dw.data_ptr(), wsp, size, st),
                "kda_add_rmsnorm_backward")
-    return dx, dw
+        return dx_, dw
+    return _run(dev, stream, call)
+
+
+def _gate_args(cfg, o, gate, o_norm_weight):
+    """(leading axes, n_tokens, addresses) of the output epilogue's inputs."""
+    H, dv, dev = cfg.num_heads, cfg.head_v_dim, o.device
+    lead = o.shape[:-2]
+    full = (*lead, H, dv)
+    return (lead, full, o.numel() // (H * dv), _at("o", o, full, cfg.out_dtype, dev),
+            _at("gate", gate, full, cfg.io_dtype, dev), _at("o_norm_weight", o_norm_weight, (dv,), torch.float32, dev))
 
 
 def kda_output_gate_fp8(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, *, y=None, y_scale=None, stream=None):
     """kda_output_gate with its output as e4m3 rows: o [..., H, dv] out dtype,
     gate the same shape in the io dtype.  Returns (y [..., H * dv]
     float8_e4m3fn, y_scale [..., ceil(H * dv / 128)] fp32)."""
-    H, dv, dev = cfg.num_heads, cfg.head_v_dim, o.device
-    lead = tuple(o.shape[:-2])
-    _want("o", o, (*lead, H, dv), cfg.out_dtype, dev)
-    _want("gate", gate, (*lead, H, dv), cfg.io_dtype, dev)
-    _want("o_norm_weight", o_norm_weight, (dv,), torch.float32, dev)
-    _want("y", y, (*lead, H * dv), torch.float8_e4m3fn, dev)
-    _want("y_scale", y_scale, (*lead, _scale_blocks(H * dv)), torch.float32, dev)
-    with _On(dev, stream) as st:
-        if y is None:
-            y = torch.empty((*lead, H * dv), dtype=torch.float8_e4m3fn, device=dev)
-        if y_scale is None:
-            y_scale = torch.empty((*lead, _scale_blocks(H * dv)), dtype=torch.float32, device=dev)
-        _check(_lib.kda_output_gate_fp8(ctypes.byref(cfg.c_struct()), o.numel() // (H * dv), _ptr(o), _ptr(gate),
-                                        _ptr(o_norm_weight), float(eps), _ptr(y), _ptr(y_scale), st),
+    dev = o.device
+    lead, _, n, op, gp, wp = _gate_args(cfg, o, gate, o_norm_weight)
+    row = cfg.num_heads * cfg.head_v_dim
+    rows, blocks = (*lead, row), (*lead, _scale_blocks(row))
+    yp, sp = _at("y", y, rows, torch.float8_e4m3fn, dev), _at("y_scale", y_scale, blocks, torch.float32, dev)
+
+    def call(st):
+        y_ = torch.empty(rows, dtype=torch.float8_e4m3fn, device=dev) if y is None else y
+        s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
+        _check(_lib.kda_output_gate_fp8(_op_struct(cfg), n, op, gp, wp, eps,
+                                        yp if y_ is y else y_.data_ptr(), sp if s_ is y_scale else s_.data_ptr(), st),
                "kda_output_gate_fp8")
-    return y, y_scale
+        return y_, s_
+    return _run(dev, stream, call)
+
+
+def kda_output_gate_backward_workspace_bytes(cfg: Config, n_tokens: int) -> int:
+    return int(_lib.kda_output_gate_backward_workspace_bytes(_op_struct(cfg), n_tokens))
 
 
 def kda_output_gate_backward(cfg: Config, o, gate, o_norm_weight, dy, eps: float = 1e-6, *, workspace=None,
@@ -569,24 +602,19 @@ def kda_output_gate_backward(cfg: Config, o, gate, o_norm_weight, dy, eps: float
     """Gradients of kda_output_gate: o, dy [..., H, dv] out dtype, gate the
     same shape in the io dtype.  Returns (d_o in the out dtype, as
     kda_varlen_backward takes it, d_gate fp32, d_weight [dv] fp32)."""
-    H, dv, dev = cfg.num_heads, cfg.head_v_dim, o.device
-    lead = tuple(o.shape[:-2])
-    _want("o", o, (*lead, H, dv), cfg.out_dtype, dev)
-    _want("gate", gate, (*lead, H, dv), cfg.io_dtype, dev)
-    _want("o_norm_weight", o_norm_weight, (dv,), torch.float32, dev)
-    _want("dy", dy, (*lead, H, dv), cfg.out_dtype, dev)
-    n = o.numel() // (H * dv)
-    with _On(dev, stream) as st:
-        d_o = torch.empty_like(o)
-        d_gate = torch.empty(gate.shape, dtype=torch.float32, device=dev)
-        dw = torch.empty((dv,), dtype=torch.float32, device=dev)
-        c = ctypes.byref(cfg.c_struct())
-        ws = _workspace(int(_lib.kda_output_gate_backward_workspace_bytes(c, n)), dev, workspace)
-        _check(_lib.kda_output_gate_backward(c, n, _ptr(o), _ptr(gate), _ptr(o_norm_weight), float(eps), _ptr(dy),
-                                             _ptr(d_o), _ptr(d_gate), _ptr(dw), _ptr(ws),
-                                             ws.numel() * ws.element_size(), st),
-               "kda_output_gate_backward")
-    return d_o, d_gate, dw
+    dev = o.device
+    _, full, n, op, gp, wp = _gate_args(cfg, o, gate, o_norm_weight)
+    dyp = _at("dy", dy, full, cfg.out_dtype, dev)
+
+    def call(st):
+        d_o, d_gate = torch.empty_like(o), torch.empty_like(gate, dtype=torch.float32)
+        dw = torch.empty_like(o_norm_weight)
+        c = _op_struct(cfg)
+        ws, wsp, size = _workspace_at(_lib.kda_output_gate_backward_workspace_bytes(c, n), dev, workspace)
+        _check(_lib.kda_output_gate_backward(c, n, op, gp, wp, eps, dyp, d_o.data_ptr(), d_gate.data_ptr(),
+                                             dw.data_ptr(), wsp, size, st), "kda_output_gate_backward")
+        return d_o, d_gate, dw
+    return _run(dev, stream, call)
 
 
 def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
@@ -594,16 +622,16 @@ def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
     [..., ceil(K / 128)] fp32 (as kda_add_rmsnorm_fp8 and kda_output_gate_fp8
     return them), w [N, K] float8_e4m3fn with w_scale [ceil(N / 128),
     ceil(K / 128)] fp32.  Returns y [..., N] in the out dtype."""
-    (N, K), dev = w.shape, a.device
-    lead = tuple(a.shape[:-1])
-    _want("a", a, (*lead, K), torch.float8_e4m3fn, dev)
-    _want("a_scale", a_scale, (*lead, _scale_blocks(K)), torch.float32, dev)
-    _want("w", w, (N, K), torch.float8_e4m3fn, dev)
-    _want("w_scale", w_scale, (_scale_blocks(N), _scale_blocks(K)), torch.float32, dev)
-    _want("y", y, (*lead, N), cfg.out_dtype, dev)
-    with _On(dev, stream) as st:
-        if y is None:
-            y = torch.empty((*lead, N), dtype=cfg.out_dtype, device=dev)
-        _check(_lib.kda_fp8_matmul(ctypes.byref(cfg.c_struct()), math.prod(lead), N, K, _ptr(a), _ptr(a_scale),
-                                   _ptr(w), _ptr(w_scale), _ptr(y), st), "kda_fp8_matmul")
-    return y
+    (N, K), dev, lead = w.shape, a.device, a.shape[:-1]
+    kb, f8 = _scale_blocks(K), torch.float8_e4m3fn
+    ap, sp = _at("a", a, (*lead, K), f8, dev), _at("a_scale", a_scale, (*lead, kb), torch.float32, dev)
+    wp, wsp = _at("w", w, (N, K), f8, dev), _at("w_scale", w_scale, (_scale_blocks(N), kb), torch.float32, dev)
+    shape = (*lead, N)
+    yp = _at("y", y, shape, cfg.out_dtype, dev)
+
+    def call(st):
+        y_ = torch.empty(shape, dtype=cfg.out_dtype, device=dev) if y is None else y
+        _check(_lib.kda_fp8_matmul(_op_struct(cfg), math.prod(lead), N, K, ap, sp, wp, wsp,
+                                   yp if y_ is y else y_.data_ptr(), st), "kda_fp8_matmul")
+        return y_
+    return _run(dev, stream, call)

@@ -224,10 +224,12 @@ hipError_t launch_output_gate_fp8(int D, int64_t n_tokens, int row, const void* 
   });
 }
 
-// Workgroups of the backward, each with a row of partial sums.
+// Workgroups of the backward, each with a row of partial sums: three a CU.
+// 32768 x 32 x 128 in bf16: 308 us (5.2 TB/s) with 768, 325 with 512, 320 with
+// 1024, 371 with 2048 (more rows at a time, in five streams of memory).
 int output_gate_bwd_parts(int D, int64_t rows) {
   const int64_t blocks = (rows * (D / 8) + kEpiThreads - 1) / kEpiThreads;
-  return static_cast<int>(blocks < 2048 ? blocks : 2048);
+  return static_cast<int>(blocks < 768 ? blocks : 768);
 }
 
 hipError_t launch_output_gate_bwd(int D, int64_t rows, const void* o, const void* gate, const float* w, float eps,

@@ -13,15 +13,18 @@
 namespace kda {
 
 // EPL consecutive io elements (EPL in {1, 2, 4, 8}) at index i of a bf16 or
-// fp32 tensor, as floats, with the widest aligned loads.
-template <bool BF16, int EPL>
+// fp32 tensor, as floats, with the widest aligned loads.  ONCE: bf16 that no
+// one reads again soon (a non-temporal load).
+template <bool BF16, int EPL, bool ONCE = false>
 __device__ __forceinline__ void load_n(const void* p, size_t i, float (&x)[EPL]) {
   if constexpr (BF16) {
     const uint16_t* q = static_cast<const uint16_t*>(p) + i;
     uint32_t w[(EPL + 1) / 2];
     if constexpr (EPL == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q);
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      const u32x4* from = reinterpret_cast<const u32x4*>(q);
+      const u32x4 v = ONCE ? __builtin_nontemporal_load(from) : *from;
+      w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
     } else if constexpr (EPL == 4) {
       const uint2 v = *reinterpret_cast<const uint2*>(q);
       w[0] = v.x; w[1] = v.y;
