@@ -518,15 +518,17 @@ static int64_t tiles_cost(int64_t tiles, int ncu, int groups, int full, int one)
 template <bool OUT_BF16>
 static hipError_t launch_fp8_matmul_to(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                                        const float* sw, void* y, hipStream_t st) {
+  if (M <= 16) return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
   int ncu = 0;
   const hipError_t e = device_cus(&ncu);
   if (e != hipSuccess) return e;
   const auto tiles = [&](int64_t of) { return (M + of - 1) / of * ((N + of - 1) / of); };
-  if (M <= 16) return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
-  if (M <= 128 && 2 * tiles(64) <= ncu) {
-    if (M <= 32) return launch_rows<2, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
-    if (M <= 64) return launch_rows<2, 2, 8, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
-    return launch_rows<4, 2, 8, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+  if (M <= 128 && 2 * tiles(64) <= ncu) {   // the most reuse that still gives every CU a workgroup
+    const auto groups = [&](int64_t outs, int64_t toks) { return (N + outs - 1) / outs * ((M + toks - 1) / toks); };
+    if (groups(64, 32) >= ncu) return launch_rows<4, 2, 8, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    if (groups(32, 32) >= ncu) return launch_rows<2, 2, 8, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    if (groups(32, 16) >= ncu) return launch_rows<2, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
   }
   const int64_t c64 = tiles_cost(tiles(64), ncu, tile_groups(64, 64, 4), OUT_BF16 ? 29 : 51, OUT_BF16 ? 20 : 29);
   const int64_t c128 = tiles_cost(tiles(128), ncu, tile_groups(128, 128, 4), OUT_BF16 ? 40 : 71, OUT_BF16 ? 26 : 45);

@@ -8,9 +8,9 @@
 //   dw = sum over tokens of dy * n
 //
 // HBM-bound: each row is read once and kept in registers between the row's
-// sums and its outputs.  A row belongs to WPR waves, 8 channels a lane and
-// step (16-byte loads in bf16), NV steps; 16 lanes hold one scale block, so
-// its largest value is four DPP steps.
+// sums and its outputs.  A row belongs to L lanes (16, 32 or whole waves), 8
+// channels a lane and step (16-byte loads in bf16), NV steps; 16 lanes hold
+// one scale block, so its largest value is four DPP steps.
 #include "kda_device.h"
 #include "kda_internal.h"
 #include "vec_io.h"
@@ -21,19 +21,19 @@ namespace {
 
 enum class Out { kBf16, kFp32, kFp8 };
 
-// Sums of A values over the WPR waves of a row, in every lane.  `parity`
+// Sums of A values over the L lanes of a row, in each of them.  `parity`
 // alternates between the two halves of `red`, so one barrier per call is
 // enough: a wave that writes a half again has passed the barrier of the call
 // in between, which every wave reaches after reading that half.
-template <int WPR, int A>
+template <int L, int A>
 __device__ __forceinline__ void row_sums(float (&s)[A], float (*red)[16][A], int wave, int parity) {
 #pragma unroll
   for (int a = 0; a < A; ++a) {
     s[a] = lane_group_sum<16>(s[a]);
-    s[a] += __shfl_xor(s[a], 16);
-    s[a] += __shfl_xor(s[a], 32);
+    if constexpr (L > 16) s[a] += __shfl_xor(s[a], 16);
+    if constexpr (L > 32) s[a] += __shfl_xor(s[a], 32);
   }
-  if constexpr (WPR > 1) {
+  if constexpr (L > 64) {
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int a = 0; a < A; ++a) red[parity][wave][a] = s[a];
@@ -42,45 +42,44 @@ __device__ __forceinline__ void row_sums(float (&s)[A], float (*red)[16][A], int
     for (int a = 0; a < A; ++a) {
       float t = 0.f;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) t += red[parity][w][a];
+      for (int w = 0; w < L / 64; ++w) t += red[parity][w][a];
       s[a] = t;
     }
   }
 }
 
-// Waves of a workgroup: one row at a time, or four rows of one wave each.
-constexpr int waves_of(int wpr) { return wpr < 4 ? 4 : wpr; }
+// Threads of a workgroup: a row at a time, or 256 with several rows.
+constexpr int threads_of(int lanes) { return lanes < 256 ? 256 : lanes; }
 
 }  // namespace
 
-template <bool BF16, Out OUT, int WPR, int NV>
-__global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_kernel(
+template <bool BF16, Out OUT, int L, int NV>
+__global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_kernel(
     int64_t n_rows, int hidden, const void* x, const void* res, const float* __restrict__ w, float eps, void* h,
     void* y, float* __restrict__ scale) {
-  constexpr int kRows = waves_of(WPR) / WPR;   // rows at a time
+  constexpr int kRows = threads_of(L) / L;   // rows at a time
   __shared__ float red[2][16][1];
-  const int lane = threadIdx.x & 63;
-  const int wave = (threadIdx.x >> 6) % WPR;
+  const int lane = threadIdx.x % L;
   const int nvec = hidden >> 3;
   const int nblk = (hidden + kScaleBlock - 1) / kScaleBlock;
   const float rcp = 1.0f / static_cast<float>(hidden);
   float wv[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = (i * WPR + wave) * 64 + lane;
+    const int v = i * L + lane;
 #pragma unroll
     for (int e = 0; e < 8; ++e) wv[i][e] = 0.f;
     if (v < nvec) load_n<false, 8>(w, static_cast<size_t>(v) * 8, wv[i]);
   }
   int parity = 0;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + (WPR == 1 ? threadIdx.x >> 6 : 0); r < n_rows;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / L; r < n_rows;
        r += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
     const size_t base = static_cast<size_t>(r) * hidden;
     float hv[NV][8];
     float ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = (i * WPR + wave) * 64 + lane;
+      const int v = i * L + lane;
 #pragma unroll
       for (int e = 0; e < 8; ++e) hv[i][e] = 0.f;
       if (v < nvec) {
@@ -104,17 +103,17 @@ __global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_kernel(
         for (int e = 0; e < 8; ++e) ss[0] = fmaf(hv[i][e], hv[i][e], ss[0]);
       }
     }
-    row_sums<WPR, 1>(ss, red, wave, parity);
+    row_sums<L, 1>(ss, red, threadIdx.x >> 6, parity);
     const float inv = 1.0f / sqrtf(ss[0] * rcp + eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = (i * WPR + wave) * 64 + lane;
+      const int v = i * L + lane;
       float t[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) t[e] = hv[i][e] * wv[i][e];
       if constexpr (OUT == Out::kFp8) {
         float s;
-        const uint2 q = quantise_block8(t, inv, &s);   // all 64 lanes: zeros past the row's end
+        const uint2 q = quantise_block8(t, inv, &s);   // whole groups of 16 lanes: zeros past the row's end
         if (v < nvec) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(y) + base + static_cast<size_t>(v) * 8) = q;
           if ((lane & 15) == 0) scale[static_cast<size_t>(r) * nblk + (v >> 4)] = s;
@@ -132,34 +131,33 @@ __global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_kernel(
 // row of `part` per workgroup.  Rows go to the workgroups by a rule on the
 // sizes alone and the sums are joined in a fixed order, so dw is the same in
 // every run.
-template <bool H_BF16, bool DY_BF16, int WPR, int NV>
-__global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_bwd_kernel(
+template <bool H_BF16, bool DY_BF16, int L, int NV>
+__global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_bwd_kernel(
     int64_t n_rows, int hidden, const void* __restrict__ h, const float* __restrict__ w, float eps,
     const void* __restrict__ dy, const float* dh, float* dx, float* __restrict__ part) {
-  constexpr int kRows = waves_of(WPR) / WPR;
+  constexpr int kRows = threads_of(L) / L;
   __shared__ float red[2][16][2];
-  __shared__ float join[WPR == 1 ? 4 * 512 : 1];
-  const int lane = threadIdx.x & 63;
-  const int wave = (threadIdx.x >> 6) % WPR;
+  __shared__ float join[kRows > 1 ? kRows * L * 8 : 1];
+  const int lane = threadIdx.x % L;
   const int nvec = hidden >> 3;
   const float rcp = 1.0f / static_cast<float>(hidden);
   float wv[NV][8], dw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = (i * WPR + wave) * 64 + lane;
+    const int v = i * L + lane;
 #pragma unroll
     for (int e = 0; e < 8; ++e) wv[i][e] = dw[i][e] = 0.f;
     if (v < nvec) load_n<false, 8>(w, static_cast<size_t>(v) * 8, wv[i]);
   }
   int parity = 0;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + (WPR == 1 ? threadIdx.x >> 6 : 0); r < n_rows;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / L; r < n_rows;
        r += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
     const size_t base = static_cast<size_t>(r) * hidden;
     float hv[NV][8], gv[NV][8];
     float s[2] = {0.f, 0.f};   // sum h^2, sum g h
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = (i * WPR + wave) * 64 + lane;
+      const int v = i * L + lane;
 #pragma unroll
       for (int e = 0; e < 8; ++e) hv[i][e] = gv[i][e] = 0.f;
       if (v < nvec) {
@@ -172,12 +170,12 @@ __global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_bwd_kernel(
         s[1] = fmaf(gv[i][e] * wv[i][e], hv[i][e], s[1]);
       }
     }
-    row_sums<WPR, 2>(s, red, wave, parity);
+    row_sums<L, 2>(s, red, threadIdx.x >> 6, parity);
     const float inv = 1.0f / sqrtf(s[0] * rcp + eps);
     const float c = s[1] * rcp * inv * inv;   // n * mean(g n) = h * c
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = (i * WPR + wave) * 64 + lane;
+      const int v = i * L + lane;
       if (v < nvec) {
         float t[8];
 #pragma unroll
@@ -195,16 +193,20 @@ __global__ __launch_bounds__(64 * waves_of(WPR)) void add_rmsnorm_bwd_kernel(
       }
     }
   }
-  if constexpr (WPR == 1) {   // the four waves' rows joined
-    float* mine = join + (threadIdx.x >> 6) * 512 + lane * 8;
-    store_n<false, 8>(mine, 0, dw[0]);
+  if constexpr (kRows > 1) {   // the rows' lanes joined
+    static_assert(NV == 1, "a lane holds 8 channels");
+    store_n<false, 8>(join, threadIdx.x * 8, dw[0]);
     __syncthreads();
-    for (int c = threadIdx.x; c < hidden; c += 256)
-      part[static_cast<size_t>(blockIdx.x) * hidden + c] = (join[c] + join[512 + c]) + (join[1024 + c] + join[1536 + c]);
+    for (int c = threadIdx.x; c < hidden; c += 256) {
+      float t = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) t += join[k * L * 8 + c];
+      part[static_cast<size_t>(blockIdx.x) * hidden + c] = t;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = (i * WPR + wave) * 64 + lane;
+      const int v = i * L + lane;
       if (v < nvec) store_n<false, 8>(part, static_cast<size_t>(blockIdx.x) * hidden + static_cast<size_t>(v) * 8, dw[i]);
     }
   }
@@ -241,29 +243,31 @@ hipError_t launch_column_sums(int parts, int cols, const float* part, float* out
   return hipGetLastError();
 }
 
-// Calls f with the waves per row and the steps of 64 x 8 channels per wave
-// that hold a row of `hidden` channels in registers.
+// Calls f with the lanes per row and the steps of 8 channels a lane that hold
+// a row of `hidden` channels in registers.
 template <class F>
 static hipError_t with_row_shape(int hidden, F&& f) {
   using std::integral_constant;
-  if (hidden <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (hidden <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  if (hidden <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (hidden <= 8192) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  if (hidden <= 16384) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if (hidden <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (hidden <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (hidden <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (hidden <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  if (hidden <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (hidden <= 8192) return f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
+  if (hidden <= 16384) return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
 hipError_t launch_add_rmsnorm(int64_t n, int hidden, const void* x, const void* res, const float* w, float eps,
                               void* h, void* y, float* scale, bool io_bf16, bool out_bf16, hipStream_t st) {
-  return with_row_shape(hidden, [&](auto wpr, auto nv) {
-    constexpr int WPR = decltype(wpr)::value, NV = decltype(nv)::value;
-    constexpr int kRows = waves_of(WPR) / WPR;
+  return with_row_shape(hidden, [&](auto lanes, auto nv) {
+    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
+    constexpr int kRows = threads_of(L) / L;
     const int64_t blocks = (n + kRows - 1) / kRows;
     const dim3 grid(static_cast<unsigned>(blocks < 65536 ? blocks : 65536));
-    const dim3 block(64 * waves_of(WPR));
+    const dim3 block(threads_of(L));
     auto go = [&](auto bf, auto out) {
-      add_rmsnorm_kernel<decltype(bf)::value, decltype(out)::value, WPR, NV>
+      add_rmsnorm_kernel<decltype(bf)::value, decltype(out)::value, L, NV>
           <<<grid, block, 0, st>>>(n, hidden, x, res, w, eps, h, y, scale);
     };
     auto by_out = [&](auto bf) {
@@ -287,11 +291,11 @@ hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const fl
                                   hipStream_t st) {
   const int parts = add_rmsnorm_bwd_parts(n);
   if (parts > 0) {
-    const hipError_t e = with_row_shape(hidden, [&](auto wpr, auto nv) {
-      constexpr int WPR = decltype(wpr)::value, NV = decltype(nv)::value;
+    const hipError_t e = with_row_shape(hidden, [&](auto lanes, auto nv) {
+      constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
       auto go = [&](auto hb, auto db) {
-        add_rmsnorm_bwd_kernel<decltype(hb)::value, decltype(db)::value, WPR, NV>
-            <<<dim3(parts), dim3(64 * waves_of(WPR)), 0, st>>>(n, hidden, h, w, eps, dy, dh, dx, part);
+        add_rmsnorm_bwd_kernel<decltype(hb)::value, decltype(db)::value, L, NV>
+            <<<dim3(parts), dim3(threads_of(L)), 0, st>>>(n, hidden, h, w, eps, dy, dh, dx, part);
       };
       if (h_bf16 && dy_bf16) go(std::true_type{}, std::true_type{});
       else if (h_bf16) go(std::true_type{}, std::false_type{});
