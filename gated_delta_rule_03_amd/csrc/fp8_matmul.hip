@@ -199,18 +199,38 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
 // The loads are written in assembly (they have no register output): the
 // compiler's own form of them makes every later LDS read wait for all of
 // them.  Their order against the LDS reads is the barrier below.  m0 is
-// reserved: the compiler keeps nothing in it.  The first form loads where
-// k < end; its branch is inside the assembly so that the products around it
-// stay one block of code, whose registers the compiler can place (with a
-// branch of its own it spills).
-__device__ __forceinline__ void load_lds16_if(int k, int end, uint32_t lds, uint32_t voff, const uint8_t* base) {
-  asm volatile(
-      "s_cmp_ge_i32 %0, %1\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %3, %4\n.Lskip%=:" ::"s"(k),
-      "s"(end), "s"(lds), "v"(voff), "s"(base)
-      : "memory", "scc");
+// reserved: the compiler keeps nothing in it; a load that reads it needs one
+// wait state behind a scalar write of it (s_nop 0), and five behind a vector
+// instruction that wrote its scalar address, which the compiler does not count
+// in front of assembly (s_nop 4).  The first form is COUNT loads
+// where k < end, to LDS `step` bytes apart; its branch is inside the assembly
+// so that the products around it stay one block of code, whose registers the
+// compiler can place (with a branch of its own it spills).
+template <int COUNT, int STEP>
+__device__ __forceinline__ void load_lds16_if(int k, int end, uint32_t lds, const uint32_t* voff, const uint8_t* base) {
+  static_assert(COUNT == 1 || COUNT == 2 || COUNT == 4, "");
+  k = __builtin_amdgcn_readfirstlane(k);
+  end = __builtin_amdgcn_readfirstlane(end);
+  lds = __builtin_amdgcn_readfirstlane(lds);
+#define KDA_LDS_FIRST \
+  "s_cmp_ge_i32 %0, %1\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %5, %3\n"
+#define KDA_LDS_NEXT(v) "\ts_add_u32 m0, m0, %4\n\ts_nop 0\n\tglobal_load_lds_dwordx4 " v ", %3\n"
+  if constexpr (COUNT == 4)
+    asm volatile(KDA_LDS_FIRST KDA_LDS_NEXT("%6") KDA_LDS_NEXT("%7") KDA_LDS_NEXT("%8") ".Lskip%=:" ::"s"(k), "s"(end),
+                 "s"(lds), "s"(base), "n"(STEP), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3])
+                 : "memory", "scc");
+  else if constexpr (COUNT == 2)
+    asm volatile(KDA_LDS_FIRST KDA_LDS_NEXT("%6") ".Lskip%=:" ::"s"(k), "s"(end), "s"(lds), "s"(base), "n"(STEP),
+                 "v"(voff[0]), "v"(voff[1])
+                 : "memory", "scc");
+  else
+    asm volatile(KDA_LDS_FIRST ".Lskip%=:" ::"s"(k), "s"(end), "s"(lds), "s"(base), "n"(STEP), "v"(voff[0])
+                 : "memory", "scc");
+#undef KDA_LDS_FIRST
+#undef KDA_LDS_NEXT
 }
 __device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, const void* base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
 }
 
 // Every load of this wave has landed and its LDS reads are done; then every
@@ -260,6 +280,10 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   constexpr int kRows = TN + TT;
   constexpr int kLoads = kRows / 8 / kWaves;              // 8 rows of 128 bytes a load
   constexpr int kWLoads = TN / 8 / kWaves;                // those of the weight
+  // Loads are issued kBatch at every kEvery products.  Spread out where the
+  // matrix cores are full (8 waves; 8192^3: 455 us, 467 in two batches), in two
+  // batches where the wave's own instructions count (4 waves: 39, 41 us).
+  constexpr int kBatch = kWaves == 8 ? 1 : kWLoads, kEvery = kWaves == 8 ? 2 : 1;
   constexpr int kBuf = kRows * kScaleBlock;
   constexpr int kScaleLoads = (TT * kSteps / 64 + kWaves - 1) / kWaves;
   constexpr int kScaleBuf = TT * kSteps * 4;
@@ -272,7 +296,7 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, grp = lane >> 4;
   const int wn = wave / WT, wt = wave % WT;
-  const int KB = (K + kScaleBlock - 1) / kScaleBlock;
+  const int KB = (K + kScaleBlock - 1) / kScaleBlock, whole = K / kScaleBlock;
 
   // The tile whose blocks are being loaded.
   const uint8_t* wbase;
@@ -303,16 +327,19 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
                             : min(row - TN, mlast) * static_cast<uint32_t>(K) + piece_a;
     }
   };
-  // Loads from .. to - 1 of block kb, if there is one, to a buffer.
-  auto issue = [&](int kb, int end, int buf, int from, int to) {
-    const uint32_t dst = smem0 + buf;
-    // beyond a short last block: any byte of the row, masked later
-    const uint32_t back_w = kb * kScaleBlock + piece_w >= K ? piece_w : 0;
-    const uint32_t back_a = kb * kScaleBlock + piece_a >= K ? piece_a : 0;
+  // kBatch loads of block kb, if there is one, to a buffer.
+  auto issue = [&](int kb, int end, int buf, int i) {
+    load_lds16_if<kBatch, kWaves * 8 * kScaleBlock>(kb, end, smem0 + buf + (i * kWaves + wave) * 8 * kScaleBlock,
+                                                    voff + i, (i < kWLoads ? wbase : abase) + kb * kScaleBlock);
+  };
+  // Before a short last block is loaded: pieces beyond it are any others of the row, masked later.
+  auto set_short = [&] {
+    const int left = K - (KB - 1) * kScaleBlock;
 #pragma unroll
-    for (int i = from; i < to; ++i)
-      load_lds16_if(kb, end, dst + (i * kWaves + wave) * 8 * kScaleBlock, voff[i] - (i < kWLoads ? back_w : back_a),
-                    (i < kWLoads ? wbase : abase) + kb * kScaleBlock);
+    for (int i = 0; i < kLoads; ++i) {
+      const int piece = i < kWLoads ? piece_w : piece_a;
+      voff[i] -= piece >= left ? piece : 0;
+    }
   };
   // The scales go to LDS for kSteps blocks at a time, [token][block]: a
   // token's scales are one run of memory, so a load of 8 tokens touches 8
@@ -322,8 +349,9 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
 #pragma unroll
     for (int i = 0; i < kScaleLoads; ++i) {
       const int r0 = (i * kWaves + wave) * (64 / kSteps);
-      if (TT * kSteps % (64 * kWaves) == 0 || r0 < TT) load_lds4(smem0 + 2 * kBuf + half * kScaleBuf + r0 * (kSteps * 4), (min(r0 + lane / kSteps, mlast) * KB + kb) * 4u,
-                sabase);
+      if (TT * kSteps % (64 * kWaves) == 0 || r0 < TT)
+        load_lds4(smem0 + 2 * kBuf + half * kScaleBuf + r0 * (kSteps * 4),
+                  (min(r0 + lane / kSteps, mlast) * KB + kb) * 4u, sabase);
     }
     if (wave == 0)
       load_lds4(smem0 + 2 * kBuf + 2 * kScaleBuf + half * 256, (min(lane / kSteps, wrows) * KB + kb) * 4u, swbase);
@@ -371,7 +399,6 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   // fences keep this order: left alone, the compiler puts each addition right
   // behind its product.
   constexpr int kLag = TTW < 4 ? 1 : 3, kUnits = NT * TTW;
-  constexpr int kEvery = 1, kBatch = 1;   // loads are issued kBatch at every kEvery products
   static_assert(NT % 2 == 0 && kUnits % (kLag + 1) == 0 && kLag <= TTW, "register slots repeat from turn to turn");
   i32x8 wf[2], af[TTW];
   f32x4 acc[NT][TTW], p[kLag + 1];
@@ -386,7 +413,10 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   auto turn = [&](int kb, int next, int end, auto is_short) {
     constexpr bool kShort = decltype(is_short)::value;
     wait_all_barrier();
-    if (next % kSteps == 0 && next < end) issue_scales(next / kSteps, half ^ 1);
+    if (next < end) {
+      if (next % kSteps == 0) issue_scales(next / kSteps, half ^ 1);
+      if (next == whole) set_short();
+    }
     const int at = half * (TT * kSteps) + kb % kSteps;
     wf[0] = frag_w(buf, 0);
     const float sb = swl[half * 64 + kb % kSteps];
@@ -400,8 +430,7 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
         wf[(j + 1) & 1] = frag_w(buf, j + 1);
       }
       if (kShort && u >= TTW && u < 2 * TTW) af[t] = masked(af[t]);
-      if (u % kEvery == 0 && u / kEvery * kBatch < kLoads)
-        issue(next, end, kBuf - buf, u / kEvery * kBatch, min(u / kEvery * kBatch + kBatch, kLoads));
+      if (u % kEvery == 0 && u / kEvery * kBatch < kLoads) issue(next, end, kBuf - buf, u / kEvery * kBatch);
       __builtin_amdgcn_sched_barrier(0);
       p[i % (kLag + 1)] = mfma_block<OUT_BF16>(wf[j & 1], af[t]);
       __builtin_amdgcn_sched_barrier(0);
@@ -421,7 +450,9 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   if (count <= 0) return;
   int2 tile = order.at(blockIdx.x, 0);
   set_tile(tile);
-  issue(0, 1, 0, 0, kLoads);
+  if (whole == 0) set_short();
+#pragma unroll
+  for (int i = 0; i < kLoads; i += kBatch) issue(0, 1, 0, i);
   issue_scales(0, 0);
   for (int it = 0; it < count; ++it) {
     const int2 here = tile;
@@ -438,7 +469,6 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
 #pragma unroll
       for (int t = 0; t < TTW; ++t) acc[j][t] = zero4();
 
-    const int whole = K / kScaleBlock;
     const int more = it + 1 < count;   // another tile: its first block is loaded during this one's last
     for (int kb = 0; kb < whole; ++kb) {
       const bool last = kb + 1 == KB;
