@@ -189,7 +189,8 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
 // (128 channels) of the tile's rows goes to LDS straight from memory, 16 bytes
 // a lane, one block ahead of the products in the other of two buffers, also
 // from a tile's last block to the next one's first; one barrier per block
-// hands over the buffers.
+// hands over the buffers.  With SPLIT > 1, each of as many groups of WN x WT
+// waves takes an equal part of K, and their sums are joined at the tile's end.
 //
 // A row's eight 16-byte pieces are stored in the order piece ^ key, with a key
 // of 0 .. 7 from the row's index, which spreads the 16 rows that a product's
@@ -239,6 +240,9 @@ __device__ __forceinline__ void wait_all_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// This wave's LDS accesses are done; then every wave's.
+__device__ __forceinline__ void wait_lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 constexpr int kSteps = 8;   // scale blocks whose scales are loaded together
 
 // LDS of a tile: two buffers of operand rows, of token scales and of weight scales.
@@ -271,8 +275,8 @@ struct TileOrder {
   }
 };
 
-template <int TN, int TT, int WN, int WT, bool OUT_BF16>
-__global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8_matmul_tile_kernel(
+template <int TN, int TT, int WN, int WT, int SPLIT, bool OUT_BF16>
+__global__ __launch_bounds__(64 * WN * WT * SPLIT, tile_waves(TN, TT, WN * WT)) void fp8_matmul_tile_kernel(
     int64_t M, int N, int K, TileOrder order, const uint8_t* __restrict__ a, const float* __restrict__ sa,
     const uint8_t* __restrict__ w, const float* __restrict__ sw, void* __restrict__ y) {
   constexpr int kWaves = WN * WT;
@@ -289,14 +293,18 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   constexpr int kScaleBuf = TT * kSteps * 4;
   static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0 && kWaves % 2 == 0, "whole loads");
   static_assert(TN / WN <= kScaleBlock && kScaleBlock % (TN / WN) == 0 && (TN + kScaleBlock - 1) / kScaleBlock <= 64 / kSteps, "scales");
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  const uint32_t smem0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)smem));
-
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem_all[];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave_id / kWaves, wave = wave_id % kWaves;   // part of K
   const int l16 = lane & 15, grp = lane >> 4;
   const int wn = wave / WT, wt = wave % WT;
-  const int KB = (K + kScaleBlock - 1) / kScaleBlock, whole = K / kScaleBlock;
+  // The scale blocks of a row, of this part, and its whole ones (with SPLIT > 1 all are).
+  const int row_blocks = (K + kScaleBlock - 1) / kScaleBlock, KB = row_blocks / SPLIT;
+  const int whole = SPLIT > 1 ? KB : K / kScaleBlock;
+
+  uint8_t* const smem = smem_all + part * tile_lds(TN, TT);
+  const uint32_t smem0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)smem));
 
   // The tile whose blocks are being loaded.
   const uint8_t* wbase;
@@ -312,11 +320,11 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   auto set_tile = [&](int2 t) {
     const int n0 = t.x * TN;
     const int64_t m0 = static_cast<int64_t>(t.y) * TT;
-    wbase = w + static_cast<size_t>(n0) * K;
-    abase = a + static_cast<size_t>(m0) * K;
-    sabase = sa + static_cast<size_t>(m0) * KB;
+    wbase = w + static_cast<size_t>(n0) * K + part * KB * kScaleBlock;
+    abase = a + static_cast<size_t>(m0) * K + part * KB * kScaleBlock;
+    sabase = sa + static_cast<size_t>(m0) * row_blocks + part * KB;
     const int wrow0 = n0 / kScaleBlock;
-    swbase = sw + static_cast<size_t>(wrow0) * KB;
+    swbase = sw + static_cast<size_t>(wrow0) * row_blocks + part * KB;
     wrows = (N - 1) / kScaleBlock - wrow0;
     const int nlast = min(TN, N - n0) - 1;
     mlast = static_cast<int>(M - m0 < TT ? M - m0 : TT) - 1;
@@ -351,10 +359,10 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
       const int r0 = (i * kWaves + wave) * (64 / kSteps);
       if (TT * kSteps % (64 * kWaves) == 0 || r0 < TT)
         load_lds4(smem0 + 2 * kBuf + half * kScaleBuf + r0 * (kSteps * 4),
-                  (min(r0 + lane / kSteps, mlast) * KB + kb) * 4u, sabase);
+                  (min(r0 + lane / kSteps, mlast) * row_blocks + kb) * 4u, sabase);
     }
     if (wave == 0)
-      load_lds4(smem0 + 2 * kBuf + 2 * kScaleBuf + half * 256, (min(lane / kSteps, wrows) * KB + kb) * 4u, swbase);
+      load_lds4(smem0 + 2 * kBuf + 2 * kScaleBuf + half * 256, (min(lane / kSteps, wrows) * row_blocks + kb) * 4u, swbase);
   };
 
   // Operand reads: 16 rows, pieces grp and grp + 4 of the block.  Two groups
@@ -488,6 +496,34 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
 #pragma unroll
     for (int i = kUnits - kLag; i < kUnits; ++i) add(i, s);
 
+    if constexpr (SPLIT > 1) {
+      // The parts' sums are joined, in their order, in the buffers of the
+      // block just done (the others may be filling with the next tile's first).
+      constexpr int kChunk = kUnits * 4 * 64 * 4;   // a wave's sums
+      static_assert(kBuf % kChunk == 0 && (SPLIT - 1) * kWaves * kChunk <= SPLIT * kBuf, "room for all parts but one");
+      auto chunk = [&](int c) {
+        return reinterpret_cast<float*>(smem_all + c / (kBuf / kChunk) * tile_lds(TN, TT) + (kBuf - buf) +
+                                        c % (kBuf / kChunk) * kChunk) + lane;
+      };
+      wait_lds_barrier();
+      if (part) {
+        float* to = chunk((part - 1) * kWaves + wave);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[(i * 4 + e) * 64] = acc[i / TTW][i % TTW][e];
+      }
+      wait_lds_barrier();
+      if (part) continue;
+#pragma unroll
+      for (int k = 0; k < SPLIT - 1; ++k) {
+        const float* from = chunk(k * kWaves + wave);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i / TTW][i % TTW][e] += from[(i * 4 + e) * 64];
+      }
+    }
     const int n0 = here.x * TN + nw + 8 * grp;
 #pragma unroll
     for (int t = 0; t < TTW; ++t) {
@@ -501,11 +537,11 @@ __global__ __launch_bounds__(64 * WN * WT, tile_waves(TN, TT, WN * WT)) void fp8
   }
 }
 
-template <int TN, int TT, int WN, int WT, bool OUT_BF16>
+template <int TN, int TT, int WN, int WT, int SPLIT, bool OUT_BF16>
 static hipError_t launch_tiles(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                                const float* sw, void* y, int ncu, hipStream_t st) {
-  const auto kernel = fp8_matmul_tile_kernel<TN, TT, WN, WT, OUT_BF16>;
-  constexpr int kLds = tile_lds(TN, TT);
+  const auto kernel = fp8_matmul_tile_kernel<TN, TT, WN, WT, SPLIT, OUT_BF16>;
+  constexpr int kLds = SPLIT * tile_lds(TN, TT);
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
@@ -514,10 +550,10 @@ static hipError_t launch_tiles(int64_t M, int N, int K, const uint8_t* a, const 
   order.t_tiles = static_cast<int>((M + TT - 1) / TT);
   const int64_t tiles = static_cast<int64_t>(order.n_tiles) * order.t_tiles;
   if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
-  const int slots = ncu * tile_groups(TN, TT, WN * WT);
+  const int slots = ncu * tile_groups(TN, TT, WN * WT) / SPLIT;
   order.turn = static_cast<int>(tiles < slots ? tiles : slots);
   order.per = order.turn % 8 == 0 ? static_cast<int>((tiles + 7) / 8) : 0;
-  kernel<<<dim3(order.turn), 64 * WN * WT, kLds, st>>>(M, N, K, order, a, sa, w, sw, y);
+  kernel<<<dim3(order.turn), 64 * WN * WT * SPLIT, kLds, st>>>(M, N, K, order, a, sa, w, sw, y);
   return hipGetLastError();
 }
 
@@ -529,22 +565,30 @@ static hipError_t launch_rows(int64_t M, int N, int K, const uint8_t* a, const f
   return hipGetLastError();
 }
 
-// Time of a pass over `tiles` tiles, of which `groups` run on a CU at a time:
-// `full` for a full load of the card, `one` for at most one a CU.
-static int64_t tiles_cost(int64_t tiles, int ncu, int groups, int full, int one) {
-  const int64_t slots = static_cast<int64_t>(ncu) * groups, left = tiles % slots;
-  return tiles / slots * full + (left == 0 ? 0 : left <= ncu ? one : full);
-}
+// The kernel by the sizes.
+//
+// Few tokens take the rows kernel (us at N = K = 4096 in bf16: 16 tokens 7.0,
+// 32 8.7, 64 11.7, 128 14.9; 64 x 64 tiles with K in four parts 12 to 12.5),
+// as long as it has no more than a workgroup a CU for 32 x 32 of the result
+// (64 tokens, 8192 outputs: 15.0, tiles 13.2), and up to 128 tokens where K
+// cannot be split.
+//
+// The others take the tile of the least cost by the measured time of a load of
+// the card at K = 4096: `full` of what runs at a time, `one` of at most a
+// workgroup a CU.  The parts of K pay where the tiles are few (256 tokens,
+// 4096 outputs: 13.0 in four parts, 14.2 in two, 19.3 whole; 1024 tokens in
+// 128 x 128 tiles: 24.0 in two, 27.5 whole) and cost where they are many (2048
+// tokens: 41, 37).  fp32 outputs have no 256 x 256 tile: with its operands
+// widened in registers 128 x 256 took as long as 128 x 128 (1077, 1118 us for
+// 32768 tokens).
+struct TileChoice {
+  int tile, split, full, one;
+};
+constexpr TileChoice kChoicesBf16[] = {{256, 1, 610, 480}, {128, 1, 380, 250}, {128, 2, 240, 210},
+                                       {64, 1, 290, 195},  {64, 2, 186, 140},  {64, 4, 130, 130}};
+constexpr TileChoice kChoicesFp32[] = {{128, 1, 720, 470}, {128, 2, 450, 375}, {64, 1, 530, 270},
+                                       {64, 2, 300, 195},  {64, 4, 185, 185}};
 
-// The kernel by the sizes.  us at N = K = 4096, bf16 out, for 16 / 32 / 64 /
-// 128 / 256 / 512 / 1024 / 2048 / 32768 tokens: rows 7.0 / 8.5 / 11.4 / 15.2 /
-// 21, tiles of 64 x 64 20 up to 256 tokens, then 23 / 32 / 59 / 1000, of 128 x
-// 128 25 up to 512, then 28 / 40 / 640, of 256 x 256 47 to 50, then 500.  So
-// few tokens take the rows kernel, unless there are outputs enough to fill
-// half the card with 64 x 64 tiles (64 tokens, 16416 outputs: 28, rows 38),
-// and the others the tile of the least cost, by the measured time of a load
-// of the card.  fp32 outputs have no 256 x 256 tile: with its operands widened
-// in registers 128 x 256 took as long as 128 x 128 (1077, 1118 us).
 template <bool OUT_BF16>
 static hipError_t launch_fp8_matmul_to(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                                        const float* sw, void* y, hipStream_t st) {
@@ -552,22 +596,42 @@ static hipError_t launch_fp8_matmul_to(int64_t M, int N, int K, const uint8_t* a
   int ncu = 0;
   const hipError_t e = device_cus(&ncu);
   if (e != hipSuccess) return e;
-  const auto tiles = [&](int64_t of) { return (M + of - 1) / of * ((N + of - 1) / of); };
-  if (M <= 128 && 2 * tiles(64) <= ncu) {   // the most reuse that still gives every CU a workgroup
-    const auto groups = [&](int64_t outs, int64_t toks) { return (N + outs - 1) / outs * ((M + toks - 1) / toks); };
+  // equal parts of K, of four blocks or more
+  const auto splits = [&](int parts) { return K % (kScaleBlock * parts) == 0 && K / kScaleBlock >= 4 * parts; };
+  const auto groups = [&](int64_t outs, int64_t toks) { return (N + outs - 1) / outs * ((M + toks - 1) / toks); };
+  if ((M <= 64 && groups(32, 32) <= ncu) || (M <= 128 && 2 * groups(64, 64) <= ncu && !splits(4))) {
+    // the most reuse that still gives every CU a workgroup
     if (groups(64, 32) >= ncu) return launch_rows<4, 2, 8, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
     if (groups(32, 32) >= ncu) return launch_rows<2, 2, 8, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
     if (groups(32, 16) >= ncu) return launch_rows<2, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
     return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
   }
-  const int64_t c64 = tiles_cost(tiles(64), ncu, tile_groups(64, 64, 4), OUT_BF16 ? 29 : 51, OUT_BF16 ? 20 : 29);
-  const int64_t c128 = tiles_cost(tiles(128), ncu, tile_groups(128, 128, 4), OUT_BF16 ? 40 : 71, OUT_BF16 ? 26 : 45);
+  int64_t least = INT64_MAX;
+  TileChoice best{};
+  const auto weigh = [&](const TileChoice& c) {
+    if (c.split > 1 && !splits(c.split)) return;
+    const int side = c.tile == 256 ? 8 : 4;   // waves of a part
+    const int64_t tiles = groups(c.tile, c.tile);
+    const int64_t slots = static_cast<int64_t>(ncu) * tile_groups(c.tile, c.tile, side) / c.split, left = tiles % slots;
+    const int64_t cost = tiles / slots * c.full + (left == 0 ? 0 : left <= ncu ? c.one : c.full);
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  };
   if constexpr (OUT_BF16) {
-    const int64_t c256 = tiles_cost(tiles(256), ncu, tile_groups(256, 256, 8), 62, 50);
-    if (c256 <= c64 && c256 <= c128) return launch_tiles<256, 256, 2, 4, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+    for (const TileChoice& c : kChoicesBf16) weigh(c);
+    if (best.tile == 256) return launch_tiles<256, 256, 2, 4, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+  } else {
+    for (const TileChoice& c : kChoicesFp32) weigh(c);
   }
-  if (c64 < c128) return launch_tiles<64, 64, 2, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
-  return launch_tiles<128, 128, 2, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+  if (best.tile == 128) {
+    if (best.split == 2) return launch_tiles<128, 128, 2, 2, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+    return launch_tiles<128, 128, 2, 2, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+  }
+  if (best.split == 4) return launch_tiles<64, 64, 2, 2, 4, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+  if (best.split == 2) return launch_tiles<64, 64, 2, 2, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+  return launch_tiles<64, 64, 2, 2, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
 }
 
 hipError_t launch_fp8_matmul(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,

@@ -237,7 +237,8 @@ def fp8_operands(r, M, N, K):
 PRODUCTS = [(1, 1, 16), (1, 17, 48), (1, 4096, 4096), (2, 130, 128), (16, 64, 112), (17, 33, 144), (33, 129, 2032),
             (64, 256, 256), (65, 320, 1024), (100, 1000, 400), (128, 128, 128), (129, 257, 384), (250, 515, 4096),
             (256, 256, 4096), (257, 300, 272), (300, 16416, 128), (511, 512, 528), (1000, 1002, 1008),
-            (2049, 260, 640), (4100, 1028, 1040), (5000, 4200, 272), (4500, 4400, 1168), (70000, 264, 128)]
+            (2049, 260, 640), (4100, 1028, 1040), (5000, 4200, 272), (4500, 4400, 1168), (70000, 264, 128),
+            (80, 520, 2048), (200, 1000, 1024), (300, 4100, 2048), (700, 3000, 2560), (900, 4200, 1024), (1300, 3500, 1536)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
