@@ -508,8 +508,13 @@ kda_status_t kda_output_gate_backward(const kda_config_t *cfg, int64_t n_tokens,
  * K is a multiple of 16; K, N up to 2^20, M below 2^31 (else
  * KDA_ERR_UNSUPPORTED).  M == 0 is a no-op; M == 1 is the single-token form.
  * A NaN scale or value reaches the outputs of its row (of its 128 columns for
- * a w_scale).  Only out_dtype and stage_events of cfg are used.  Needs no
- * workspace.  The same inputs give the same bits on every run.
+ * a w_scale).  Nothing aliases.  Only out_dtype and stage_events of cfg are
+ * used.  Needs no workspace.  The same inputs give the same bits on every run.
+ *
+ * The products of a scale block are exact and summed by the matrix cores.  For
+ * fp32 y in fp32.  For bf16 y in their e4m3 form, which cuts each product at
+ * 2^-13 of the block's largest: about 1.3e-5 of the result's norm, against
+ * 1.7e-3 of the rounding to bf16.
  */
 kda_status_t kda_fp8_matmul(const kda_config_t *cfg, int64_t M, int32_t N, int32_t K,
                             const void *a, const float *a_scale,

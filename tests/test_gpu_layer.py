@@ -282,6 +282,7 @@ def everything(kda, r, stream=None):
     x, res, w = r(n, H * d, dtype=BF), r(n, H * d, dtype=BF), r.weight(H * d)
     o, gate, ow, dy = r(n, H, d, dtype=BF), r(n, H, d, dtype=BF), r.weight(d), r(n, H, d, dtype=BF)
     wq, sw = ref.quantise_weight(r(200, H * d))
+    tiles = [fp8_operands(r, 300, 520, 1024), fp8_operands(r, 1100, 1000, 512), fp8_operands(r, 4500, 4400, 272)]
     torch.cuda.synchronize()
 
     def call():
@@ -291,7 +292,8 @@ def everything(kda, r, stream=None):
         p2 = kda.kda_fp8_matmul(cfg, z, zs, wq, sw, stream=stream)
         yb, _ = kda.kda_add_rmsnorm(cfg, x, res, w, stream=stream)
         grads = kda.kda_output_gate_backward(cfg, o, gate, ow, dy, stream=stream)
-        return (y, ys, h, p, z, zs, p2, yb, *grads,
+        products = [kda.kda_fp8_matmul(cfg, *t, stream=stream) for t in tiles]
+        return (y, ys, h, p, z, zs, p2, yb, *grads, *products,
                 *kda.kda_add_rmsnorm_backward(cfg, h, w, dy.view(n, H * d), stream=stream))
     return call
 
