@@ -438,20 +438,23 @@ def kda_output_gate(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, *, y
 # They are called once a token and layer, so the binding's own time counts: it
 # does each step once (a kernel launch is ~4 us, the binding 3 to 6).
 
-def _run(device, stream, call):
-    """call(stream handle) with the tensors' device current, on `stream` or on
-    that device's current stream, which is also where `call` allocates."""
+def _on_stream(device, stream, again):
+    """again() with the tensors' device current, and `stream` if there is one:
+    what it allocates and launches is that stream's."""
     if device.type != "cuda":
         raise ValueError("tensors must be on the GPU")
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("the stream belongs to another device than the tensors")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if device.index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(device.index))
-    with torch.cuda.device(device):
-        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is None:
+        with torch.cuda.device(device):
+            return again()
+    if stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    with torch.cuda.stream(stream):
+        return again()
+
+
+def _elsewhere(device, stream):
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or device.type != "cuda" or device.index != torch.cuda.current_device()
 
 
 def _at(name, t, shape, dtype, device):
@@ -501,15 +504,15 @@ def kda_add_rmsnorm(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=No
     xp, rp = _at("x", x, shape, cfg.io_dtype, dev), _at("residual", residual, shape, cfg.io_dtype, dev)
     wp = _at("weight", weight, (hidden,), torch.float32, dev)
     hp, yp = _at("h", h, shape, cfg.io_dtype, dev), _at("y", y, shape, cfg.out_dtype, dev)
-
-    def call(st):
-        h_ = torch.empty_like(x) if h is None and residual is not None else h
-        y_ = torch.empty_like(x, dtype=cfg.out_dtype) if y is None else y
-        _check(_lib.kda_add_rmsnorm(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
-                                    hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(), st),
-               "kda_add_rmsnorm")
-        return y_, x if h_ is None else h_
-    return _run(dev, stream, call)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_add_rmsnorm(cfg, x, residual, weight, eps, h=h, y=y))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    h_ = torch.empty_like(x) if h is None and residual is not None else h
+    y_ = torch.empty_like(x, dtype=cfg.out_dtype) if y is None else y
+    _check(_lib.kda_add_rmsnorm(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
+                                hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(), st),
+           "kda_add_rmsnorm")
+    return y_, x if h_ is None else h_
 
 
 def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=None, y=None, y_scale=None,
@@ -523,16 +526,17 @@ def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, 
     wp = _at("weight", weight, (hidden,), torch.float32, dev)
     hp, yp = _at("h", h, shape, cfg.io_dtype, dev), _at("y", y, shape, torch.float8_e4m3fn, dev)
     sp = _at("y_scale", y_scale, blocks, torch.float32, dev)
-
-    def call(st):
-        h_ = torch.empty_like(x) if h is None and residual is not None else h
-        y_ = torch.empty_like(x, dtype=torch.float8_e4m3fn) if y is None else y
-        s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
-        _check(_lib.kda_add_rmsnorm_fp8(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
-                                        hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(),
-                                        sp if s_ is y_scale else s_.data_ptr(), st), "kda_add_rmsnorm_fp8")
-        return y_, s_, x if h_ is None else h_
-    return _run(dev, stream, call)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_add_rmsnorm_fp8(cfg, x, residual, weight, eps, h=h, y=y,
+                                                                    y_scale=y_scale))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    h_ = torch.empty_like(x) if h is None and residual is not None else h
+    y_ = torch.empty_like(x, dtype=torch.float8_e4m3fn) if y is None else y
+    s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
+    _check(_lib.kda_add_rmsnorm_fp8(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
+                                    hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(),
+                                    sp if s_ is y_scale else s_.data_ptr(), st), "kda_add_rmsnorm_fp8")
+    return y_, s_, x if h_ is None else h_
 
 
 def kda_add_rmsnorm_backward_workspace_bytes(cfg: Config, n_tokens: int, hidden: int) -> int:
@@ -551,17 +555,18 @@ def kda_add_rmsnorm_backward(cfg: Config, h, weight, dy, d_h=None, eps: float = 
     hp, wp = _at("h", h, shape, cfg.io_dtype, dev), _at("weight", weight, (hidden,), torch.float32, dev)
     dyp, dhp = _at("dy", dy, shape, cfg.out_dtype, dev), _at("d_h", d_h, shape, torch.float32, dev)
     dxp = _at("dx", dx, shape, torch.float32, dev)
-
-    def call(st):
-        dx_ = torch.empty_like(h, dtype=torch.float32) if dx is None else dx
-        dw = torch.empty_like(weight)
-        c = _op_struct(cfg)
-        ws, wsp, size = _workspace_at(_lib.kda_add_rmsnorm_backward_workspace_bytes(c, n, hidden), dev, workspace)
-        _check(_lib.kda_add_rmsnorm_backward(c, n, hidden, hp, wp, eps, dyp, dhp,
-                                             dxp if dx_ is dx else dx_.data_ptr(), dw.data_ptr(), wsp, size, st),
-               "kda_add_rmsnorm_backward")
-        return dx_, dw
-    return _run(dev, stream, call)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_add_rmsnorm_backward(cfg, h, weight, dy, d_h, eps, dx=dx,
+                                                                         workspace=workspace))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    dx_ = torch.empty_like(h, dtype=torch.float32) if dx is None else dx
+    dw = torch.empty_like(weight)
+    c = _op_struct(cfg)
+    ws, wsp, size = _workspace_at(_lib.kda_add_rmsnorm_backward_workspace_bytes(c, n, hidden), dev, workspace)
+    _check(_lib.kda_add_rmsnorm_backward(c, n, hidden, hp, wp, eps, dyp, dhp,
+                                         dxp if dx_ is dx else dx_.data_ptr(), dw.data_ptr(), wsp, size, st),
+           "kda_add_rmsnorm_backward")
+    return dx_, dw
 
 
 def _gate_args(cfg, o, gate, o_norm_weight):
@@ -569,7 +574,7 @@ def _gate_args(cfg, o, gate, o_norm_weight):
     H, dv, dev = cfg.num_heads, cfg.head_v_dim, o.device
     lead = o.shape[:-2]
     full = (*lead, H, dv)
-    return (lead, full, o.numel() // (H * dv), _at("o", o, full, cfg.out_dtype, dev),
+    return (lead, full, o.numel() // max(H * dv, 1), _at("o", o, full, cfg.out_dtype, dev),
             _at("gate", gate, full, cfg.io_dtype, dev), _at("o_norm_weight", o_norm_weight, (dv,), torch.float32, dev))
 
 
@@ -582,15 +587,16 @@ def kda_output_gate_fp8(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, 
     row = cfg.num_heads * cfg.head_v_dim
     rows, blocks = (*lead, row), (*lead, _scale_blocks(row))
     yp, sp = _at("y", y, rows, torch.float8_e4m3fn, dev), _at("y_scale", y_scale, blocks, torch.float32, dev)
-
-    def call(st):
-        y_ = torch.empty(rows, dtype=torch.float8_e4m3fn, device=dev) if y is None else y
-        s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
-        _check(_lib.kda_output_gate_fp8(_op_struct(cfg), n, op, gp, wp, eps,
-                                        yp if y_ is y else y_.data_ptr(), sp if s_ is y_scale else s_.data_ptr(), st),
-               "kda_output_gate_fp8")
-        return y_, s_
-    return _run(dev, stream, call)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_output_gate_fp8(cfg, o, gate, o_norm_weight, eps, y=y,
+                                                                    y_scale=y_scale))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    y_ = torch.empty(rows, dtype=torch.float8_e4m3fn, device=dev) if y is None else y
+    s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
+    _check(_lib.kda_output_gate_fp8(_op_struct(cfg), n, op, gp, wp, eps,
+                                    yp if y_ is y else y_.data_ptr(), sp if s_ is y_scale else s_.data_ptr(), st),
+           "kda_output_gate_fp8")
+    return y_, s_
 
 
 def kda_output_gate_backward_workspace_bytes(cfg: Config, n_tokens: int) -> int:
@@ -605,16 +611,17 @@ def kda_output_gate_backward(cfg: Config, o, gate, o_norm_weight, dy, eps: float
     dev = o.device
     _, full, n, op, gp, wp = _gate_args(cfg, o, gate, o_norm_weight)
     dyp = _at("dy", dy, full, cfg.out_dtype, dev)
-
-    def call(st):
-        d_o, d_gate = torch.empty_like(o), torch.empty_like(gate, dtype=torch.float32)
-        dw = torch.empty_like(o_norm_weight)
-        c = _op_struct(cfg)
-        ws, wsp, size = _workspace_at(_lib.kda_output_gate_backward_workspace_bytes(c, n), dev, workspace)
-        _check(_lib.kda_output_gate_backward(c, n, op, gp, wp, eps, dyp, d_o.data_ptr(), d_gate.data_ptr(),
-                                             dw.data_ptr(), wsp, size, st), "kda_output_gate_backward")
-        return d_o, d_gate, dw
-    return _run(dev, stream, call)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_output_gate_backward(cfg, o, gate, o_norm_weight, dy, eps,
+                                                                         workspace=workspace))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    d_o, d_gate = torch.empty_like(o), torch.empty_like(gate, dtype=torch.float32)
+    dw = torch.empty_like(o_norm_weight)
+    c = _op_struct(cfg)
+    ws, wsp, size = _workspace_at(_lib.kda_output_gate_backward_workspace_bytes(c, n), dev, workspace)
+    _check(_lib.kda_output_gate_backward(c, n, op, gp, wp, eps, dyp, d_o.data_ptr(), d_gate.data_ptr(),
+                                         dw.data_ptr(), wsp, size, st), "kda_output_gate_backward")
+    return d_o, d_gate, dw
 
 
 def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
@@ -628,10 +635,10 @@ def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
     wp, wsp = _at("w", w, (N, K), f8, dev), _at("w_scale", w_scale, (_scale_blocks(N), kb), torch.float32, dev)
     shape = (*lead, N)
     yp = _at("y", y, shape, cfg.out_dtype, dev)
-
-    def call(st):
-        y_ = torch.empty(shape, dtype=cfg.out_dtype, device=dev) if y is None else y
-        _check(_lib.kda_fp8_matmul(_op_struct(cfg), math.prod(lead), N, K, ap, sp, wp, wsp,
-                                   yp if y_ is y else y_.data_ptr(), st), "kda_fp8_matmul")
-        return y_
-    return _run(dev, stream, call)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_fp8_matmul(cfg, a, a_scale, w, w_scale, y=y))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    y_ = torch.empty(shape, dtype=cfg.out_dtype, device=dev) if y is None else y
+    _check(_lib.kda_fp8_matmul(_op_struct(cfg), math.prod(lead), N, K, ap, sp, wp, wsp,
+                               yp if y_ is y else y_.data_ptr(), st), "kda_fp8_matmul")
+    return y_
