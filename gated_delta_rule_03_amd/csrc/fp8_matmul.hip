@@ -258,8 +258,9 @@ constexpr int tile_groups(int TN, int TT, int waves) {
 // The order of the tiles: workgroups go to the 8 XCDs in turn, so each XCD
 // takes a run of neighbouring tiles, and within it groups of kGroup token
 // tiles wide, so that the tiles running at a time share rows in its L2
-// (8192 x 8192 x 8192: 447 us, 526 us row by row).
-constexpr int kGroup = 4;
+// (8192 x 8192 x 8192, us: 526 row by row, 475 two wide, 461 six, 474 sixteen;
+// 32768 x 16416 x 2048: 1081, 1059, 1125).
+constexpr int kGroup = 6;
 struct TileOrder {
   int n_tiles, t_tiles, per, turn;   // per: tiles of an XCD, 0 where they are too few to split; turn: workgroups
   __device__ int count(int wg) const {
