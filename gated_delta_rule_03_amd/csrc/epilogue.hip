@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kEpiThreads) void output_gate_fp8_kernel(int64_t un
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(ov[e], ov[e], ss);
     ss = dpp_group_sum<DV / 8>(ss);
-    float inv = 1.0f / sqrtf(ss * (1.0f / DV) + eps);
+    float inv = rsqrt_precise(ss * (1.0f / DV) + eps);
     // heads narrower than a block have norms of their own inside it, and lanes
     // past the row's end none (with eps = 0 it would be infinite)
     const float each = DV == kScaleBlock ? 1.0f : (mine ? inv : 0.0f);

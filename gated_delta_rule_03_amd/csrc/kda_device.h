@@ -74,6 +74,16 @@ __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcp
 
 __device__ __forceinline__ float sigmoidf_(float x) { return rcp_fast(1.0f + exp_fast(-x)); }
 
+// 1 / sqrt(x): the hardware's (v_rsq_f32, 1 ulp) with a Newton step; the
+// library's square root and division (about 25 instructions against 5) only
+// where x or its root leaves the normal range.
+__device__ __forceinline__ float rsqrt_precise(float x) {
+  float r = __builtin_amdgcn_rsqf(x);
+  r = fmaf(fmaf(-x * r, r, 1.0f), 0.5f * r, r);
+  if (!(x > 1e-30f && x < 1e30f)) r = 1.0f / sqrtf(x);
+  return r;
+}
+
 // log(1 + e^x) without overflow: max(x, 0) + log(1 + e^-|x|), the second
 // term through the hardware base-2 logarithm (v_log_f32).  Its absolute
 // error is ~1e-7, which is all that matters here: the result enters the gate

@@ -112,10 +112,11 @@ constexpr float kAmaxFloor = 1e-30f;    // a block of zeros still has a scale
 
 // The scale of the 128-channel block whose values m * t[e] sit 8 to a lane
 // over an aligned group of 16 lanes (every lane active; lanes past the row's
-// end hold zeros), and those 8 values as e4m3: s = max(amax, 1e-30) / 448 and
-// t * (m / s), rounded to nearest even.  m (the row's 1 / rms, one value in
-// every lane of the group) goes into the scale, not into each value: one
-// rounding less per value.  A NaN in the block makes its scale NaN.
+// end hold zeros), and those 8 values as e4m3, rounded to nearest even:
+// s = max(amax |m t|, 1e-30) / 448, q = t * (448 / amax |t|).  m, the row's
+// 1 / rms (one value in every lane of the group), goes into the scale alone:
+// two roundings less per value than (m t) / s.  A NaN in the block makes its
+// scale NaN.
 __device__ __forceinline__ uint2 quantise_block8(const float (&t)[8], float m, float* scale) {
   uint32_t a = 0;
 #pragma unroll
@@ -123,18 +124,16 @@ __device__ __forceinline__ uint2 quantise_block8(const float (&t)[8], float m, f
     const uint32_t b = __float_as_uint(t[e]) & 0x7fffffffu;
     a = b > a ? b : a;
   }
-  const float amax = __uint_as_float(lane_group_umax16(a)) * m;
-  const float s = (amax <= kAmaxFloor ? kAmaxFloor : amax) / kE4M3Max;
-  // finite, so that a zero times it stays a zero (m / s can pass fp32 where
-  // a block of zeros lies in a row of tiny values)
-  float c = m / s;
-  c = c > 3.4028235e38f ? 3.4028235e38f : c;
+  const float amax = __uint_as_float(lane_group_umax16(a));
+  const bool tiny = amax * m <= kAmaxFloor;
+  *scale = (tiny ? kAmaxFloor : amax * m) * (1.0f / kE4M3Max);
+  // (finite, so that a zero times it stays a zero)
+  const float c = tiny ? fminf(m * (kE4M3Max / kAmaxFloor), 3.4028235e38f) : kE4M3Max / amax;
   int lo = 0, hi = 0;
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0] * c, t[1] * c, lo, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[2] * c, t[3] * c, lo, true);
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[4] * c, t[5] * c, hi, false);
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[6] * c, t[7] * c, hi, true);
-  *scale = s;
   return make_uint2(static_cast<uint32_t>(lo), static_cast<uint32_t>(hi));
 }
 
