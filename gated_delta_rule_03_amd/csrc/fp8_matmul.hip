@@ -243,7 +243,7 @@ __device__ __forceinline__ void wait_all_barrier() {
 // This wave's LDS accesses are done; then every wave's.
 __device__ __forceinline__ void wait_lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-constexpr int kSteps = 8;   // scale blocks whose scales are loaded together
+constexpr int kSteps = 8;   // scale blocks whose scales are loaded together, 8 tokens a load
 
 // LDS of a tile: two buffers of operand rows, of token scales and of weight scales.
 constexpr int tile_lds(int TN, int TT) { return 2 * ((TN + TT) * kScaleBlock + TT * kSteps * 4 + 256); }
@@ -350,20 +350,23 @@ __global__ __launch_bounds__(64 * WN * WT * SPLIT, tile_waves(TN, TT, WN * WT)) 
       voff[i] -= piece >= left ? piece : 0;
     }
   };
-  // The scales go to LDS for kSteps blocks at a time, [token][block]: a
-  // token's scales are one run of memory, so a load of 8 tokens touches 8
-  // lines where a load per block would touch one for each token.
+  // The scales go to LDS for kSteps = 8 blocks at a time: a token's scales are
+  // one run of memory, so a load of 8 tokens touches 8 lines where a load per
+  // block would touch one for each token.  Each load's 64 values lie
+  // [block][token], the blocks of every other load turned by one, so that the
+  // 16 tokens of a read are in different banks.
   auto issue_scales = [&](int chunk, int half) {
-    const int kb = min(chunk * kSteps + lane % kSteps, KB - 1);
+    const int turned = min(chunk * kSteps + ((lane / 8 - (wave & 1)) & 7), KB - 1);
 #pragma unroll
     for (int i = 0; i < kScaleLoads; ++i) {
       const int r0 = (i * kWaves + wave) * (64 / kSteps);
       if (TT * kSteps % (64 * kWaves) == 0 || r0 < TT)
         load_lds4(smem0 + 2 * kBuf + half * kScaleBuf + r0 * (kSteps * 4),
-                  (min(r0 + lane / kSteps, mlast) * row_blocks + kb) * 4u, sabase);
+                  (min(r0 + lane % 8, mlast) * row_blocks + turned) * 4u, sabase);
     }
-    if (wave == 0)
-      load_lds4(smem0 + 2 * kBuf + 2 * kScaleBuf + half * 256, (min(lane / kSteps, wrows) * row_blocks + kb) * 4u, swbase);
+    if (wave == 0)   // [row of blocks][block]
+      load_lds4(smem0 + 2 * kBuf + 2 * kScaleBuf + half * 256,
+                (min(lane / kSteps, wrows) * row_blocks + min(chunk * kSteps + lane % kSteps, KB - 1)) * 4u, swbase);
   };
 
   // Operand reads: 16 rows, pieces grp and grp + 4 of the block.  Two groups
@@ -381,7 +384,7 @@ __global__ __launch_bounds__(64 * WN * WT * SPLIT, tile_waves(TN, TT, WN * WT)) 
   const uint8_t* ar = smem + (TN + wt * (TT / WT) + l16) * kScaleBlock;
   auto frag_w = [&](int buf, int j) { return frag(wr + buf + (32 * (j >> 1) + 4 * (j & 1)) * kScaleBlock); };
   auto frag_a = [&](int buf, int t) { return frag(ar + buf + 16 * t * kScaleBlock); };
-  const float* sal = reinterpret_cast<const float*>(smem + 2 * kBuf) + (wt * (TT / WT) + l16) * kSteps;
+  const float* sal = reinterpret_cast<const float*>(smem + 2 * kBuf) + wt * (TT / WT) * kSteps + (l16 >> 3) * 64 + (l16 & 7);
   const float* swl = reinterpret_cast<const float*>(smem + 2 * kBuf + 2 * kScaleBuf) + nw / kScaleBlock * kSteps;
   // pieces past K of the last block hold other channels: zeros on both sides
   auto masked = [&](i32x8 f) {
@@ -407,7 +410,8 @@ __global__ __launch_bounds__(64 * WN * WT * SPLIT, tile_waves(TN, TT, WN * WT)) 
   // waits for the other; the last three of a turn fall into the next one.  The
   // fences keep this order: left alone, the compiler puts each addition right
   // behind its product.
-  constexpr int kLag = TTW < 4 ? 1 : 3, kUnits = NT * TTW;
+  // (kLag 3 where the SIMD has one wave of the workgroup, 1 where two take turns.)
+  constexpr int kLag = TTW < 4 || kWaves == 8 || !OUT_BF16 ? 1 : 3, kUnits = NT * TTW;
   static_assert(NT % 2 == 0 && kUnits % (kLag + 1) == 0 && kLag <= TTW, "register slots repeat from turn to turn");
   i32x8 wf[2], af[TTW];
   f32x4 acc[NT][TTW], p[kLag + 1];
@@ -426,7 +430,7 @@ __global__ __launch_bounds__(64 * WN * WT * SPLIT, tile_waves(TN, TT, WN * WT)) 
       if (next % kSteps == 0) issue_scales(next / kSteps, half ^ 1);
       if (next == whole) set_short();
     }
-    const int at = half * (TT * kSteps) + kb % kSteps;
+    const int at = half * (TT * kSteps) + ((kb + (l16 >> 3)) & 7) * 8;
     wf[0] = frag_w(buf, 0);
     const float sb = swl[half * 64 + kb % kSteps];
 #pragma unroll
