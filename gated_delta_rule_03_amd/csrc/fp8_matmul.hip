@@ -89,7 +89,9 @@ __device__ __forceinline__ void store_out8(void* y, size_t row, int n, int N, co
 // The kernel for few tokens: 16 J outputs x 16 T tokens a workgroup, the
 // operands straight from memory to registers.  Its waves share the scale
 // blocks, each with U blocks' loads in flight, and join their sums in LDS in
-// a fixed order.
+// a fixed order.  It is bound by the weight's bytes and, as the call is short,
+// by the launch and one trip to memory: 1 x 4096 x 4096 takes 5.2 us, 3.2
+// TB/s, where a large copy's rate would take 3.5.
 template <int J, int T, int WAVES, int U, bool OUT_BF16>
 __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
     int64_t M, int N, int K, const uint8_t* __restrict__ a, const float* __restrict__ sa,
@@ -192,6 +194,12 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
 // hands over the buffers.  With SPLIT > 1, each of as many groups of WN x WT
 // waves takes an equal part of K, and their sums are joined at the tile's end.
 //
+// The 256 x 256 tile (8 waves, one workgroup a CU) runs 32768 x 4096 x 4096 in
+// 455 to 490 us, 2.24 to 2.4 PFLOP/s, and 128 x 128 tiles in 610; the library's
+// product without block scales takes 389 to 427.  Both are bound by the clock
+// that the card's power leaves on such operands (on zeros they take 362 and
+// 256), and this one by the four scaled additions a lane of each product.
+//
 // A row's eight 16-byte pieces are stored in the order piece ^ key, with a key
 // of 0 .. 7 from the row's index, which spreads the 16 rows that a product's
 // operand read touches over all banks; the loads read the same 128-byte lines
@@ -258,8 +266,8 @@ constexpr int tile_groups(int TN, int TT, int waves) {
 // The order of the tiles: workgroups go to the 8 XCDs in turn, so each XCD
 // takes a run of neighbouring tiles, and within it groups of kGroup token
 // tiles wide, so that the tiles running at a time share rows in its L2
-// (8192 x 8192 x 8192, us: 526 row by row, 475 two wide, 461 six, 474 sixteen;
-// 32768 x 16416 x 2048: 1081, 1059, 1125).
+// (8192 x 8192 x 8192, us: 530 row by row, 485 two wide, 470 six, 489 sixteen;
+// 32768 x 16416 x 2048: 1205, 1102, 1089, 1171).
 constexpr int kGroup = 6;
 struct TileOrder {
   int n_tiles, t_tiles, per, turn;   // per: tiles of an XCD, 0 where they are too few to split; turn: workgroups
@@ -286,8 +294,9 @@ __global__ __launch_bounds__(64 * WN * WT * SPLIT, tile_waves(TN, TT, WN * WT)) 
   constexpr int kLoads = kRows / 8 / kWaves;              // 8 rows of 128 bytes a load
   constexpr int kWLoads = TN / 8 / kWaves;                // those of the weight
   // Loads are issued kBatch at every kEvery products.  Spread out where the
-  // matrix cores are full (8 waves; 8192^3: 455 us, 467 in two batches), in two
-  // batches where the wave's own instructions count (4 waves: 39, 41 us).
+  // matrix cores are full (8 waves; 8192^3: 470 us, 505 in two batches), in two
+  // batches where the wave's own instructions count (4 waves, 250 x 16416 x
+  // 4096: 39, spread out 44).
   constexpr int kBatch = kWaves == 8 ? 1 : kWLoads, kEvery = kWaves == 8 ? 2 : 1;
   constexpr int kBuf = kRows * kScaleBlock;
   constexpr int kScaleLoads = (TT * kSteps / 64 + kWaves - 1) / kWaves;
@@ -406,11 +415,12 @@ __global__ __launch_bounds__(64 * WN * WT * SPLIT, tile_waves(TN, TT, WN * WT)) 
   // block kb - 1, whose buffer the loads of the next block take, and the loads
   // of block kb have landed.  (A tile's first turn has a leftover of zeros.)
   //
-  // A product's scaled addition follows three products later, so neither
-  // waits for the other; the last three of a turn fall into the next one.  The
-  // fences keep this order: left alone, the compiler puts each addition right
-  // behind its product.
-  // (kLag 3 where the SIMD has one wave of the workgroup, 1 where two take turns.)
+  // A product's scaled addition follows kLag products later, so neither waits
+  // for the other; the last ones of a turn fall into the next one.  The fences
+  // keep this order: left alone, the compiler puts each addition right behind
+  // its product.  One product is enough where two waves of the workgroup share
+  // a SIMD (32768 x 4096 x 4096, us: 489, with three 497) and where a product
+  // is four steps (fp32 outputs).
   constexpr int kLag = TTW < 4 || kWaves == 8 || !OUT_BF16 ? 1 : 3, kUnits = NT * TTW;
   static_assert(NT % 2 == 0 && kUnits % (kLag + 1) == 0 && kLag <= TTW, "register slots repeat from turn to turn");
   i32x8 wf[2], af[TTW];
@@ -573,17 +583,17 @@ static hipError_t launch_rows(int64_t M, int N, int K, const uint8_t* a, const f
 // The kernel by the sizes.
 //
 // Few tokens take the rows kernel (us at N = K = 4096 in bf16: 16 tokens 7.0,
-// 32 8.7, 64 11.7, 128 14.9; 64 x 64 tiles with K in four parts 12 to 12.5),
-// as long as it has no more than a workgroup a CU for 32 x 32 of the result
-// (64 tokens, 8192 outputs: 15.0, tiles 13.2), and up to 128 tokens where K
-// cannot be split.
+// 32 8.6, 64 11.6, 128 14.9; 64 x 64 tiles with K in four parts 11.9, 11.9,
+// 12.5, 12.5), as long as it has no more than a workgroup a CU for 32 x 32 of
+// the result (64 tokens, 8192 outputs: 15.0, tiles 13.2), and up to 128 tokens
+// where K cannot be split.
 //
 // The others take the tile of the least cost by the measured time of a load of
 // the card at K = 4096: `full` of what runs at a time, `one` of at most a
 // workgroup a CU.  The parts of K pay where the tiles are few (256 tokens,
-// 4096 outputs: 13.0 in four parts, 14.2 in two, 19.3 whole; 1024 tokens in
-// 128 x 128 tiles: 24.0 in two, 27.5 whole) and cost where they are many (2048
-// tokens: 41, 37).  fp32 outputs have no 256 x 256 tile: with its operands
+// 4096 outputs: 13.0 in four parts, 14.2 in two, 19.7 whole; 1024 tokens in
+// 128 x 128 tiles: 24.1 in two, 27.9 whole) and cost where they are many (2048
+// tokens: 43, 39).  fp32 outputs have no 256 x 256 tile: with its operands
 // widened in registers 128 x 256 took as long as 128 x 128 (1077, 1118 us for
 // 32768 tokens).
 struct TileChoice {

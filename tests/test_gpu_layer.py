@@ -125,6 +125,19 @@ def test_add_rmsnorm_special_rows(kda, io):
     assert torch.isnan(s[4, 2]) and torch.isnan(y[4, 300]) and (q[4, :256].float() == 0).all()
 
 
+def test_fp8_rows_of_far_values_with_a_small_eps(kda):
+    """Rows so small that 448 / amax has no fp32 value, while 1 / rms (1 / sqrt(eps): their squares are 0) lifts them."""
+    r = Rand(6)
+    x, w = r(4, 256) * torch.tensor([[1.0], [1e-30], [2e-37], [3e-36]], device="cuda"), r.weight(256)
+    q, s, _ = kda.kda_add_rmsnorm_fp8(make_cfg(kda, F32), x, None, w, 1e-30)
+    check_rows_fp8(q, s, ref.rmsnorm(x, w, 1e-30), ref.norm_chain(256) * U)
+    gate = r(4, 2, 128)
+    cfg = make_cfg(kda, F32, F32, 2)
+    q, s = kda.kda_output_gate_fp8(cfg, x.view(4, 2, 128), gate, w[:128].contiguous(), 1e-30)
+    e = ref.output_gate(x.view(4, 2, 128), gate, w[:128], 1e-30).view(4, -1)
+    check_rows_fp8(q, s, e, (ref.norm_chain(128) + 22) * U)
+
+
 @pytest.mark.parametrize("n,hidden", ROWS)
 @pytest.mark.parametrize("io,out,with_dh", [(BF, BF, True), (F32, F32, True), (BF, F32, False), (F32, BF, True)])
 def test_add_rmsnorm_backward(kda, n, hidden, io, out, with_dh):
