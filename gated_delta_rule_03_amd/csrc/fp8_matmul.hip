@@ -270,14 +270,19 @@ constexpr int tile_groups(int TN, int TT, int waves) {
 // 32768 x 16416 x 2048: 1205, 1102, 1089, 1171).
 constexpr int kGroup = 6;
 struct TileOrder {
-  int n_tiles, t_tiles, per, turn;   // per: tiles of an XCD, 0 where they are too few to split; turn: workgroups
-  __device__ int count(int wg) const {
-    if (!per) return (n_tiles * t_tiles - wg + turn - 1) / turn;
-    const int left = min(per, n_tiles * t_tiles - (wg & 7) * per) - (wg >> 3);
-    return left <= 0 ? 0 : (left + (turn >> 3) - 1) / (turn >> 3);
+  int n_tiles, t_tiles, turn;   // turn: workgroups, a multiple of 8 where they are fewer than the tiles
+  // The first tile of an XCD's run: an equal part of them, and one more for the first few.
+  __device__ int first(int xcd) const {
+    const int tiles = n_tiles * t_tiles;
+    return xcd * (tiles >> 3) + min(xcd, tiles & 7);
   }
+  __device__ int count(int wg) const {
+    const int left = first((wg & 7) + 1) - first(wg & 7) - (wg >> 3);
+    return left <= 0 ? 0 : (left + each() - 1) / each();
+  }
+  __device__ int each() const { return (turn + 7) >> 3; }   // workgroups of an XCD
   __device__ int2 at(int wg, int i) const {   // (output tile, token tile)
-    const int id = per ? (wg & 7) * per + (wg >> 3) + i * (turn >> 3) : wg + i * turn;
+    const int id = first(wg & 7) + (wg >> 3) + i * each();
     const int g = id / (kGroup * n_tiles), r = id - g * (kGroup * n_tiles);
     const int wide = min(kGroup, t_tiles - g * kGroup);
     return make_int2(r / wide, g * kGroup + r % wide);
@@ -565,9 +570,8 @@ static hipError_t launch_tiles(int64_t M, int N, int K, const uint8_t* a, const 
   order.t_tiles = static_cast<int>((M + TT - 1) / TT);
   const int64_t tiles = static_cast<int64_t>(order.n_tiles) * order.t_tiles;
   if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
-  const int slots = ncu * tile_groups(TN, TT, WN * WT) / SPLIT;
+  const int slots = std::max(8, ncu * tile_groups(TN, TT, WN * WT) / SPLIT / 8 * 8);
   order.turn = static_cast<int>(tiles < slots ? tiles : slots);
-  order.per = order.turn % 8 == 0 ? static_cast<int>((tiles + 7) / 8) : 0;
   kernel<<<dim3(order.turn), 64 * WN * WT * SPLIT, kLds, st>>>(M, N, K, order, a, sa, w, sw, y);
   return hipGetLastError();
 }
