@@ -21,6 +21,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass, field
@@ -478,14 +479,22 @@ def _workspace_at(nbytes, device, workspace):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+@functools.lru_cache(maxsize=64)
+def _op_fields(num_heads, head_v_dim, io_dtype, out_dtype):
+    """The struct of these values (never written afterwards, so calls share it)."""
+    c = KdaConfigC()
+    c.num_heads = num_heads
+    c.head_v_dim = head_v_dim
+    c.io_dtype = _dtype_code(io_dtype)
+    c.out_dtype = _dtype_code(out_dtype)
+    return c
+
+
 def _op_struct(cfg: Config):
     """The fields of the config that these operators read."""
-    c = KdaConfigC()
-    c.num_heads = cfg.num_heads
-    c.head_v_dim = cfg.head_v_dim
-    c.io_dtype = _dtype_code(cfg.io_dtype)
-    c.out_dtype = _dtype_code(cfg.out_dtype)
+    c = _op_fields(cfg.num_heads, cfg.head_v_dim, cfg.io_dtype, cfg.out_dtype)
     if cfg.stage_events is not None:
+        c = KdaConfigC.from_buffer_copy(c)
         c.stage_events = ctypes.cast(cfg.stage_events, ctypes.c_void_p)
     return ctypes.byref(c)
 
@@ -532,7 +541,7 @@ def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, 
     st = torch._C._cuda_getCurrentRawStream(dev.index)
     h_ = torch.empty_like(x) if h is None and residual is not None else h
     y_ = torch.empty_like(x, dtype=torch.float8_e4m3fn) if y is None else y
-    s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
+    s_ = torch.empty(*blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
     _check(_lib.kda_add_rmsnorm_fp8(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
                                     hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(),
                                     sp if s_ is y_scale else s_.data_ptr(), st), "kda_add_rmsnorm_fp8")
@@ -591,8 +600,8 @@ def kda_output_gate_fp8(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, 
         return _on_stream(dev, stream, lambda: kda_output_gate_fp8(cfg, o, gate, o_norm_weight, eps, y=y,
                                                                     y_scale=y_scale))
     st = torch._C._cuda_getCurrentRawStream(dev.index)
-    y_ = torch.empty(rows, dtype=torch.float8_e4m3fn, device=dev) if y is None else y
-    s_ = torch.empty(blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
+    y_ = torch.empty(*rows, dtype=torch.float8_e4m3fn, device=dev) if y is None else y
+    s_ = torch.empty(*blocks, dtype=torch.float32, device=dev) if y_scale is None else y_scale
     _check(_lib.kda_output_gate_fp8(_op_struct(cfg), n, op, gp, wp, eps,
                                     yp if y_ is y else y_.data_ptr(), sp if s_ is y_scale else s_.data_ptr(), st),
            "kda_output_gate_fp8")
@@ -638,7 +647,7 @@ def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
     if _elsewhere(dev, stream):
         return _on_stream(dev, stream, lambda: kda_fp8_matmul(cfg, a, a_scale, w, w_scale, y=y))
     st = torch._C._cuda_getCurrentRawStream(dev.index)
-    y_ = torch.empty(shape, dtype=cfg.out_dtype, device=dev) if y is None else y
+    y_ = torch.empty(*shape, dtype=cfg.out_dtype, device=dev) if y is None else y
     _check(_lib.kda_fp8_matmul(_op_struct(cfg), math.prod(lead), N, K, ap, sp, wp, wsp,
                                yp if y_ is y else y_.data_ptr(), st), "kda_fp8_matmul")
     return y_
