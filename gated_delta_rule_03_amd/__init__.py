@@ -499,6 +499,11 @@ def _op_struct(cfg: Config):
     return ctypes.byref(c)
 
 
+# ctypes cuts an integer to its argument's width: a size above that is passed as
+# one that the library refuses
+_INT32_MAX = 2**31 - 1
+
+
 def _scale_blocks(k: int) -> int:
     return (k + SCALE_BLOCK - 1) // SCALE_BLOCK
 
@@ -509,7 +514,7 @@ def kda_add_rmsnorm(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=No
     fp32.  Returns (y, h), y in the out dtype, h in the io dtype (x itself
     without a residual or h).  h=x or h=residual works in place."""
     shape, dev = x.shape, x.device
-    hidden = shape[-1]
+    hidden = min(shape[-1], _INT32_MAX)
     xp, rp = _at("x", x, shape, cfg.io_dtype, dev), _at("residual", residual, shape, cfg.io_dtype, dev)
     wp = _at("weight", weight, (hidden,), torch.float32, dev)
     hp, yp = _at("h", h, shape, cfg.io_dtype, dev), _at("y", y, shape, cfg.out_dtype, dev)
@@ -529,7 +534,7 @@ def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, 
     """kda_add_rmsnorm with y as e4m3 rows.  Returns (y, y_scale, h): y
     [..., hidden] float8_e4m3fn, y_scale [..., ceil(hidden / 128)] fp32."""
     shape, dev = x.shape, x.device
-    hidden = shape[-1]
+    hidden = min(shape[-1], _INT32_MAX)
     blocks = (*shape[:-1], _scale_blocks(hidden))
     xp, rp = _at("x", x, shape, cfg.io_dtype, dev), _at("residual", residual, shape, cfg.io_dtype, dev)
     wp = _at("weight", weight, (hidden,), torch.float32, dev)
@@ -559,7 +564,7 @@ def kda_add_rmsnorm_backward(cfg: Config, h, weight, dy, d_h=None, eps: float = 
     Returns (dx [..., hidden], dweight [hidden]), fp32; dx is the gradient of x
     and of residual alike.  dx=d_h works in place."""
     shape, dev = h.shape, h.device
-    hidden = shape[-1]
+    hidden = min(shape[-1], _INT32_MAX)
     n = h.numel() // hidden if hidden else 0
     hp, wp = _at("h", h, shape, cfg.io_dtype, dev), _at("weight", weight, (hidden,), torch.float32, dev)
     dyp, dhp = _at("dy", dy, shape, cfg.out_dtype, dev), _at("d_h", d_h, shape, torch.float32, dev)
@@ -648,6 +653,6 @@ def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
         return _on_stream(dev, stream, lambda: kda_fp8_matmul(cfg, a, a_scale, w, w_scale, y=y))
     st = torch._C._cuda_getCurrentRawStream(dev.index)
     y_ = torch.empty(*shape, dtype=cfg.out_dtype, device=dev) if y is None else y
-    _check(_lib.kda_fp8_matmul(_op_struct(cfg), math.prod(lead), N, K, ap, sp, wp, wsp,
+    _check(_lib.kda_fp8_matmul(_op_struct(cfg), math.prod(lead), min(N, _INT32_MAX), min(K, _INT32_MAX), ap, sp, wp, wsp,
                                yp if y_ is y else y_.data_ptr(), st), "kda_fp8_matmul")
     return y_

@@ -415,6 +415,8 @@ kda_status_t kda_output_gate(const kda_config_t *cfg, int64_t n_tokens,
  *   weight         [hidden] fp32
  *   eps            >= 0 (NaN or negative: KDA_ERR_INVALID_ARGUMENT); with 0 a
  *                  row of zeros gives NaN
+ *                  (the squares are summed in fp32: where the sum passes
+ *                  3.4e38 the row's y is 0, squares below 1e-45 count as 0)
  *   h              [n_tokens][hidden] io_dtype, or NULL if not wanted; may
  *                  alias x or residual (in place)
  *   y              [n_tokens][hidden] out_dtype; with h NULL it may alias x

@@ -286,6 +286,93 @@ def test_fp8_matmul_special_values(kda, M):
     assert torch.isnan(y[0]).all() and torch.isfinite(y[1:, cols]).all()
 
 
+# ---- offsets beyond 32 bits ----------------------------------------------------
+
+def big(*shape, dtype=BF):
+    """Zeros of more than 2^31 values."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of free memory")
+    t = torch.zeros(shape, dtype=dtype, device="cuda")
+    assert t.numel() > 2**31
+    return t
+
+
+def test_add_rmsnorm_large(kda):
+    r, n, hidden = Rand(41), 65600, 32768
+    x, w = big(n, hidden), r.weight(hidden)
+    x[-3:], x[0] = r(3, hidden, dtype=BF), r(hidden, dtype=BF)
+    rows = [0, n - 3, n - 2, n - 1]
+    cfg = make_cfg(kda)
+    e, rel = ref.rmsnorm(x[rows], w, EPS), ref.norm_chain(hidden) * U
+    q, s, h = kda.kda_add_rmsnorm_fp8(cfg, x, None, w)
+    assert h is x
+    check_rows_fp8(q[rows], s[rows], e, rel)
+    assert (q[n // 2].float() == 0).all()
+    del q, s
+    dy = big(n, hidden)
+    dy[-2:] = r(2, hidden, dtype=BF)
+    dx, dw = kda.kda_add_rmsnorm_backward(cfg, x, w, dy)
+    ex, ew, m, mw = ref.rmsnorm_backward(x[rows], w, dy[rows], None, EPS)
+    rel = 2 * rel + 8 * U
+    check(dx[rows], ex, m, rel)
+    check(dw, ew, mw, rel + (-(-n // 768) + 768) * U)
+    assert (dx[n // 2] == 0).all()
+
+
+def test_output_gate_large(kda):
+    r, n, H, d = Rand(42), 131200, 128, 128
+    o, gate, w = big(n, H, d), big(n, H, d), r.weight(d)
+    rows = [0, n - 2, n - 1]
+    o[rows], gate[rows] = r(3, H, d, dtype=BF), r(3, H, d, dtype=BF)
+    cfg = make_cfg(kda, BF, BF, H, d)
+    q, s = kda.kda_output_gate_fp8(cfg, o, gate, w)
+    rel = (ref.norm_chain(d) + 22) * U
+    check_rows_fp8(q[rows], s[rows], ref.output_gate(o[rows], gate[rows], w, EPS).view(3, -1), rel)
+    del q, s
+    dy = torch.zeros_like(o)
+    dy[rows] = r(3, H, d, dtype=BF)
+    d_o, d_gate, dw = kda.kda_output_gate_backward(cfg, o, gate, w, dy)
+    e, eg, ew, m, mg, mw = ref.output_gate_backward(o[rows], gate[rows], w, dy[rows], EPS)
+    check(d_o[rows], e, m, 2 * rel + 8 * U)
+    check(d_gate[rows], eg, mg, 2 * rel + 8 * U)
+    check(dw, ew, mw, 2 * rel + (8 + 5500 + 128 + 128 + 16) * U)
+
+
+@pytest.mark.parametrize("M,N,K", [(131200, 16416, 16384), (1, 262200, 8208), (40, 262200, 8208), (300, 262200, 8208)])
+def test_fp8_matmul_large(kda, M, N, K):
+    """The operand or the output of more than 2^31 values, by its first and last rows and columns."""
+    r, f = Rand(43), 64
+    a, w = torch.zeros(M, K, dtype=F8, device="cuda"), torch.zeros(N, K, dtype=F8, device="cuda")
+    assert max(a.numel(), w.numel()) > 2**31
+    kb, m, n = -(-K // 128), min(M, f), min(N, f)
+    sa, sw = r(M, kb).exp(), r(-(-N // 128), kb).exp()
+    rows, cols = sorted({*range(m), *range(M - m, M)}), [*range(n), *range(N - n, N)]
+    q = lambda k: r(k, K).to(F8).view(torch.uint8)   # noqa: E731  (indexed as bytes)
+    a.view(torch.uint8)[rows], w.view(torch.uint8)[cols] = q(len(rows)), q(len(cols))
+    y = kda.kda_fp8_matmul(make_cfg(kda), a, sa, w, sw)
+    a, sa = a.view(torch.uint8)[rows].view(F8), sa[rows]
+    scale = sw.repeat_interleave(128, 0)[cols]   # a row's own scale
+    x = ref.dequantised(a, sa)
+    z = w.view(torch.uint8)[cols].view(F8).double() * scale.double().repeat_interleave(128, -1)[:, :K]
+    e = x @ z.T.contiguous()
+    lim = (128 + kb + 19) * U * (x.abs() @ z.abs().T.contiguous())
+    lim = lim + 128 * 2.0 ** -13 * (ref.blocks_of(x).abs().amax(-1) @ ref.blocks_of(z).abs().amax(-1).T.contiguous())
+    check(y[rows][:, cols], e, lim, 1.0)
+    assert (y[M // 2, n:N - n] == 0).all()
+
+
+def test_sizes_beyond_32_bits_are_refused(kda):
+    """Sizes that an int32 argument would cut to small ones."""
+    empty = lambda *s, dtype=F8: torch.empty(s, dtype=dtype, device="cuda")   # noqa: E731
+    k = 2**32 + 16
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_fp8_matmul(make_cfg(kda), empty(0, k), empty(0, k // 128 + 1, dtype=F32), empty(1, k),
+                           empty(1, k // 128 + 1, dtype=F32))
+    assert e.value.status == kda.KDA_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):
+        kda.kda_add_rmsnorm(make_cfg(kda), empty(0, 2**32 + 8, dtype=BF), None, empty(8, dtype=F32))
+
+
 # ---- streams, graphs, repeats ------------------------------------------------
 
 def everything(kda, r, stream=None):
