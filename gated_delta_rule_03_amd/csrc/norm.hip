@@ -140,7 +140,7 @@ __global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_bwd_kernel(
     const void* __restrict__ dy, const float* dh, float* dx, float* __restrict__ part) {
   constexpr int kRows = threads_of(L) / L;
   __shared__ float red[2][16][2];
-  __shared__ float join[kRows > 1 ? kRows * L * 8 : 1];
+  __shared__ float join[kRows > 1 ? kRows * NV * L * 8 : 1];
   const int lane = threadIdx.x % L;
   const int nvec = hidden >> 3;
   const float rcp = 1.0f / static_cast<float>(hidden);
@@ -197,13 +197,14 @@ __global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_bwd_kernel(
     }
   }
   if constexpr (kRows > 1) {   // the rows' lanes joined
-    static_assert(NV == 1, "a lane holds 8 channels");
-    store_n<false, 8>(join, threadIdx.x * 8, dw[0]);
+    const int row = threadIdx.x / L * NV * L;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) store_n<false, 8>(join, (row + i * L + lane) * 8, dw[i]);
     __syncthreads();
     for (int c = threadIdx.x; c < hidden; c += 256) {
       float t = 0.f;
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) t += join[k * L * 8 + c];
+      for (int k = 0; k < kRows; ++k) t += join[k * NV * L * 8 + c];
       part[static_cast<size_t>(blockIdx.x) * hidden + c] = t;
     }
   } else {
@@ -247,15 +248,27 @@ hipError_t launch_column_sums(int parts, int cols, const float* part, float* out
 }
 
 // Calls f with the lanes per row and the steps of 8 channels a lane that hold
-// a row of `hidden` channels in registers.
-template <class F>
+// a row of `hidden` channels in registers.  A wave to a row needs no barrier;
+// the more lanes a row has beyond that, the more of them the odd sizes leave
+// idle, but wide rows on few lanes leave few loads of other rows in flight.
+// (400 MB tensors, TB/s, forward with e4m3 out / backward.  bf16: 520 channels
+// on 256 lanes 2.8 / 2.2, on 64 4.8 / 5.0; 1032 4.7 / 3.7, 4.9 / 5.2; 2048
+// 5.7 / 5.4, 5.4 / 4.7; 4104 on 1024 lanes 4.3 / 4.0, on 256 4.9 / 4.8; 8192
+// 5.6 / 5.3, 5.2 / 4.3.  fp32: 520 5.0 / 3.5, 5.3 / 5.3; 1000 5.6 / 5.2, 5.3 /
+// 5.2; 5120 5.9 / 5.2, 5.6 / 5.2.)
+template <bool BF16, class F>
 static hipError_t with_row_shape(int hidden, F&& f) {
   using std::integral_constant;
   if (hidden <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   if (hidden <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   if (hidden <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (hidden <= (BF16 ? 1024 : 768)) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if constexpr (BF16)
+    if (hidden <= 1536) return f(integral_constant<int, 64>{}, integral_constant<int, 3>{});
   if (hidden <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
   if (hidden <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if constexpr (BF16)
+    if (hidden <= 6144) return f(integral_constant<int, 256>{}, integral_constant<int, 3>{});
   if (hidden <= 8192) return f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
   if (hidden <= 16384) return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
@@ -263,52 +276,51 @@ static hipError_t with_row_shape(int hidden, F&& f) {
 
 hipError_t launch_add_rmsnorm(int64_t n, int hidden, const void* x, const void* res, const float* w, float eps,
                               void* h, void* y, float* scale, bool io_bf16, bool out_bf16, hipStream_t st) {
-  return with_row_shape(hidden, [&](auto lanes, auto nv) {
-    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
-    constexpr int kRows = threads_of(L) / L;
-    const int64_t blocks = (n + kRows - 1) / kRows;
-    const dim3 grid(static_cast<unsigned>(blocks < 65536 ? blocks : 65536));
-    const dim3 block(threads_of(L));
-    auto go = [&](auto bf, auto out) {
-      add_rmsnorm_kernel<decltype(bf)::value, decltype(out)::value, L, NV>
-          <<<grid, block, 0, st>>>(n, hidden, x, res, w, eps, h, y, scale);
-    };
-    auto by_out = [&](auto bf) {
-      if (scale) go(bf, std::integral_constant<Out, Out::kFp8>{});
-      else if (out_bf16) go(bf, std::integral_constant<Out, Out::kBf16>{});
-      else go(bf, std::integral_constant<Out, Out::kFp32>{});
-    };
-    if (io_bf16) by_out(std::true_type{});
-    else by_out(std::false_type{});
-    return hipGetLastError();
-  });
+  auto by_io = [&](auto bf) {
+    return with_row_shape<decltype(bf)::value>(hidden, [&](auto lanes, auto nv) {
+      constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
+      constexpr int kRows = threads_of(L) / L;
+      const int64_t blocks = (n + kRows - 1) / kRows;
+      const dim3 grid(static_cast<unsigned>(blocks < 65536 ? blocks : 65536));
+      auto go = [&](auto out) {
+        add_rmsnorm_kernel<decltype(bf)::value, decltype(out)::value, L, NV>
+            <<<grid, dim3(threads_of(L)), 0, st>>>(n, hidden, x, res, w, eps, h, y, scale);
+      };
+      if (scale) go(std::integral_constant<Out, Out::kFp8>{});
+      else if (out_bf16) go(std::integral_constant<Out, Out::kBf16>{});
+      else go(std::integral_constant<Out, Out::kFp32>{});
+      return hipGetLastError();
+    });
+  };
+  return io_bf16 ? by_io(std::true_type{}) : by_io(std::false_type{});
 }
 
-// Workgroups of the backward, each with a row of partial sums: three a CU.
-// 32768 x 4096 in bf16: 292 us (5.5 TB/s) with 768, 296 with 1024, 305 with
-// 512; with cached loads of h and dy 298.
+// Workgroups of the backward at most, each with a row of partial sums: three a
+// CU.  32768 x 4096 in bf16: 292 us (5.5 TB/s) with 768, 296 with 1024, 305
+// with 512; with cached loads of h and dy 298.
 int add_rmsnorm_bwd_parts(int64_t n) { return static_cast<int>(n < 768 ? n : 768); }
 
 hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const float* w, float eps, const void* dy,
                                   const float* dh, float* dx, float* dw, float* part, bool h_bf16, bool dy_bf16,
                                   hipStream_t st) {
-  const int parts = add_rmsnorm_bwd_parts(n);
-  if (parts > 0) {
-    const hipError_t e = with_row_shape(hidden, [&](auto lanes, auto nv) {
+  int parts = 0;
+  auto by_h = [&](auto hb) {
+    return with_row_shape<decltype(hb)::value>(hidden, [&](auto lanes, auto nv) {
       constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
-      auto go = [&](auto hb, auto db) {
+      constexpr int kRows = threads_of(L) / L;
+      parts = add_rmsnorm_bwd_parts((n + kRows - 1) / kRows);   // (short rows fill a workgroup together)
+      if (parts == 0) return hipSuccess;
+      auto go = [&](auto db) {
         add_rmsnorm_bwd_kernel<decltype(hb)::value, decltype(db)::value, L, NV>
             <<<dim3(parts), dim3(threads_of(L)), 0, st>>>(n, hidden, h, w, eps, dy, dh, dx, part);
       };
-      if (h_bf16 && dy_bf16) go(std::true_type{}, std::true_type{});
-      else if (h_bf16) go(std::true_type{}, std::false_type{});
-      else if (dy_bf16) go(std::false_type{}, std::true_type{});
-      else go(std::false_type{}, std::false_type{});
+      if (dy_bf16) go(std::true_type{});
+      else go(std::false_type{});
       return hipGetLastError();
     });
-    if (e != hipSuccess) return e;
-  }
-  return launch_column_sums(parts, hidden, part, dw, st);
+  };
+  const hipError_t e = h_bf16 ? by_h(std::true_type{}) : by_h(std::false_type{});
+  return e != hipSuccess ? e : launch_column_sums(parts, hidden, part, dw, st);
 }
 
 }  // namespace kda

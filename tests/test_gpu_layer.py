@@ -53,7 +53,7 @@ def guarded(shape, dtype):
 # ---- the norm -------------------------------------------------------------
 
 ROWS = [(1, 8), (5, 72), (3, 512), (9, 520), (1, 2048), (7, 2056), (2, 4096), (5, 4104), (3, 8192), (2, 8200),
-        (3, 16384), (2, 16392), (1, 32768), (1031, 128), (4099, 264)]
+        (3, 16384), (2, 16392), (1, 32768), (1031, 128), (4099, 264), (4001, 640), (7, 784), (13, 1288), (3, 6144)]
 
 
 @pytest.mark.parametrize("n,hidden", ROWS)
