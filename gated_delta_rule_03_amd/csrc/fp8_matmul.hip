@@ -584,67 +584,94 @@ static hipError_t launch_rows(int64_t M, int N, int K, const uint8_t* a, const f
   return hipGetLastError();
 }
 
-// The kernel by the sizes.
+// The kernel by the sizes: the one whose measured time is least.
 //
-// Few tokens take the rows kernel (us at N = K = 4096 in bf16: 16 tokens 7.0,
-// 32 8.6, 64 11.6, 128 14.9; 64 x 64 tiles with K in four parts 11.9, 11.9,
-// 12.5, 12.5), as long as it has no more than a workgroup a CU for 32 x 32 of
-// the result (64 tokens, 8192 outputs: 15.0, tiles 13.2), and up to 128 tokens
-// where K cannot be split.
+// A launch of `groups` workgroups, ncu * per of which run at a time, takes
+//   base + loads * each + (scale blocks of a row) * (full * whole loads + the last load's)
+// where the last load costs `one` with at most a workgroup a CU, up to `full`
+// with `per`.  The figures (ns) are a fit to 583 sizes of 17 to 8000 tokens,
+// 256 to 16416 outputs and 512 to 8192 channels: the kernel that they pick
+// takes 1.1% longer than the fastest one on average (1.0% with fp32 outputs).
 //
-// The others take the tile of the least cost by the measured time of a load of
-// the card at K = 4096: `full` of what runs at a time, `one` of at most a
-// workgroup a CU.  The parts of K pay where the tiles are few (256 tokens,
-// 4096 outputs: 13.0 in four parts, 14.2 in two, 19.7 whole; 1024 tokens in
-// 128 x 128 tiles: 24.1 in two, 27.9 whole) and cost where they are many (2048
-// tokens: 43, 39).  fp32 outputs have no 256 x 256 tile: with its operands
-// widened in registers 128 x 256 took as long as 128 x 128 (1077, 1118 us for
-// 32768 tokens).
-struct TileChoice {
-  int tile, split, full, one;
+// What they say: the rows kernel is the fastest while its workgroups are few
+// (32 tokens, 4096 x 4096, bf16: 8.6 us, tiles 11.9; fp32, 200 tokens, 1024 x
+// 4096: 11.6, tiles 17.2) and loses to the tiles' reuse beyond (128 tokens,
+// 4096 x 4096, bf16: 14.9, tiles 12.5).  The parts of K pay where the tiles
+// are few (256 tokens, 4096 outputs: 13.0 in four parts, 14.2 in two, 19.7
+// whole; 1024 tokens in 128 x 128 tiles: 24.1 in two, 27.9 whole) and cost
+// where they are many (2048 tokens: 43, 39).  fp32 outputs have no 256 x 256
+// tile: with its operands widened in registers 128 x 256 took as long as 128 x
+// 128 (1077, 1118 us for 32768 tokens).
+struct Choice {
+  int outs, toks, split;   // the workgroup's results; split 0: the rows kernel
+  int base, each, full, one;
 };
-constexpr TileChoice kChoicesBf16[] = {{256, 1, 610, 480}, {128, 1, 380, 250}, {128, 2, 240, 210},
-                                       {64, 1, 290, 195},  {64, 2, 186, 140},  {64, 4, 130, 130}};
-constexpr TileChoice kChoicesFp32[] = {{128, 1, 720, 470}, {128, 2, 450, 375}, {64, 1, 530, 270},
-                                       {64, 2, 300, 195},  {64, 4, 185, 185}};
+constexpr Choice kChoicesBf16[] = {
+    {16, 16, 0, 3570, 0, 100, 0},      {32, 16, 0, 3820, 0, 151, 0},      {32, 32, 0, 3260, 370, 221, 0},
+    {64, 32, 0, 3650, 0, 313, 0},      {64, 64, 4, 2900, 1650, 242, 0},   {64, 64, 2, 3550, 380, 446, 272},
+    {64, 64, 1, 3520, 430, 841, 336},  {128, 128, 2, 2990, 2020, 542, 0}, {128, 128, 1, 2880, 1690, 971, 613},
+    {256, 256, 1, 3160, 5080, 1418, 0}};
+constexpr Choice kChoicesFp32[] = {
+    {16, 16, 0, 3480, 90, 105, 0},      {32, 16, 0, 3760, 0, 159, 0},      {32, 32, 0, 2980, 640, 234, 0},
+    {64, 32, 0, 3310, 290, 350, 0},     {64, 64, 4, 4850, 1870, 359, 0},   {64, 64, 2, 4880, 1070, 726, 373},
+    {64, 64, 1, 4230, 1470, 1540, 465}, {128, 128, 2, 4030, 4790, 964, 0}, {128, 128, 1, 4120, 5580, 1951, 987}};
+
+// Workgroups of a choice that a CU runs at a time.
+static int64_t choice_per_cu(const Choice& c) {
+  return c.split ? tile_groups(c.outs, c.toks, c.outs == 256 ? 8 : 4) / c.split : 1;
+}
+
+static int64_t choice_cost(const Choice& c, int64_t M, int N, int blocks, int ncu) {
+  const int64_t per = choice_per_cu(c), slots = ncu * per;
+  const int64_t groups = (N + c.outs - 1) / c.outs * ((M + c.toks - 1) / c.toks);
+  const int64_t left = groups % slots;
+  int64_t loads = groups / slots, time = loads * c.full;
+  if (left) {
+    const int64_t deep = (left + ncu - 1) / ncu;   // workgroups on the fullest CU
+    time += deep == per ? c.full : c.one + (c.full - c.one) * (deep - 1) / (per - 1);
+    ++loads;
+  }
+  return c.base + loads * c.each + blocks * time;
+}
 
 template <bool OUT_BF16>
 static hipError_t launch_fp8_matmul_to(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                                        const float* sw, void* y, hipStream_t st) {
-  if (M <= 16) return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
   int ncu = 0;
   const hipError_t e = device_cus(&ncu);
   if (e != hipSuccess) return e;
-  // equal parts of K, of four blocks or more
-  const auto splits = [&](int parts) { return K % (kScaleBlock * parts) == 0 && K / kScaleBlock >= 4 * parts; };
-  const auto groups = [&](int64_t outs, int64_t toks) { return (N + outs - 1) / outs * ((M + toks - 1) / toks); };
-  if ((M <= 64 && groups(32, 32) <= ncu) || (M <= 128 && 2 * groups(64, 64) <= ncu && !splits(4))) {
-    // the most reuse that still gives every CU a workgroup
-    if (groups(64, 32) >= ncu) return launch_rows<4, 2, 8, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
-    if (groups(32, 32) >= ncu) return launch_rows<2, 2, 8, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
-    if (groups(32, 16) >= ncu) return launch_rows<2, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+  const int blocks = (K + kScaleBlock - 1) / kScaleBlock;
+  // (of its 16 waves' blocks a second one in flight pays only if there is one: 16 blocks 4.6 us, 6.2)
+  const auto rows_16x16 = [&] {
+    if (blocks <= 16) return launch_rows<1, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
     return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
-  }
+  };
+  if ((M + 15) / 16 * ((N + 15) / 16) <= ncu) return rows_16x16();   // one load of them: the least of every figure
   int64_t least = INT64_MAX;
-  TileChoice best{};
-  const auto weigh = [&](const TileChoice& c) {
-    if (c.split > 1 && !splits(c.split)) return;
-    const int side = c.tile == 256 ? 8 : 4;   // waves of a part
-    const int64_t tiles = groups(c.tile, c.tile);
-    const int64_t slots = static_cast<int64_t>(ncu) * tile_groups(c.tile, c.tile, side) / c.split, left = tiles % slots;
-    const int64_t cost = tiles / slots * c.full + (left == 0 ? 0 : left <= ncu ? c.one : c.full);
+  Choice best{};
+  const auto weigh = [&](const Choice& c) {
+    if (c.split == 0 ? M > 4096 : M <= 16) return;   // (a tile would be nearly empty; rows: the grid's second axis)
+    // equal parts of K, of four blocks or more
+    if (c.split > 1 && (K % (kScaleBlock * c.split) || blocks < 4 * c.split)) return;
+    const int64_t cost = choice_cost(c, M, N, blocks, ncu);
     if (cost < least) {
       least = cost;
       best = c;
     }
   };
   if constexpr (OUT_BF16) {
-    for (const TileChoice& c : kChoicesBf16) weigh(c);
-    if (best.tile == 256) return launch_tiles<256, 256, 2, 4, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
+    for (const Choice& c : kChoicesBf16) weigh(c);
+    if (best.outs == 256) return launch_tiles<256, 256, 2, 4, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
   } else {
-    for (const TileChoice& c : kChoicesFp32) weigh(c);
+    for (const Choice& c : kChoicesFp32) weigh(c);
   }
-  if (best.tile == 128) {
+  if (best.split == 0) {
+    if (best.outs == 64) return launch_rows<4, 2, 8, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    if (best.toks == 32) return launch_rows<2, 2, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    if (best.outs == 32) return launch_rows<2, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
+    return rows_16x16();
+  }
+  if (best.outs == 128) {
     if (best.split == 2) return launch_tiles<128, 128, 2, 2, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
     return launch_tiles<128, 128, 2, 2, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, ncu, st);
   }

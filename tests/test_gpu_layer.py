@@ -251,7 +251,10 @@ PRODUCTS = [(1, 1, 16), (1, 17, 48), (1, 4096, 4096), (2, 130, 128), (16, 64, 11
             (64, 256, 256), (65, 320, 1024), (100, 1000, 400), (128, 128, 128), (129, 257, 384), (250, 515, 4096),
             (256, 256, 4096), (257, 300, 272), (300, 16416, 128), (511, 512, 528), (1000, 1002, 1008),
             (2049, 260, 640), (4100, 1028, 1040), (5000, 4200, 272), (4500, 4400, 1168), (70000, 264, 128),
-            (80, 520, 2048), (200, 1000, 1024), (300, 4100, 2048), (700, 3000, 2560), (900, 4200, 1024), (1300, 3500, 1536)]
+            (80, 520, 2048), (200, 1000, 1024), (300, 4100, 2048), (700, 3000, 2560), (900, 4200, 1024), (1300, 3500, 1536),
+            (275, 228, 800), (322, 767, 1968), (518, 486, 16), (609, 781, 48), (762, 663, 272), (419, 591, 1024),
+            (393, 628, 4096), (1059, 589, 7680), (1226, 1615, 1376), (1266, 1611, 1280), (1854, 2262, 1024),
+            (3505, 3049, 144), (2323, 3339, 128), (3589, 3397, 416), (5337, 5563, 432)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
