@@ -455,7 +455,7 @@ def _on_stream(device, stream, again):
 
 def _elsewhere(device, stream):
     """Whether a call has to change the current device or stream first."""
-    return stream is not None or device.type != "cuda" or device.index != torch.cuda.current_device()
+    return stream is not None or device.type != "cuda" or device.index != torch._C._cuda_getDevice()
 
 
 def _at(name, t, shape, dtype, device):

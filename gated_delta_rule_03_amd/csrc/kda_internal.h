@@ -167,7 +167,7 @@ hipError_t launch_add_rmsnorm(int64_t n, int hidden, const void* x, const void* 
                               void* h, void* y, float* scale, bool io_bf16, bool out_bf16, hipStream_t st);
 
 // Its backward pass; dh may be null and may be dx.  part holds
-// add_rmsnorm_bwd_parts rows of `hidden` partial sums of dw.
+// up to add_rmsnorm_bwd_parts rows of `hidden` partial sums of dw.
 int add_rmsnorm_bwd_parts(int64_t n);
 hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const float* w, float eps, const void* dy,
                                   const float* dh, float* dx, float* dw, float* part, bool h_bf16, bool dy_bf16,

@@ -14,6 +14,8 @@
 // 131072 x 4096 in bf16 with a residual and e4m3 out: 655 us, 5.8 TB/s (a large
 // copy reaches 4.8).  A single row of 4096 takes 3.0 us, the launch and one trip
 // to memory.
+#include <algorithm>
+
 #include "kda_device.h"
 #include "kda_internal.h"
 #include "vec_io.h"
@@ -295,10 +297,21 @@ hipError_t launch_add_rmsnorm(int64_t n, int hidden, const void* x, const void* 
   return io_bf16 ? by_io(std::true_type{}) : by_io(std::false_type{});
 }
 
-// Workgroups of the backward at most, each with a row of partial sums: three a
-// CU.  32768 x 4096 in bf16: 292 us (5.5 TB/s) with 768, 296 with 1024, 305
-// with 512; with cached loads of h and dy 298.
-int add_rmsnorm_bwd_parts(int64_t n) { return static_cast<int>(n < 768 ? n : 768); }
+// Workgroups of the backward, each with a row of partial sums to write and to
+// join: at most three a CU, and with a row at a time a whole number a CU.  One
+// until three rows would share it (us, 700 x 2056 fp32: 11.9 with 256, 12.6
+// with 512, 13.9 with 700), two up to 3000 rows (1200 x 4096 bf16: 20.9, 18.9,
+// 19.8 with 768), then three (8000 x 4096 bf16: 115, 81, 77; 32768 x 4096: 296
+// with 1024, 292 with 768).  Several rows at a time take what they fill (1600 x
+// 640 bf16: 9.5 with 256, 8.8 with 400).
+template <int kRows>
+static int bwd_groups(int64_t n) {
+  const int64_t groups = (n + kRows - 1) / kRows;
+  if (kRows > 1 || groups <= 256) return static_cast<int>(std::min<int64_t>(groups, 768));
+  return groups <= 768 ? 256 : groups <= 3000 ? 512 : 768;
+}
+
+int add_rmsnorm_bwd_parts(int64_t n) { return static_cast<int>(std::min<int64_t>(n, 768)); }   // the most of them
 
 hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const float* w, float eps, const void* dy,
                                   const float* dh, float* dx, float* dw, float* part, bool h_bf16, bool dy_bf16,
@@ -308,7 +321,7 @@ hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const fl
     return with_row_shape<decltype(hb)::value>(hidden, [&](auto lanes, auto nv) {
       constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
       constexpr int kRows = threads_of(L) / L;
-      parts = add_rmsnorm_bwd_parts((n + kRows - 1) / kRows);   // (short rows fill a workgroup together)
+      parts = bwd_groups<kRows>(n);
       if (parts == 0) return hipSuccess;
       auto go = [&](auto db) {
         add_rmsnorm_bwd_kernel<decltype(hb)::value, decltype(db)::value, L, NV>
