@@ -137,7 +137,8 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
     float sc[U][T];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int b = min(b0 + u * WAVES, KB - 1), k = b * kScaleBlock + kq;
+      const int b = b0 + u * WAVES, k = b * kScaleBlock + kq;
+      if (b >= KB) break;
 #pragma unroll
       for (int j = 0; j < J; ++j) wf[u][j] = load(wrow[j], k);
       const float s = swrow[b];
@@ -641,16 +642,23 @@ static hipError_t launch_fp8_matmul_to(int64_t M, int N, int K, const uint8_t* a
   const hipError_t e = device_cus(&ncu);
   if (e != hipSuccess) return e;
   const int blocks = (K + kScaleBlock - 1) / kScaleBlock;
-  // (of its 16 waves' blocks a second one in flight pays only if there is one: 16 blocks 4.6 us, 6.2)
+  // One load of the smallest groups is the least of every figure.  With up to
+  // 16 tokens the rows kernels share no tokens, and what counts beyond is the
+  // stream of the weight: many short loads for a few tokens and a long K (1 x
+  // 16416 x 4096: 14.1 us, with 32 outputs a workgroup 17.0; x 2048 9.1, 8.8),
+  // fewer reads of the tokens for more of them (16 x 16416 x 4096: 24.3, 21.3).
+  const bool one_load = (M + 15) / 16 * ((N + 15) / 16) <= ncu;
+  // (Without a second block for the waves the shorter code is 0.3 us faster.)
   const auto rows_16x16 = [&] {
     if (blocks <= 16) return launch_rows<1, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
     return launch_rows<1, 1, 16, 2, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
   };
-  if ((M + 15) / 16 * ((N + 15) / 16) <= ncu) return rows_16x16();   // one load of them: the least of every figure
+  if (one_load || (M < 8 && blocks >= 32)) return rows_16x16();
+  if (M <= 16) return launch_rows<2, 1, 16, 1, OUT_BF16>(M, N, K, a, sa, w, sw, y, st);
   int64_t least = INT64_MAX;
   Choice best{};
   const auto weigh = [&](const Choice& c) {
-    if (c.split == 0 ? M > 4096 : M <= 16) return;   // (a tile would be nearly empty; rows: the grid's second axis)
+    if (c.split == 0 && M > 4096) return;   // (the grid's second axis)
     // equal parts of K, of four blocks or more
     if (c.split > 1 && (K % (kScaleBlock * c.split) || blocks < 4 * c.split)) return;
     const int64_t cost = choice_cost(c, M, N, blocks, ncu);

@@ -254,7 +254,7 @@ PRODUCTS = [(1, 1, 16), (1, 17, 48), (1, 4096, 4096), (2, 130, 128), (16, 64, 11
             (80, 520, 2048), (200, 1000, 1024), (300, 4100, 2048), (700, 3000, 2560), (900, 4200, 1024), (1300, 3500, 1536),
             (275, 228, 800), (322, 767, 1968), (518, 486, 16), (609, 781, 48), (762, 663, 272), (419, 591, 1024),
             (393, 628, 4096), (1059, 589, 7680), (1226, 1615, 1376), (1266, 1611, 1280), (1854, 2262, 1024),
-            (3505, 3049, 144), (2323, 3339, 128), (3589, 3397, 416), (5337, 5563, 432)]
+            (3505, 3049, 144), (2323, 3339, 128), (3589, 3397, 416), (5337, 5563, 432), (12, 6000, 1040), (3, 8200, 4112), (2, 40, 2576)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
