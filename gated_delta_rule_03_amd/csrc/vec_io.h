@@ -127,17 +127,18 @@ __device__ __forceinline__ uint2 quantise_block8(const float (&t)[8], float m, f
   const float amax = __uint_as_float(lane_group_umax16(a));
   const bool tiny = amax * m <= kAmaxFloor;
   *scale = (tiny ? kAmaxFloor : amax * m) * (1.0f / kE4M3Max);
-  // The values are multiplied by 2^-30 of that factor and the conversion
-  // multiplies by 2^30: the factor is finite for every amax (a small eps lifts
-  // values near the type's smallest), so a zero times it stays a zero.
-  constexpr float kRaise = 0x1p-30f;
-  const float c = tiny ? fminf(m * (kE4M3Max * kRaise / kAmaxFloor), 3.4028235e38f) : kE4M3Max * kRaise / amax;
+  // Where amax is below 1 the values are multiplied by 2^-30 of that factor and
+  // the conversion multiplies by 2^30, so that the factor is a normal number for
+  // every amax (a small eps lifts values near the type's smallest) and a zero
+  // times it stays a zero.
+  const float raise = amax < 1.0f ? 0x1p-30f : 1.0f;
+  const float c = tiny ? fminf(m * (kE4M3Max * 0x1p-30f / kAmaxFloor), 3.4028235e38f) : kE4M3Max * raise / amax;
   typedef short s16x2 __attribute__((ext_vector_type(2)));
   s16x2 lo = {}, hi = {};
-  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, t[0] * c, t[1] * c, kRaise, false);
-  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, t[2] * c, t[3] * c, kRaise, true);
-  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, t[4] * c, t[5] * c, kRaise, false);
-  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, t[6] * c, t[7] * c, kRaise, true);
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, t[0] * c, t[1] * c, raise, false);
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, t[2] * c, t[3] * c, raise, true);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, t[4] * c, t[5] * c, raise, false);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, t[6] * c, t[7] * c, raise, true);
   return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 

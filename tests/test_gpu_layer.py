@@ -138,6 +138,18 @@ def test_fp8_rows_of_far_values_with_a_small_eps(kda):
     check_rows_fp8(q, s, e, (ref.norm_chain(128) + 22) * U)
 
 
+def test_fp8_rows_of_far_values_with_a_large_weight(kda):
+    """Rows whose weighted values are so large that 448 / amax is near fp32's smallest normal number."""
+    r = Rand(7)
+    x, w = r(4, 256) * torch.tensor([[1.0], [1e12], [1e17], [3e17]], device="cuda"), r.weight(256) * 1e18
+    q, s, _ = kda.kda_add_rmsnorm_fp8(make_cfg(kda, F32), x, None, w)
+    check_rows_fp8(q, s, ref.rmsnorm(x, w, EPS), ref.norm_chain(256) * U)
+    gate = r(4, 2, 128)
+    q, s = kda.kda_output_gate_fp8(make_cfg(kda, F32, F32, 2), x.view(4, 2, 128), gate, w[:128].contiguous())
+    e = ref.output_gate(x.view(4, 2, 128), gate, w[:128], EPS).view(4, -1)
+    check_rows_fp8(q, s, e, (ref.norm_chain(128) + 22) * U)
+
+
 @pytest.mark.parametrize("n,hidden", ROWS)
 @pytest.mark.parametrize("io,out,with_dh", [(BF, BF, True), (F32, F32, True), (BF, F32, False), (F32, BF, True)])
 def test_add_rmsnorm_backward(kda, n, hidden, io, out, with_dh):
