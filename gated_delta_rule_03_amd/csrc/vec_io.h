@@ -7,6 +7,7 @@
 
 #include <type_traits>
 
+#include "e4m3.h"
 #include "kda_device.h"
 #include "mfma.h"
 
@@ -105,10 +106,6 @@ __device__ __forceinline__ float dpp_group_sum(float x) {
   if constexpr (W == 16) x += dpp_mov<0x140>(x);
   return x;
 }
-
-constexpr int kScaleBlock = 128;        // channels that share an e4m3 scale
-constexpr float kE4M3Max = 448.0f;
-constexpr float kAmaxFloor = 1e-30f;    // a block of zeros still has a scale
 
 // The scale of the 128-channel block whose values m * t[e] sit 8 to a lane
 // over an aligned group of 16 lanes (every lane active; lanes past the row's
