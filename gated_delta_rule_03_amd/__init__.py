@@ -512,7 +512,8 @@ def kda_add_rmsnorm(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=No
     """h = x + residual and y = h / sqrt(mean(h^2) + eps) * weight per row:
     x, residual [..., hidden] io dtype (residual may be None), weight [hidden]
     fp32.  Returns (y, h), y in the out dtype, h in the io dtype (x itself
-    without a residual or h).  h=x or h=residual works in place."""
+    without a residual or h).  h=x or h=residual works in place; so does y=x
+    without either, which leaves no h: None is returned for it."""
     shape, dev = x.shape, x.device
     hidden = min(shape[-1], _INT32_MAX)
     xp, rp = _at("x", x, shape, cfg.io_dtype, dev), _at("residual", residual, shape, cfg.io_dtype, dev)
@@ -526,7 +527,9 @@ def kda_add_rmsnorm(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=No
     _check(_lib.kda_add_rmsnorm(_op_struct(cfg), x.numel() // hidden if hidden else 0, hidden, xp, rp, wp, eps,
                                 hp if h_ is h else h_.data_ptr(), yp if y_ is y else y_.data_ptr(), st),
            "kda_add_rmsnorm")
-    return y_, x if h_ is None else h_
+    if h_ is None and not (yp and yp == xp):   # (y over x: x no longer holds h)
+        h_ = x
+    return y_, h_
 
 
 def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, h=None, y=None, y_scale=None,
