@@ -483,8 +483,8 @@ def _workspace_at(nbytes, device, workspace):
 def _op_fields(num_heads, head_v_dim, io_dtype, out_dtype):
     """The struct of these values (never written afterwards, so calls share it)."""
     c = KdaConfigC()
-    c.num_heads = num_heads
-    c.head_v_dim = head_v_dim
+    c.num_heads = _int32(num_heads)
+    c.head_v_dim = _int32(head_v_dim)
     c.io_dtype = _dtype_code(io_dtype)
     c.out_dtype = _dtype_code(out_dtype)
     return c
@@ -499,9 +499,17 @@ def _op_struct(cfg: Config):
     return ctypes.byref(c)
 
 
-# ctypes cuts an integer to its argument's width: a size above that is passed as
+# ctypes cuts an integer to its argument's width: a size beyond that is passed as
 # one that the library refuses
 _INT32_MAX = 2**31 - 1
+
+
+def _int32(n: int) -> int:
+    return max(-1, min(n, _INT32_MAX))
+
+
+def _int64(n: int) -> int:
+    return max(-1, min(n, 2**63 - 1))
 
 
 def _scale_blocks(k: int) -> int:
@@ -557,7 +565,8 @@ def kda_add_rmsnorm_fp8(cfg: Config, x, residual, weight, eps: float = 1e-6, *, 
 
 
 def kda_add_rmsnorm_backward_workspace_bytes(cfg: Config, n_tokens: int, hidden: int) -> int:
-    return int(_lib.kda_add_rmsnorm_backward_workspace_bytes(_op_struct(cfg), n_tokens, hidden))
+    """Bytes of workspace; 0 for sizes that the library refuses."""
+    return int(_lib.kda_add_rmsnorm_backward_workspace_bytes(_op_struct(cfg), _int64(n_tokens), _int32(hidden)))
 
 
 def kda_add_rmsnorm_backward(cfg: Config, h, weight, dy, d_h=None, eps: float = 1e-6, *, dx=None, workspace=None,
@@ -617,7 +626,8 @@ def kda_output_gate_fp8(cfg: Config, o, gate, o_norm_weight, eps: float = 1e-6, 
 
 
 def kda_output_gate_backward_workspace_bytes(cfg: Config, n_tokens: int) -> int:
-    return int(_lib.kda_output_gate_backward_workspace_bytes(_op_struct(cfg), n_tokens))
+    """Bytes of workspace; 0 for sizes that the library refuses."""
+    return int(_lib.kda_output_gate_backward_workspace_bytes(_op_struct(cfg), _int64(n_tokens)))
 
 
 def kda_output_gate_backward(cfg: Config, o, gate, o_norm_weight, dy, eps: float = 1e-6, *, workspace=None,
