@@ -116,11 +116,14 @@ __global__ __launch_bounds__(kEpiThreads) void output_gate_fp8_kernel(int64_t un
     ss = dpp_group_sum<DV / 8>(ss);
     float inv = rsqrt_precise(ss * (1.0f / DV) + eps);
     // heads narrower than a block have norms of their own inside it, and lanes
-    // past the row's end none (with eps = 0 it would be infinite)
+    // past the row's end none (with eps = 0 it would be infinite).  They are
+    // applied in front of the weight, so that o * weight stays in fp32's range;
+    // heads as wide as a block would need the norm's split of 1 / rms for that
+    // (131072 x 32 x 128: 454 us, without it 442)
     const float each = DV == kScaleBlock ? 1.0f : (mine ? inv : 0.0f);
     float t[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = ov[e] * wv[e] * sigmoidf_(gv[e]) * each;
+    for (int e = 0; e < 8; ++e) t[e] = ov[e] * each * wv[e] * sigmoidf_(gv[e]);
     float s;
     const uint2 q = quantise_block8(t, DV == kScaleBlock ? inv : 1.0f, &s);
     if (mine) {

@@ -110,15 +110,17 @@ __global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_kernel(
     }
     row_sums<L, 1>(ss, red, threadIdx.x >> 6, parity);
     const float inv = 1.0f / sqrtf(ss[0] * rcp + eps);
+    float m = inv;
+    const float up = OUT == Out::kFp8 ? split_power(m) : 1.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * L + lane;
       float t[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = hv[i][e] * wv[i][e];
       if constexpr (OUT == Out::kFp8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = hv[i][e] * up * wv[i][e];
         float s;
-        const uint2 q = quantise_block8(t, inv, &s);   // whole groups of 16 lanes: zeros past the row's end
+        const uint2 q = quantise_block8(t, m, &s);   // whole groups of 16 lanes: zeros past the row's end
         if (v < nvec) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(y) + base + static_cast<size_t>(v) * 8) = q;
           if ((lane & 15) == 0) scale[static_cast<size_t>(r) * nblk + (v >> 4)] = s;

@@ -107,13 +107,22 @@ __device__ __forceinline__ float dpp_group_sum(float x) {
   return x;
 }
 
+// x = 2^k m with m in [0.5, 1): returns 2^k and leaves m in x.  Infinity and NaN
+// stay in x, with 2^0; 0 gives 0 and 0.
+__device__ __forceinline__ float split_power(float& x) {
+  const float p = x == 0.0f ? 0.0f : __builtin_amdgcn_ldexpf(1.0f, __builtin_amdgcn_frexp_expf(x));
+  x = __builtin_amdgcn_frexp_mantf(x);
+  return p;
+}
+
 // The scale of the 128-channel block whose values m * t[e] sit 8 to a lane
 // over an aligned group of 16 lanes (every lane active; lanes past the row's
 // end hold zeros), and those 8 values as e4m3, rounded to nearest even:
-// s = max(amax |m t|, 1e-30) / 448, q = t * (448 / amax |t|).  m, the row's
-// 1 / rms (one value in every lane of the group), goes into the scale alone:
-// two roundings less per value than (m t) / s.  A NaN in the block makes its
-// scale NaN.
+// s = max(amax |m t|, 1e-30) / 448, q = t * (448 / amax |t|).  m (one value in
+// every lane of the group), the row's 1 / rms up to a power of two, goes into
+// the scale alone: two roundings less per value than (m t) / s.  The norm takes
+// the power into t, which so stays in fp32's range where m t does; heads of 128
+// pass 1 / rms itself.  A NaN in the block makes its scale NaN.
 __device__ __forceinline__ uint2 quantise_block8(const float (&t)[8], float m, float* scale) {
   uint32_t a = 0;
 #pragma unroll

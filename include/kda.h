@@ -467,6 +467,10 @@ kda_status_t kda_add_rmsnorm_backward(const kda_config_t *cfg, int64_t n_tokens,
  * that follows: a token's heads are one row of num_heads * head_v_dim values.
  *   y              [n_tokens][H * dv] e4m3
  *   y_scale        [n_tokens][ceil(H * dv / 128)] fp32
+ * With heads of 128, o * o_norm_weight has to stay inside fp32's range, else
+ * the block's scale is infinite or NaN (below 1e-38 it keeps a denormal's
+ * bits); narrower heads are normalised before the weight and have no such
+ * limit.  A row whose squares sum to more than 3.4e38 has y 0.
  * The other arguments as for kda_output_gate; nothing aliases.
  */
 kda_status_t kda_output_gate_fp8(const kda_config_t *cfg, int64_t n_tokens,

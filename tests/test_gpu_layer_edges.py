@@ -29,3 +29,37 @@ def test_norm_over_its_input_returns_no_h(kda):
     # an output of its own leaves x, and returns it
     y, h = kda.kda_add_rmsnorm(cfg, x, None, w, y=torch.empty_like(x))
     assert h is x and torch.equal(y, y0)
+
+
+@pytest.mark.parametrize("h_scale,w_scale,eps", [(1e17, 1e22, EPS), (1e-18, 1e-24, 1e-38), (1e12, 1e27, EPS)])
+def test_fp8_rows_whose_weighted_values_leave_fp32(kda, h_scale, w_scale, eps):
+    """h * weight passes fp32's range (or its normal numbers), h / rms * weight does not."""
+    r = Rand(62)
+    x, w = r(5, 392) * h_scale, r.weight(392) * w_scale
+    e = ref.rmsnorm(x, w, eps)
+    assert e.abs().max() < 1e38 and ref.block_scale(e).min() > 1e-30
+    q, s, _ = kda.kda_add_rmsnorm_fp8(make_cfg(kda, F32, F32), x, None, w, eps)
+    check_rows_fp8(q, s, e, ref.norm_chain(392) * U)
+    for d in (16, 32, 64):   # (the products o * weight of wider heads have a range of their own, see kda.h)
+        o, gate, ow = r(7, 3, d) * h_scale, r(7, 3, d), r.weight(d) * w_scale
+        q, s = kda.kda_output_gate_fp8(make_cfg(kda, F32, F32, 3, d), o, gate, ow, eps)
+        check_rows_fp8(q, s, ref.output_gate(o, gate, ow, eps).view(7, -1), (ref.norm_chain(d) + 22) * U)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_fp8_rows_whose_squares_leave_fp32(kda, io):
+    """The row's 1 / rms is 0 then, and so is its y, also where h * weight passes fp32's range; its neighbours stay."""
+    r = Rand(66)
+    x, w = r(4, 392, dtype=io), 1.25 + r.weight(392)
+    x[1] = torch.finfo(BF).min
+    x[2, ::3] = 1e20
+    cfg = make_cfg(kda, io, F32)
+    q, s, _ = kda.kda_add_rmsnorm_fp8(cfg, x, None, w)
+    y, _ = kda.kda_add_rmsnorm(cfg, x, None, w)
+    e = ref.rmsnorm(x, w, EPS)
+    check_rows_fp8(q[[0, 3]], s[[0, 3]], e[[0, 3]], ref.norm_chain(392) * U)
+    assert (y[1:3] == 0).all() and (q[1:3].float() == 0).all() and torch.isfinite(s).all()
+    o, gate, ow = r(4, 3, 32, dtype=io), r(4, 3, 32, dtype=io), 1.25 + r.weight(32)
+    o[1, 1] = torch.finfo(BF).min
+    q, s = kda.kda_output_gate_fp8(make_cfg(kda, io, io, 3, 32), o, gate, ow)
+    assert (q[1, 32:64].float() == 0).all() and torch.isfinite(s).all()
