@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kEpiThreads) void output_gate_bwd_kernel(int64_t ch
     float ss = 0.f, sg = 0.f, sig[8], off[8];   // off = 1 - sigmoid, exact also where the sigmoid is near 1
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float x = exp_fast(-gv[e]);
+      const float x = exp_precise_any(-gv[e]);
       sig[e] = rcp_fast(1.0f + x);
       off[e] = fminf(x, 1e38f) * sig[e];   // (an infinite x has sigmoid 0)
       ss = fmaf(ov[e], ov[e], ss);

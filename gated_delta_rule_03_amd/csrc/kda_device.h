@@ -69,6 +69,15 @@ __device__ __forceinline__ float exp_precise(float x) {
   return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.6931471805599453f, 1.0f);
 }
 
+// exp_precise for every x: infinities give infinity and 0, NaN stays NaN.
+__device__ __forceinline__ float exp_precise_any(float x) {
+  constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.925963033500011e-08f;
+  const float t = x * kLog2e;
+  // (within 1 but where t is far out or an infinity; of NaN the median is -1)
+  const float r = __builtin_amdgcn_fmed3f(fmaf(x, kLog2eLo, fmaf(x, kLog2e, -t)), -1.0f, 1.0f);
+  return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.6931471805599453f, 1.0f);
+}
+
 // 1/x through the hardware reciprocal (v_rcp_f32, 1 ulp).
 __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
 

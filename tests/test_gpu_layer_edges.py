@@ -63,3 +63,46 @@ def test_fp8_rows_whose_squares_leave_fp32(kda, io):
     o[1, 1] = torch.finfo(BF).min
     q, s = kda.kda_output_gate_fp8(make_cfg(kda, io, io, 3, 32), o, gate, ow)
     assert (q[1, 32:64].float() == 0).all() and torch.isfinite(s).all()
+
+
+@pytest.mark.parametrize("d", [16, 128])
+def test_output_gate_far_gates(kda, d):
+    """Gates of 64 to 85 and of -64 to -85, where a product x * log2(e) rounded to fp32 is off by 44 U in e^x.
+
+    Roundings on the way to d_gate, in U (half a step of fp32): the row's squares 8 + 4, the mean's eps 1, halved by the
+    root, the root 2 and the division 1: 1 / rms 10.  e^-gate 4 (2 ulp), 1 + x 1, the reciprocal 2: the sigmoid 7; one
+    minus it 4 + 7 + 1.  d_gate = dy sig w n (1 - sig): 7 + 11 + 12 and four products: 34.  Two more for the second
+    order."""
+    r = Rand(63)
+    n, H = 64, 4
+    o, w, dy = r(n, H, d), r.weight(d), r(n, H, d) * 1e6
+    far = 64 + 21 * torch.rand((n, H, d), generator=r.g, device="cuda")
+    gate = torch.where(r(n, H, d) < 0, far, -far)
+    d_o, d_gate, dw = kda.kda_output_gate_backward(make_cfg(kda, F32, F32, H, d), o, gate, w, dy, EPS)
+    e, _, ew, m, _, mw = ref.output_gate_backward(o, gate, w, dy, EPS)
+    eg = dy * ref.output_gate(o, gate, w, EPS) * torch.sigmoid(-gate.double())   # 1 - sigmoid(64) is 0 in 64 bits too
+    off = ((d_gate.double() - eg) / eg).abs()
+    assert off.max() <= 36 * U, f"d_gate {off.max() / U:.1f} U"
+    check(d_o, e, m, (2 * 36 + 8) * U, "d_o")
+    check(dw, ew, mw, (36 + 64 + 256) * U, "dw")
+
+
+def test_output_gate_backward_gates_at_the_ends(kda):
+    """The type's largest and lowest values, infinities and NaN as gates: the sigmoid is 0 or 1, both gradients of it 0."""
+    r = Rand(65)
+    n, H, d = 6, 2, 128
+    o, w, dy = r(n, H, d), r.weight(d), r(n, H, d)
+    ends = [3.4e38, -3.4e38, float("inf"), -float("inf"), 1e30, -1e30, 104.0, -104.0]
+    for dtype in (F32, BF):
+        gate = r(n, H, d)
+        gate[:, :, ::16] = torch.tensor(ends, device="cuda")
+        gate[5, 1, 3] = float("nan")
+        gate = gate.to(dtype)
+        assert dtype == F32 or gate[0, 0, 0] == torch.finfo(BF).max or torch.isinf(gate[0, 0, 0])
+        d_o, d_gate, dw = kda.kda_output_gate_backward(make_cfg(kda, dtype, F32, H, d), o, gate, w, dy, EPS)
+        assert (d_gate[:, :, ::16].abs() <= 1e-37).all() and torch.isnan(d_gate[5, 1, 3]) and torch.isnan(dw[3])
+        e, eg, _, m, mg, _ = ref.output_gate_backward(o, gate, w, dy, EPS)
+        rel = 2 * (ref.norm_chain(d) + 22) * U + 8 * U
+        check(d_o[:5], e[:5], m[:5], rel)
+        check(d_gate[:5], eg[:5], mg[:5], rel)
+        assert torch.isfinite(d_o[5, 0]).all() and torch.isnan(d_o[5, 1]).all()
