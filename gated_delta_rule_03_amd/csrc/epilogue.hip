@@ -176,7 +176,8 @@ __global__ __launch_bounds__(kEpiThreads) void output_gate_bwd_kernel(int64_t ch
     ss = dpp_group_sum<kLanes>(ss);
     sg = dpp_group_sum<kLanes>(sg);
     const float inv = 1.0f / sqrtf(ss * (1.0f / DV) + eps);
-    const float k = sg * (1.0f / DV) * inv * inv;   // n * mean(g n) = o * k
+    // n * mean(g n) = o * k; 0 where the squares pass fp32's range, as n is
+    const float k = inv == 0.f ? 0.f : sg * (1.0f / DV) * inv * inv;
     float a[8], b[8];
     if (mine) {
 #pragma unroll

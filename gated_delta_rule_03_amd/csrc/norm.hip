@@ -179,7 +179,8 @@ __global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_bwd_kernel(
     }
     row_sums<L, 2>(s, red, threadIdx.x >> 6, parity);
     const float inv = 1.0f / sqrtf(s[0] * rcp + eps);
-    const float c = s[1] * rcp * inv * inv;   // n * mean(g n) = h * c
+    // n * mean(g n) = h * c; 0 where the squares pass fp32's range, as n is, and not an infinite sum times 0
+    const float c = inv == 0.f ? 0.f : s[1] * rcp * inv * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * L + lane;

@@ -106,3 +106,30 @@ def test_output_gate_backward_gates_at_the_ends(kda):
         check(d_o[:5], e[:5], m[:5], rel)
         check(d_gate[:5], eg[:5], mg[:5], rel)
         assert torch.isfinite(d_o[5, 0]).all() and torch.isnan(d_o[5, 1]).all()
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_backward_rows_whose_squares_leave_fp32(kda, io):
+    """y is 0 on such a row whatever its values are: its gradients are 0, and d_h passes through; the others stay."""
+    r = Rand(67)
+    h, w, dy, d_h = r(5, 392, dtype=io), 1.25 + r.weight(392), r(5, 392, dtype=F32), r(5, 392)
+    h[1] = torch.finfo(BF).min
+    h[2, ::3] = 1e38
+    fine = [0, 3, 4]
+    dx, dw = kda.kda_add_rmsnorm_backward(make_cfg(kda, io, F32), h, w, dy, d_h, EPS)
+    e, edw, m, mdw = ref.rmsnorm_backward(h[fine], w, dy[fine], d_h[fine], EPS)
+    rel = 2 * ref.norm_chain(392) * U + 8 * U
+    check(dx[fine], e, m, rel, "dx")
+    check(dw, edw, mdw, rel + 100 * U, "dw")
+    assert torch.equal(dx[1:3], d_h[1:3])
+    for d in (32, 128):
+        o, gate, ow, dz = r(5, 2, d, dtype=io), r(5, 2, d), 1.25 + r.weight(d), r(5, 2, d, dtype=io)
+        o[1] = torch.finfo(BF).min
+        d_o, d_gate, dw = kda.kda_output_gate_backward(make_cfg(kda, F32, io, 2, d), o, gate, ow, dz, EPS)
+        keep = [0, 2, 3, 4]
+        e, eg, ew, m, mg, mw = ref.output_gate_backward(o[keep], gate[keep], ow, dz[keep], EPS)
+        rel = 2 * (ref.norm_chain(d) + 22) * U + 8 * U
+        check(d_o[keep], e, m, rel, "d_o")
+        check(d_gate[keep], eg, mg, rel, "d_gate")
+        check(dw, ew, mw, rel + 300 * U, "d_weight")
+        assert (d_o[1] == 0).all() and (d_gate[1] == 0).all()
