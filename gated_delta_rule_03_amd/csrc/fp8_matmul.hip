@@ -209,14 +209,17 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_matmul_rows_kernel(
 //
 // The loads are written in assembly (they have no register output): the
 // compiler's own form of them makes every later LDS read wait for all of
-// them.  Their order against the LDS reads is the barrier below.  m0 is
-// reserved: the compiler keeps nothing in it; a load that reads it needs one
-// wait state behind a scalar write of it (s_nop 0), and five behind a vector
-// instruction that wrote its scalar address, which the compiler does not count
-// in front of assembly (s_nop 4).  The first form is COUNT loads
+// them.  Their order against the LDS reads is the barrier below.  m0 is named
+// as written, so that no value of the compiler's own is carried across in it
+// (its warning about that says only that it never allocates m0).  A load that
+// reads m0 needs one wait state behind a scalar write of it (s_nop 0), and five
+// behind a vector instruction that wrote its scalar address, which the compiler
+// does not count in front of assembly (s_nop 4).  The first form is COUNT loads
 // where k < end, to LDS `step` bytes apart; its branch is inside the assembly
 // so that the products around it stay one block of code, whose registers the
 // compiler can place (with a branch of its own it spills).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int COUNT, int STEP>
 __device__ __forceinline__ void load_lds16_if(int k, int end, uint32_t lds, const uint32_t* voff, const uint8_t* base) {
   static_assert(COUNT == 1 || COUNT == 2 || COUNT == 4, "");
@@ -229,20 +232,22 @@ __device__ __forceinline__ void load_lds16_if(int k, int end, uint32_t lds, cons
   if constexpr (COUNT == 4)
     asm volatile(KDA_LDS_FIRST KDA_LDS_NEXT("%6") KDA_LDS_NEXT("%7") KDA_LDS_NEXT("%8") ".Lskip%=:" ::"s"(k), "s"(end),
                  "s"(lds), "s"(base), "n"(STEP), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3])
-                 : "memory", "scc");
+                 : "memory", "scc", "m0");
   else if constexpr (COUNT == 2)
     asm volatile(KDA_LDS_FIRST KDA_LDS_NEXT("%6") ".Lskip%=:" ::"s"(k), "s"(end), "s"(lds), "s"(base), "n"(STEP),
                  "v"(voff[0]), "v"(voff[1])
-                 : "memory", "scc");
+                 : "memory", "scc", "m0");
   else
     asm volatile(KDA_LDS_FIRST ".Lskip%=:" ::"s"(k), "s"(end), "s"(lds), "s"(base), "n"(STEP), "v"(voff[0])
-                 : "memory", "scc");
+                 : "memory", "scc", "m0");
 #undef KDA_LDS_FIRST
 #undef KDA_LDS_NEXT
 }
 __device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, const void* base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base)
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Every load of this wave has landed and its LDS reads are done; then every
 // wave's.

@@ -2,6 +2,7 @@
 rule, compiled on the host, has to give the sizes of tests/product_shapes.py
 the kernels that they are there for, and every kernel has to have a size."""
 import os
+import re
 import subprocess
 
 import pytest
@@ -66,3 +67,13 @@ def test_parts_of_k_are_equal_and_whole(ask):
              for k in (16, 496, 512, 1000 - 8, 1024, 1040, 1152, 2048, 4096, 4112, 7680)]
     for (_, m, n, k), (_, _, split, _) in zip(sizes, ask(sizes)[1]):
         assert split <= 1 or (k % (128 * split) == 0 and k // 128 >= 4 * split), (m, n, k)
+
+
+def test_inline_assembly_names_m0():
+    """Assembly that writes m0 says so to the compiler."""
+    for name in sorted(os.listdir(CSRC)):
+        src = open(os.path.join(CSRC, name)).read()
+        for m in re.finditer(r"\basm(?: volatile)?\((.*?)\);", src, re.S):
+            if "m0" in m.group(1) or "KDA_LDS_FIRST" in m.group(1):
+                clobbers = m.group(1).rsplit(":", 1)[1]
+                assert '"m0"' in clobbers, f"{name}: {m.group(0)[:90]}"
