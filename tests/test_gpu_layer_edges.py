@@ -1,10 +1,12 @@
 """The operators around the core where a value, an alias or an order is at its
-edge."""
+edge: weighted values beyond fp32 that the row's norm brings back, gates far
+out, an output over its input, products that cancel."""
 import pytest
 import torch
 
 from tests import layer_reference as ref
 from tests.layer_reference import U, check, check_rows_fp8
+from tests.product_shapes import BF16
 from tests.test_gpu_layer import BF, EPS, F8, F32, Rand, kda, make_cfg  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
@@ -92,13 +94,12 @@ def test_output_gate_backward_gates_at_the_ends(kda):
     r = Rand(65)
     n, H, d = 6, 2, 128
     o, w, dy = r(n, H, d), r.weight(d), r(n, H, d)
-    ends = [3.4e38, -3.4e38, float("inf"), -float("inf"), 1e30, -1e30, 104.0, -104.0]
     for dtype in (F32, BF):
+        top = torch.finfo(dtype).max
         gate = r(n, H, d)
-        gate[:, :, ::16] = torch.tensor(ends, device="cuda")
+        gate[:, :, ::16] = torch.tensor([top, -top, float("inf"), -float("inf"), 1e30, -1e30, 104.0, -104.0], device="cuda")
         gate[5, 1, 3] = float("nan")
         gate = gate.to(dtype)
-        assert dtype == F32 or gate[0, 0, 0] == torch.finfo(BF).max or torch.isinf(gate[0, 0, 0])
         d_o, d_gate, dw = kda.kda_output_gate_backward(make_cfg(kda, dtype, F32, H, d), o, gate, w, dy, EPS)
         assert (d_gate[:, :, ::16].abs() <= 1e-37).all() and torch.isnan(d_gate[5, 1, 3]) and torch.isnan(dw[3])
         e, eg, _, m, mg, _ = ref.output_gate_backward(o, gate, w, dy, EPS)
@@ -133,3 +134,95 @@ def test_backward_rows_whose_squares_leave_fp32(kda, io):
         check(d_gate[keep], eg, mg, rel, "d_gate")
         check(dw, ew, mw, rel + 300 * U, "d_weight")
         assert (d_o[1] == 0).all() and (d_gate[1] == 0).all()
+
+
+# ---- the product's sums --------------------------------------------------------
+
+def exponent(v):
+    """The power of two of an e4m3 value; -6, that of its smallest normal numbers, for those below and for 0."""
+    return (torch.frexp(v.float())[1] - 1).clamp(min=-6)
+
+
+def cut_bound(a, a_scale, w, w_scale):
+    """What an e4m3 step may lose of each output.  The step sums the products of 8 neighbouring channels in units of 2^-13
+    of the power of two of the largest of them (of their exponents' sum); what lies below a unit is cut.  The largest
+    loses nothing, so a group loses less than 7 units."""
+    k = a.shape[1]
+    ea, ew = exponent(a), exponent(w)
+    bound = torch.zeros((a.shape[0], w.shape[0]), dtype=torch.float64, device=a.device)
+    for g in range(0, k, 8):
+        top = (ea[:, None, g:g + 8] + ew[None, :, g:g + 8]).amax(-1).double()
+        bound += 7 * torch.exp2(top - 13) * (a_scale[:, g // 128].double()[:, None] * w_scale[:, g // 128].double()[None])
+    return bound
+
+
+def outliers(r, M, N, K):
+    """Operands with three channels 50 times larger in each block, two of which cancel in every output exactly."""
+    a, w = r(M, K), r(N, K)
+    for b in range(0, K, 128):
+        a[:, b + 3] *= 50
+        a[:, b + 9] *= 50
+        w[:, b + 3] *= 4
+    sa = ref.block_scale(a)
+    qa = (a / sa.repeat_interleave(128, -1)[:, :K]).to(F8)
+    wq, sw = ref.quantise_weight(w)
+    one, other = list(range(3, K, 128)), [min(b + 12, K - 1) for b in range(0, K, 128)]
+    a8, w8 = qa.view(torch.uint8), wq.view(torch.uint8)
+    a8[:, other] = a8[:, one]
+    w8[:, other] = w8[:, one] ^ 0x80
+    return qa, sa, wq, sw
+
+
+@pytest.mark.parametrize("M,N,K", [s for ss in BF16.values() for s in ss[:1] if s[2] > 16] + [(1, 500, 4112), (7, 4000, 272)])
+def test_product_of_outliers_that_cancel(kda, M, N, K):
+    """Fp32 outputs keep fp32's sums; bf16 outputs stay within what an e4m3 step cuts."""
+    a, sa, w, sw = outliers(Rand(M + N), M, N, K)
+    rows = sorted({*range(min(M, 40)), *range(max(0, M - 24), M)})
+    cols = sorted({*range(min(N, 140)), *range(max(0, N - 60), N)})
+    ra, rs = a.float()[rows], sa[rows]
+    rw, rws = w.float()[cols], sw.repeat_interleave(128, 0)[cols]
+    x = ra.double() * rs.double().repeat_interleave(128, -1)[:, :K]
+    z = rw.double() * rws.double().repeat_interleave(128, -1)[:, :K]
+    e, m = x @ z.T.contiguous(), x.abs() @ z.abs().T.contiguous()
+    lim = (min(K, 128) + (K + 127) // 128 + 19) * U * m
+    y = kda.kda_fp8_matmul(make_cfg(kda, out=F32), a, sa, w, sw)
+    check(y[rows][:, cols], e, lim, 1.0, "fp32")
+    y = kda.kda_fp8_matmul(make_cfg(kda), a, sa, w, sw)
+    check(y[rows][:, cols], e, lim + cut_bound(ra, rs, rw, rws), 1.0, "bf16")
+
+
+@pytest.mark.parametrize("M,N", [(1, 40), (300, 520), (5337, 5563)])
+@pytest.mark.parametrize("at", [(0, 1), (5, 100)])
+def test_product_of_two_large_values_that_cancel(kda, M, N, at):
+    """448 * 448 - 448 * 448 + 126 ones: 126 in fp32.  In an e4m3 step the ones beside a large product, in its group of 8
+    channels, lie below its unit (2^(8 + 8 - 13) = 8) and are cut; the others stay."""
+    a, w = torch.ones(M, 128, device="cuda"), torch.ones(N, 128, device="cuda")
+    a[:, at[0]] = a[:, at[1]] = w[:, at[0]] = 448
+    w[:, at[1]] = -448
+    one = lambda n: torch.ones(n, 1, device="cuda")   # noqa: E731
+    args = (a.to(F8), one(M), w.to(F8), one(-(-N // 128)))
+    assert (kda.kda_fp8_matmul(make_cfg(kda, out=F32), *args) == 126).all()
+    assert (kda.kda_fp8_matmul(make_cfg(kda), *args) == (120 if at[0] // 8 == at[1] // 8 else 112)).all()
+
+
+def test_product_bf16_loss_by_data(kda):
+    """The loss of bf16 outputs on Gaussian operands, and with two channels in 128 up to a hundred times larger.  A value
+    off by c before its rounding ends at most 2 c further from its exact value than the nearest bf16 value is."""
+    r = Rand(64)
+    M, N, K = 600, 520, 1024
+    for k in (1, 5, 20, 100):
+        a = r(M, K)
+        a.view(M, -1, 128)[:, :, :2] *= k
+        sa = ref.block_scale(a)
+        q = (a / sa.repeat_interleave(128, -1)).to(F8)
+        wq, sw = ref.quantise_weight(r(N, K))
+        y = kda.kda_fp8_matmul(make_cfg(kda), q, sa, wq, sw).double()
+        x, z = ref.dequantised(q, sa), ref.dequantised(wq, sw, 128)
+        e, m = x @ z.T.contiguous(), x.abs() @ z.abs().T.contiguous()
+        nearest = e.to(BF).double()
+        cut = cut_bound(q.float(), sa, wq.float(), sw.repeat_interleave(128, 0)[:N]) + (128 + 8 + 19) * U * m
+        off, best, most = ((y - e).norm() / e.norm()).item(), ((nearest - e).norm() / e.norm()).item(), (cut.norm() / e.norm()).item()
+        print(f"outliers x {k}: off by {off:.6e}, rounding alone {best:.6e}, not the nearest "
+              f"{(y != nearest).double().mean().item():.4f}, the cut's bound {most:.2e}", flush=True)
+        assert off <= best + 2 * most
+        assert ((y - e).abs() <= (nearest - e).abs() + 2 * cut).all()
