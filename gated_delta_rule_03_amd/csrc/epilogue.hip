@@ -80,7 +80,11 @@ hipError_t launch_output_gate(int D, int64_t rows, const void* o, const void* ga
 // (whole heads: dv divides 128) with one scale each.  16 lanes hold a block,
 // 8 channels a lane, so dv / 8 lanes sum a head's squares and all 16 the
 // block's largest value, all in DPP steps.  HBM-bound: 131072 x 32 x 128 in
-// bf16 takes 437 us, 6.2 TB/s; 256 tokens 3.4 us, the launch and one trip to memory.
+// bf16 takes 437 to 445 us, 6.1 TB/s; 256 tokens 3.4 us, the launch and one
+// trip to memory.  The sigmoid takes the fast exponential, as the plain epilogue
+// does: what that is off by at far gates (65 half steps of fp32 at 85) reaches
+// the fp32 scale where all gates of a block are far out, and no e4m3 value by
+// more than 2e-4 of its step (the precise one takes 6 us more).
 template <int DV, bool O_BF16, bool G_BF16>
 __global__ __launch_bounds__(kEpiThreads) void output_gate_fp8_kernel(int64_t units, int row, const void* o,
                                                                       const void* gate, const float* __restrict__ w,
@@ -140,7 +144,9 @@ __global__ __launch_bounds__(kEpiThreads) void output_gate_fp8_kernel(int64_t un
 // One pass over the rows, 8 channels a lane.  A lane keeps its channels for
 // the whole launch, so dw gathers in registers; a workgroup joins its lanes
 // in LDS and leaves one row of `part`.  The order of every sum is fixed.
-// HBM-bound: 32768 x 32 x 128 in bf16 takes 298 us with the join, 5.4 TB/s.
+// The exponential is the precise one, for the fp32 gradient of far gates (2 us
+// more).  HBM-bound: 32768 x 32 x 128 in bf16 takes 300 us with the join, 5.4
+// TB/s.
 template <int DV, bool O_BF16, bool G_BF16>
 __global__ __launch_bounds__(kEpiThreads) void output_gate_bwd_kernel(int64_t chunks, const void* __restrict__ o,
                                                                       const void* __restrict__ gate,

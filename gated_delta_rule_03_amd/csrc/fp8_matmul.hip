@@ -40,8 +40,9 @@ __device__ __forceinline__ bf16x8 widen(int lo, int hi) {
 // of the largest (by the operands' exponents, -6 for subnormal ones; products
 // of 0 do not count), each cut to whole units; the sums of the eights keep
 // fp32's bits, rounded down (measured value by value).  An eight loses less
-// than 7 units, so a row at most 7 * 2^-13 < 2^-10 of the sum of |a w|, against
-// the 2^-8 that half a step of bf16 is; on Gaussian operands 1.3e-5 of the
+// than 7 units, so a row at most 7 * 2^-13 < 2^-10 of the sum of |a w| (2^-7 in
+// an eight whose largest product has a subnormal operand), against the 2^-8
+// that half a step of bf16 is; on Gaussian operands 1.3e-5 of the
 // result's norm, with two channels in 128 a hundred times larger 4.2e-5, 1 / 130
 // and 1 / 40 of what the rounding to bf16 costs.  For fp32 outputs the operands
 // are widened to bf16, which holds every e4m3 value, and multiplied in four

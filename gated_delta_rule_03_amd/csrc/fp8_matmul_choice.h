@@ -28,7 +28,10 @@ constexpr int tile_groups(int TN, int TT, int waves) {
 // where the last load costs `one` with at most a workgroup a CU, up to `full`
 // with `per`.  The figures (ns) are a fit to 583 sizes of 17 to 8000 tokens,
 // 256 to 16416 outputs and 512 to 8192 channels: the kernel that they pick
-// takes 1.1% longer than the fastest one on average (1.0% with fp32 outputs).
+// takes 1.1% longer than the fastest of them on average (1.0% with fp32
+// outputs).  A rows kernel of 16 outputs x 32 tokens is not among them, which
+// is up to 22% faster for 17 to 32 tokens (17 x 4096 x 8192: 12.4 us, here 15.7;
+// 17 x 4096 x 4096: 7.65, here 8.6).
 //
 // What they say: the rows kernel is the fastest while its workgroups are few
 // (32 tokens, 4096 x 4096, bf16: 8.6 us, tiles 11.9; fp32, 200 tokens, 1024 x

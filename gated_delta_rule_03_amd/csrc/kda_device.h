@@ -54,8 +54,9 @@ __device__ __forceinline__ void st2(void* p, size_t i, float2 x) {
   }
 }
 
-// e^x through the hardware base-2 exponential (v_exp_f32): a few ulp, no
-// range-reduction sequence.  Underflows to 0 below about -87.
+// e^x through the hardware base-2 exponential (v_exp_f32), no range-reduction
+// sequence: off by an ulp and up to 1.3 half steps for each unit of |x|.
+// Underflows to 0 below about -87.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 
 // e^x to about 2 ulp over the whole fp32 range: the rounding residual of

@@ -8,7 +8,8 @@
 //   dw = sum over tokens of dy * n
 //
 // HBM-bound: each row is read once and kept in registers between the row's
-// sums and its outputs.  A row belongs to L lanes (16, 32 or whole waves), 8
+// sums and its outputs (but for the backward's rows of more than 16384 channels,
+// below).  A row belongs to L lanes (16, 32 or whole waves), 8
 // channels a lane and step (16-byte loads in bf16), NV steps; 16 lanes hold
 // one scale block, so its largest value is four DPP steps.
 // 131072 x 4096 in bf16 with a residual and e4m3 out: 655 us, 5.8 TB/s (a large
@@ -138,6 +139,10 @@ __global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_kernel(
 // row of `part` per workgroup.  Rows go to the workgroups by a rule on the
 // sizes alone and the sums are joined in a fixed order, so dw is the same in
 // every run.  32768 x 4096 in bf16 with d_h: 280 us with the join, 5.7 TB/s.
+// Above 16384 channels the 128 values a lane of h, dy, w and dw do not fit the
+// 128 registers that 1024 lanes leave it: 131 to 133 are spilled, and the pass
+// runs at half the rate (TB/s at 16384 / 16392 / 32768 channels: bf16 5.3 / 2.5 / 2.8,
+// fp32 5.0 / 3.1 / 3.1; the forward 5.6 / 5.3 / 5.4 and 5.0 / 5.3 / 5.3).
 template <bool H_BF16, bool DY_BF16, int L, int NV>
 __global__ __launch_bounds__(threads_of(L)) void add_rmsnorm_bwd_kernel(
     int64_t n_rows, int hidden, const void* __restrict__ h, const float* __restrict__ w, float eps,

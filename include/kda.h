@@ -132,7 +132,11 @@ typedef struct kda_config {
     void **stage_events;
 } kda_config_t;
 
-/* Library version, major*10000 + minor*100 + patch. */
+/* Library version, major*10000 + minor*100 + patch.  The operators around the
+ * core (kda_add_rmsnorm and those after it) came without a new one: a caller
+ * that opens the library at run time looks for their symbols.  The arrays of
+ * stage_events that callers of the core made for 7 stages stay valid for its
+ * calls, which record no others. */
 int32_t kda_version(void);
 
 /* Human-readable name of a status code (static storage). */
@@ -448,7 +452,8 @@ kda_status_t kda_add_rmsnorm_fp8(const kda_config_t *cfg, int64_t n_tokens, int3
  *   d_h            [n_tokens][hidden] fp32: the gradient that reaches h by the
  *                  residual stream, or NULL (zero)
  *   dx             [n_tokens][hidden] fp32: the gradient of x, and of residual
- *                  alike; may alias d_h
+ *                  alike; may alias d_h.  On a row whose squares sum to more
+ *                  than 3.4e38 (its y is 0) it is d_h
  *   dweight        [hidden] fp32; zeros when n_tokens == 0
  *   workspace      kda_add_rmsnorm_backward_workspace_bytes(); calls that
  *                  overlap in time need one each
@@ -524,13 +529,14 @@ kda_status_t kda_output_gate_backward(const kda_config_t *cfg, int64_t n_tokens,
  * power of two of the largest (an operand below 2^-6 counting as one of 2^-6),
  * what lies below a unit is cut, and the sums of the eights are added in fp32.
  * An eight so loses less than 7 units: over a row at most 2^-10 of the sum of
- * |a w|, a quarter of half a step of bf16.  That is not small against the
- * result where large products cancel: 448 * 448 - 448 * 448 + 126 ones gives
- * 112 or 120.  Measured against the result's norm, in front of the rounding to
- * bf16 (1.7e-3): 1.3e-5 on Gaussian operands, 4.2e-5 with two channels in 128
- * a hundred times larger; 1.1% to 2.8% of the values are then a neighbour of
- * the nearest bf16 value.  A caller who needs fp32's sums on any operands takes
- * y in fp32 and rounds it.
+ * |a w|, a quarter of half a step of bf16 (2^-7 in an eight whose largest
+ * product has an operand below 2^-6).  That is not small against the result
+ * where large products cancel: 448 * 448 - 448 * 448 + 126 ones gives 112 or
+ * 120.  Measured against the result's norm, in front of the rounding to bf16
+ * (1.7e-3): 1.3e-5 on Gaussian operands, 4.2e-5 with two channels in 128 a
+ * hundred times larger; 1.1% to 2.8% of the values are then a neighbour of the
+ * nearest bf16 value.  A caller who needs fp32's sums on any operands takes y
+ * in fp32 and rounds it.
  */
 kda_status_t kda_fp8_matmul(const kda_config_t *cfg, int64_t M, int32_t N, int32_t K,
                             const void *a, const float *a_scale,
