@@ -16,6 +16,9 @@ Entry points (same names as the C ABI):
   kda_add_rmsnorm_fp8 / kda_output_gate_fp8        the norm / the epilogue with e4m3 rows and block scales
   kda_add_rmsnorm_backward / kda_output_gate_backward
   kda_fp8_matmul(cfg, a, a_scale, w, w_scale)      a projection of e4m3 rows
+  kda_qk_norm_rope(cfg, rope, q, k, ...)           norm and rotation of query and key heads; kda_qk_norm_rope_backward
+  kda_append_kv(cfg, cache, ...) / kda_read_kv     a paged 4-bit cache of keys and values
+  kda_paged_attention(cfg, cache, q, ...)          attention of the newest tokens over it
   kda_prefill_workspace_bytes / kda_varlen_workspace_bytes / kda_prefill_slab_workspace_bytes
 """
 from __future__ import annotations
@@ -48,7 +51,7 @@ FLAG_RAW_BETA = 1 << 3
 FLAG_BETA_X2 = 1 << 4
 
 STAGES = ("chunk_table", "chunk_prep", "chunk_scan", "conv_state", "decode", "output_gate", "backward", "norm",
-          "matmul")
+          "matmul", "rope", "cache", "attention")
 NUM_STAGES = len(STAGES)
 
 EXPORTED = ("kda_version", "kda_status_string", "kda_prefill_workspace_bytes", "kda_prefill",
@@ -57,7 +60,9 @@ EXPORTED = ("kda_version", "kda_status_string", "kda_prefill_workspace_bytes", "
             "kda_varlen_backward_workspace_bytes", "kda_varlen_backward", "kda_prefill_slab_workspace_bytes",
             "kda_add_rmsnorm", "kda_add_rmsnorm_fp8", "kda_add_rmsnorm_backward_workspace_bytes",
             "kda_add_rmsnorm_backward", "kda_output_gate_fp8", "kda_output_gate_backward_workspace_bytes",
-            "kda_output_gate_backward", "kda_fp8_matmul")
+            "kda_output_gate_backward", "kda_fp8_matmul", "kda_qk_norm_rope",
+            "kda_qk_norm_rope_backward_workspace_bytes", "kda_qk_norm_rope_backward", "kda_append_kv", "kda_read_kv",
+            "kda_paged_attention_workspace_bytes", "kda_paged_attention")
 
 # consecutive values of an e4m3 row that share a scale
 SCALE_BLOCK = 128
@@ -91,6 +96,18 @@ class KdaConfigC(ctypes.Structure):
         ("conv_w_v", ctypes.c_void_p),
         ("stage_events", ctypes.c_void_p),
     ]
+
+
+class KdaRopeC(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("axis", ctypes.c_void_p)]
+
+
+class KdaKvCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p)]
 
 
 def _load_library():
@@ -148,6 +165,21 @@ def _load_library():
     lib.kda_output_gate_backward.argtypes = [cfgp, i64, vp, vp, vp, f32, vp, vp, vp, vp, vp, sz, vp]
     lib.kda_fp8_matmul.restype = ctypes.c_int
     lib.kda_fp8_matmul.argtypes = [cfgp, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+    ropep, cachep = ctypes.POINTER(KdaRopeC), ctypes.POINTER(KdaKvCacheC)
+    lib.kda_qk_norm_rope.restype = ctypes.c_int
+    lib.kda_qk_norm_rope.argtypes = [cfgp, ropep, i64, i32, vp, i64, vp, i64, vp, vp, f32, vp, vp, vp, vp]
+    lib.kda_qk_norm_rope_backward_workspace_bytes.restype = sz
+    lib.kda_qk_norm_rope_backward_workspace_bytes.argtypes = [cfgp, i64, i32]
+    lib.kda_qk_norm_rope_backward.restype = ctypes.c_int
+    lib.kda_qk_norm_rope_backward.argtypes = [cfgp, ropep, i64, i32, vp, i64, vp, i64, vp, vp, f32] + [vp] * 7 + [sz, vp]
+    lib.kda_append_kv.restype = ctypes.c_int
+    lib.kda_append_kv.argtypes = [cfgp, ropep, cachep, i32, i64, vp, i64, vp, i64, vp, f32, vp, vp]
+    lib.kda_read_kv.restype = ctypes.c_int
+    lib.kda_read_kv.argtypes = [cfgp, cachep, i32, i64, vp, vp, vp]
+    lib.kda_paged_attention_workspace_bytes.restype = sz
+    lib.kda_paged_attention_workspace_bytes.argtypes = [cfgp, i32, i32, i64, i32]
+    lib.kda_paged_attention.restype = ctypes.c_int
+    lib.kda_paged_attention.argtypes = [cfgp, cachep, i32, i64, i32, vp, f32, vp, vp, vp, sz, vp]
     return lib
 
 
@@ -669,3 +701,264 @@ def kda_fp8_matmul(cfg: Config, a, a_scale, w, w_scale, *, y=None, stream=None):
     _check(_lib.kda_fp8_matmul(_op_struct(cfg), math.prod(lead), min(N, _INT32_MAX), min(K, _INT32_MAX), ap, sp, wp, wsp,
                                yp if y_ is y else y_.data_ptr(), st), "kda_fp8_matmul")
     return y_
+
+
+# ---- the full-attention layers ----------------------------------------------
+
+# channels of a head that share a scale in the cache, and the page sizes it can have
+KV_BLOCK = 32
+PAGE_SIZES = (32, 64, 128, 256)
+
+
+@dataclass(frozen=True, eq=False)
+class Rope:
+    """A rotation of the first 2 * len(inv_freq) channels of a head: pair i
+    turns by positions[axis[i]] * inv_freq[i] (axis None: one axis).  Pair i is
+    channels (i, i + len(inv_freq)), or (2 i, 2 i + 1) when interleaved."""
+    inv_freq: torch.Tensor                    # [pairs] fp32, on the GPU; pairs a multiple of 8
+    axis: Optional[torch.Tensor] = None       # [pairs] int32
+    num_axes: int = 1
+    interleaved: bool = False
+
+    def __post_init__(self):
+        n, dev = self.inv_freq.numel(), self.inv_freq.device
+        c = KdaRopeC(2 * n, int(self.interleaved), _int32(self.num_axes), _at("inv_freq", self.inv_freq, (n,), torch.float32, dev),
+                     _at("axis", self.axis, (n,), torch.int32, dev))
+        object.__setattr__(self, "_c", c)     # (frozen: the tensors it points to stay)
+
+    @classmethod
+    def build(cls, rotary_dim: int, theta: float = 10000.0, sections=None, interleaved: bool = False, device="cuda"):
+        """The usual frequencies theta^(-2 i / rotary_dim).  sections: pairs of
+        each position axis, in order (their sum is rotary_dim / 2)."""
+        half = rotary_dim // 2
+        inv_freq = (float(theta) ** (-torch.arange(half, dtype=torch.float64) / max(half, 1))).float().to(device)
+        if sections is None:
+            return cls(inv_freq, interleaved=interleaved)
+        if sum(sections) != half:
+            raise ValueError("the sections have to add up to rotary_dim / 2 pairs")
+        axis = torch.repeat_interleave(torch.arange(len(sections), dtype=torch.int32), torch.tensor(list(sections)))
+        return cls(inv_freq, axis.to(device), len(sections), interleaved)
+
+
+@dataclass(frozen=True, eq=False)
+class KvCache:
+    """A paged cache of 4-bit keys and values (layout in include/kda.h)."""
+    k: torch.Tensor          # [num_pages, num_kv_heads, page_size, d / 2] uint8
+    k_scale: torch.Tensor    # [num_pages, num_kv_heads, d / 32, page_size] uint8
+    v: torch.Tensor
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        dev, u8 = self.k.device, torch.uint8
+        if self.k.dim() != 4 or self.k.shape[3] % (KV_BLOCK // 2):
+            raise ValueError("k must be [num_pages, num_kv_heads, page_size, d / 2]")
+        pages, heads, size, half = self.k.shape
+        scales = (pages, heads, 2 * half // KV_BLOCK, size)
+        c = KdaKvCacheC(_at("k", self.k, self.k.shape, u8, dev), _at("k_scale", self.k_scale, scales, u8, dev),
+                        _at("v", self.v, self.k.shape, u8, dev), _at("v_scale", self.v_scale, scales, u8, dev),
+                        _int32(pages), _int32(size), _int32(heads))
+        object.__setattr__(self, "_c", c)
+
+    @classmethod
+    def empty(cls, num_pages: int, num_kv_heads: int, head_dim: int, page_size: int = 64, device="cuda"):
+        """A cache of zeros."""
+        t = lambda *shape: torch.zeros((num_pages, num_kv_heads, *shape), dtype=torch.uint8, device=device)
+        return cls(t(page_size, head_dim // 2), t(head_dim // KV_BLOCK, page_size),
+                   t(page_size, head_dim // 2), t(head_dim // KV_BLOCK, page_size))
+
+
+@functools.lru_cache(maxsize=64)
+def _attention_fields(num_heads, head_k_dim, head_v_dim, io_dtype, out_dtype):
+    c = KdaConfigC()
+    c.num_heads, c.head_k_dim, c.head_v_dim = _int32(num_heads), _int32(head_k_dim), _int32(head_v_dim)
+    c.io_dtype, c.out_dtype = _dtype_code(io_dtype), _dtype_code(out_dtype)
+    return c
+
+
+def _attention_struct(cfg: Config):
+    """The fields of the config that these operators read."""
+    c = _attention_fields(cfg.num_heads, cfg.head_k_dim, cfg.head_v_dim, cfg.io_dtype, cfg.out_dtype)
+    if cfg.stage_events is not None:
+        c = KdaConfigC.from_buffer_copy(c)
+        c.stage_events = ctypes.cast(cfg.stage_events, ctypes.c_void_p)
+    return ctypes.byref(c)
+
+
+def _rows_at(name, t, shape, dtype, device):
+    """(address, row stride) of a tensor whose rows are contiguous: its leading axis may be strided."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}, "
+                         f"not {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+    row = shape[1] * shape[2]
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    s = t.stride()
+    if (s[2] != 1 and shape[2] > 1) or (s[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), s[0]
+
+
+def _rope_at(rope, positions, n, device):
+    """(pointer to the struct or None, address of the positions)."""
+    if rope is None:
+        return None, None
+    if rope.inv_freq.device != device:
+        raise ValueError(f"rope must be on {device}")
+    if positions is not None and positions.dim() == 1 and rope.num_axes == 1:
+        positions = positions[None]
+    return ctypes.byref(rope._c), _at("positions", positions, (rope.num_axes, n), torch.int32, device)
+
+
+def kda_qk_norm_rope(cfg: Config, rope: Optional[Rope], q, k, q_weight=None, k_weight=None, positions=None,
+                     eps: float = 1e-6, *, q_out=None, k_out=None, stream=None):
+    """y = rotate(x / sqrt(mean(x^2) + eps) * weight) per head: q [n, num_heads,
+    d], k [n, kv heads, d] or None, io dtype (their tokens may be strided:
+    views into a wider projection); weights [d] fp32 or None (no norm); rope
+    None rotates nothing; positions int32 [num_axes, n] (or [n]).  Returns
+    (q_out, k_out), out dtype.  q_out=q and k_out=k work in place for
+    contiguous tensors of one type."""
+    dev, d, H = q.device, cfg.head_k_dim, cfg.num_heads
+    n = q.shape[0]
+    heads = 0 if k is None else k.shape[1]
+    qp, qs = _rows_at("q", q, (n, H, d), cfg.io_dtype, dev)
+    kp, ks = (None, 0) if k is None else _rows_at("k", k, (n, heads, d), cfg.io_dtype, dev)
+    f32, out = torch.float32, cfg.out_dtype
+    wp, vp = _at("q_weight", q_weight, (d,), f32, dev), _at("k_weight", k_weight, (d,), f32, dev)
+    rp, pp = _rope_at(rope, positions, n, dev)
+    qo, ko = _at("q_out", q_out, (n, H, d), out, dev), _at("k_out", k_out, (n, heads, d), out, dev)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_qk_norm_rope(cfg, rope, q, k, q_weight, k_weight, positions, eps,
+                                                                 q_out=q_out, k_out=k_out))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    y = torch.empty((n, H, d), dtype=out, device=dev) if q_out is None else q_out
+    z = torch.empty((n, heads, d), dtype=out, device=dev) if k_out is None and k is not None else k_out
+    _check(_lib.kda_qk_norm_rope(_attention_struct(cfg), rp, n, heads, qp, qs, kp, ks, wp, vp, eps, pp,
+                                 qo or y.data_ptr(), ko or (z.data_ptr() if z is not None else None), st),
+           "kda_qk_norm_rope")
+    return y, z
+
+
+def kda_qk_norm_rope_backward_workspace_bytes(cfg: Config, n_tokens: int, num_kv_heads: int) -> int:
+    """Bytes of workspace; 0 for sizes that the library refuses."""
+    return int(_lib.kda_qk_norm_rope_backward_workspace_bytes(_attention_struct(cfg), _int64(n_tokens), _int32(num_kv_heads)))
+
+
+def kda_qk_norm_rope_backward(cfg: Config, rope: Optional[Rope], q, k, q_weight, k_weight, positions, dq_out, dk_out,
+                              eps: float = 1e-6, *, workspace=None, stream=None):
+    """Gradients of kda_qk_norm_rope: its inputs, dq_out [n, num_heads, d] and
+    dk_out (None with k) in the out dtype.  Returns (dq, dk, dq_weight,
+    dk_weight), fp32; a weight that is None has a gradient of zeros, k None a
+    dk of None."""
+    dev, d, H = q.device, cfg.head_k_dim, cfg.num_heads
+    n = q.shape[0]
+    heads = 0 if k is None else k.shape[1]
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out come together")
+    qp, qs = _rows_at("q", q, (n, H, d), cfg.io_dtype, dev)
+    kp, ks = (None, 0) if k is None else _rows_at("k", k, (n, heads, d), cfg.io_dtype, dev)
+    f32, out = torch.float32, cfg.out_dtype
+    wp, vp = _at("q_weight", q_weight, (d,), f32, dev), _at("k_weight", k_weight, (d,), f32, dev)
+    rp, pp = _rope_at(rope, positions, n, dev)
+    gp, hp = _at("dq_out", dq_out, (n, H, d), out, dev), _at("dk_out", dk_out, (n, heads, d), out, dev)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_qk_norm_rope_backward(
+            cfg, rope, q, k, q_weight, k_weight, positions, dq_out, dk_out, eps, workspace=workspace))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    dq = torch.empty((n, H, d), dtype=f32, device=dev)
+    dk = None if k is None else torch.empty((n, heads, d), dtype=f32, device=dev)
+    dw = torch.empty((2, d), dtype=f32, device=dev)
+    c = _attention_struct(cfg)
+    ws, wsp, size = _workspace_at(_lib.kda_qk_norm_rope_backward_workspace_bytes(c, n, heads), dev, workspace)
+    _check(_lib.kda_qk_norm_rope_backward(c, rp, n, heads, qp, qs, kp, ks, wp, vp, eps, pp, gp, hp, dq.data_ptr(),
+                                          None if dk is None else dk.data_ptr(), dw.data_ptr(), wsp, size, st),
+           "kda_qk_norm_rope_backward")
+    return dq, dk, dw[0], dw[1]
+
+
+def _cache_at(cfg, cache, cu_seqlens, page_table, lengths):
+    """(struct of the cache and the call's sequences in it, N, device)."""
+    dev = cache.k.device
+    if 2 * cache.k.shape[3] != cfg.head_k_dim:
+        raise ValueError("the cache's heads are not head_k_dim wide")
+    N = lengths.numel()
+    i32 = torch.int32
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [N, max_pages]")
+    c = KdaKvCacheC.from_buffer_copy(cache._c)
+    c.max_pages = _int32(page_table.shape[1])
+    c.page_table = _at("page_table", page_table, (N, page_table.shape[1]), i32, dev)
+    c.lengths = _at("lengths", lengths, (N,), i32, dev)
+    c.cu_seqlens = _at("cu_seqlens", cu_seqlens, (N + 1,), i32, dev)
+    return c, N, dev
+
+
+def kda_append_kv(cfg: Config, cache: KvCache, cu_seqlens, page_table, lengths, k, v, k_weight=None,
+                  eps: float = 1e-6, *, rope: Optional[Rope] = None, positions=None, stream=None):
+    """Appends keys and values [n_tokens, kv heads, d] (io dtype; their tokens
+    may be strided): token j of the q_n tokens of sequence n goes to position
+    lengths[n] - q_n + j of page_table's pages.  cu_seqlens [N + 1], page_table
+    [N, max_pages], lengths [N], int32; cu_seqlens None: one token each.  Keys
+    are normed and rotated on the way as in kda_qk_norm_rope; positions None:
+    the cache positions."""
+    c, N, dev = _cache_at(cfg, cache, cu_seqlens, page_table, lengths)
+    n, shape = k.shape[0], (k.shape[0], cache.k.shape[1], cfg.head_k_dim)
+    kp, ks = _rows_at("k", k, shape, cfg.io_dtype, dev)
+    vp, vs = _rows_at("v", v, shape, cfg.io_dtype, dev)
+    wp = _at("k_weight", k_weight, (cfg.head_k_dim,), torch.float32, dev)
+    rp, pp = _rope_at(rope, positions, n, dev)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_append_kv(cfg, cache, cu_seqlens, page_table, lengths, k, v, k_weight,
+                                                              eps, rope=rope, positions=positions))
+    _check(_lib.kda_append_kv(_attention_struct(cfg), rp, ctypes.byref(c), N, n, kp, ks, vp, vs, wp, eps, pp,
+                              torch._C._cuda_getCurrentRawStream(dev.index)), "kda_append_kv")
+
+
+def kda_read_kv(cfg: Config, cache: KvCache, cu_seqlens, page_table, lengths, n_tokens: int, *, k=None, v=None,
+                stream=None):
+    """The last cu_seqlens[n + 1] - cu_seqlens[n] rows of each sequence, as
+    kda_append_kv left them.  Returns (k, v) [n_tokens, kv heads, d], out dtype;
+    rows that are not held are 0, rows behind cu_seqlens[N] are not written."""
+    c, N, dev = _cache_at(cfg, cache, cu_seqlens, page_table, lengths)
+    shape, out = (n_tokens, cache.k.shape[1], cfg.head_k_dim), cfg.out_dtype
+    kp, vp = _at("k", k, shape, out, dev), _at("v", v, shape, out, dev)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_read_kv(cfg, cache, cu_seqlens, page_table, lengths, n_tokens, k=k, v=v))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    k_ = torch.empty(shape, dtype=out, device=dev) if k is None else k
+    v_ = torch.empty(shape, dtype=out, device=dev) if v is None else v
+    _check(_lib.kda_read_kv(_attention_struct(cfg), ctypes.byref(c), N, n_tokens, kp or k_.data_ptr(),
+                            vp or v_.data_ptr(), st), "kda_read_kv")
+    return k_, v_
+
+
+def kda_paged_attention_workspace_bytes(cfg: Config, num_kv_heads: int, N: int, n_tokens: int, max_q: int = 0) -> int:
+    """Bytes of workspace; 0 for sizes that the library refuses."""
+    return int(_lib.kda_paged_attention_workspace_bytes(_attention_struct(cfg), _int32(num_kv_heads), _int32(N),
+                                                        _int64(n_tokens), _int32(max_q)))
+
+
+def kda_paged_attention(cfg: Config, cache: KvCache, q, cu_seqlens, page_table, lengths, scale: Optional[float] = None,
+                        *, max_q: int = 0, o=None, lse=None, workspace=None, stream=None):
+    """Attention of each sequence's newest tokens, q [n_tokens, num_heads, d]
+    (io dtype), over its cache (their own keys and values among it), causal:
+    token j of q_n sees positions up to lengths[n] - q_n + j.  scale: 1 /
+    sqrt(d) by default; max_q: at least the most tokens of one sequence (0: not
+    known; cu_seqlens None: one each).  lse: fp32 [n_tokens, num_heads], filled
+    with the log of the sum of exponentials.  Returns o, out dtype; rows behind
+    cu_seqlens[N] are not written."""
+    c, N, dev = _cache_at(cfg, cache, cu_seqlens, page_table, lengths)
+    d, H, heads = cfg.head_k_dim, cfg.num_heads, cache.k.shape[1]
+    n = q.shape[0]
+    qp, op = _at("q", q, (n, H, d), cfg.io_dtype, dev), _at("o", o, (n, H, d), cfg.out_dtype, dev)
+    lp = _at("lse", lse, (n, H), torch.float32, dev)
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, lambda: kda_paged_attention(cfg, cache, q, cu_seqlens, page_table, lengths, scale,
+                                                                    max_q=max_q, o=o, lse=lse, workspace=workspace))
+    st = torch._C._cuda_getCurrentRawStream(dev.index)
+    o_ = torch.empty((n, H, d), dtype=cfg.out_dtype, device=dev) if o is None else o
+    cs = _attention_struct(cfg)
+    max_q = 1 if cu_seqlens is None else _int32(max_q)
+    ws, wsp, size = _workspace_at(_lib.kda_paged_attention_workspace_bytes(cs, heads, N, n, max_q), dev, workspace)
+    _check(_lib.kda_paged_attention(cs, ctypes.byref(c), N, n, max_q, qp, d ** -0.5 if scale is None else scale,
+                                    op or o_.data_ptr(), lp, wsp, size, st), "kda_paged_attention")
+    return o_

@@ -1,0 +1,564 @@
+// Attention of each sequence's newest tokens over its paged 4-bit cache.
+//
+// With G query heads to a key head, the q_n tokens of a sequence give q_n * G
+// rows that share one head's keys and values.  Transposed products keep a row
+// in one column of lanes all the way:
+//   S^T = K Q^T   (32 positions x 16 rows: two 16x16x32 steps per 32 channels)
+//   O^T += V^T P^T
+// The result layout of S^T (lane l: positions 8 (l / 16) .. + 7, row l % 16) is
+// the operand layout of P^T when the 32 positions are taken in the order
+// 2 j + t (row j of step t), so the softmax and its weights never leave their
+// lane.  Keys and values go from memory to registers and are widened to bf16
+// there (exact; half an instruction a value with the scale applied), each lane
+// reading whole bytes: of keys d / 4 channels of two neighbouring positions, of
+// values d / 16 channels of eight.
+//
+// The running maximum of a row is raised only when a score passes it by 2^8:
+// weights then reach 256, which neither fp32 sums nor bf16 operands mind, and
+// the accumulators are rescaled a few times a row instead of at every step.
+// Weights enter the matrix cores as the sum of PP bf16 values (2 for bf16
+// outputs: their rounding alone costs as much as the output's own; 3 for fp32),
+// queries as QP (1 or 3); keys and values are exact in bf16.
+//
+// Work: all (sequence, key head, row tile) units are laid end to end in blocks
+// of 128 positions, and every workgroup takes an equal share of that line, so
+// ragged batches balance without the host knowing a length.  A unit that one
+// workgroup finishes is written at once; the pieces of the others (at most two
+// a workgroup) go to the workspace and a second kernel joins them in their
+// order.
+#include <algorithm>
+
+#include "kda_device.h"
+#include "kda_internal.h"
+#include "kv_cache.h"
+#include "mfma.h"
+#include "vec_io.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kStep = 32;                   // positions of a wave's step
+constexpr int kBlockPos = kWaves * kStep;   // positions of a block
+constexpr float kRaise = 8.0f;              // log2 by which a score may pass the running maximum
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
+
+// A piece's place in the workspace: its rows' sums, then maxima and weights' sums.
+template <int D, int ROWS>
+__device__ __forceinline__ float* piece_at(float* pieces, int64_t slot) {
+  return pieces + slot * (static_cast<int64_t>(ROWS) * (D + 2));
+}
+
+// What the joining kernel has to know of a workgroup's last unit, if it began
+// there and goes on in the next workgroups.
+struct Split {
+  int seq, head, tile;
+  int pieces;   // 0: nothing to join
+};
+
+struct Sequence {
+  int first;          // its first row of q
+  int tokens;         // new tokens
+  int64_t length;     // positions held
+};
+
+__device__ __forceinline__ Sequence sequence(const CacheArgs& c, int n) {
+  Sequence s;
+  s.first = c.cu ? c.cu[n] : n;
+  const int64_t end = c.cu ? c.cu[n + 1] : n + 1;
+  const int64_t last = end < c.n_tokens ? end : c.n_tokens;
+  s.tokens = s.first < 0 || last <= s.first ? 0 : static_cast<int>(last - s.first);
+  const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
+  const int64_t len = c.lengths[n];
+  s.length = len < 0 ? 0 : len < most ? len : most;
+  return s;
+}
+
+// The line of all units' blocks: before[n] blocks in front of sequence n's.
+__device__ __forceinline__ void lay_out(const CacheArgs& c, int group, int rows, int64_t* before, int64_t* sums) {
+  // each thread a run of neighbouring sequences, then the threads' sums
+  const int per = (c.N + blockDim.x - 1) / blockDim.x;
+  const int n0 = threadIdx.x * per, n1 = n0 + per < c.N ? n0 + per : c.N;
+  int64_t mine = 0;
+  for (int n = n0; n < n1; ++n) {
+    const Sequence s = sequence(c, n);
+    const int64_t tiles = (static_cast<int64_t>(s.tokens) * group + rows - 1) / rows;
+    before[n + 1] = mine += tiles * c.heads * ((s.length + kBlockPos - 1) / kBlockPos);
+  }
+  sums[threadIdx.x] = mine;
+  __syncthreads();
+  if (threadIdx.x < 64) {   // four threads' sums a lane
+    int64_t four[4], t = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      four[i] = t;
+      t += sums[threadIdx.x * 4 + i];
+    }
+    int64_t run = t;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int64_t up = __shfl_up(run, m);
+      if (threadIdx.x >= m) run += up;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[threadIdx.x * 4 + i] = run - t + four[i];
+  }
+  __syncthreads();
+  const int64_t front = sums[threadIdx.x];
+  for (int n = n0; n < n1; ++n) before[n + 1] += front;
+  if (threadIdx.x == 0) before[0] = 0;
+  __syncthreads();
+}
+
+// A wave's step of 32 positions as it lies in memory.
+template <int D>
+struct RawStep {
+  uint32_t k[2][D / 32];                  // positions 2 (l % 16) and the next
+  uint32_t ks[D > 128 ? 2 : 1];           // their scale bytes, for each 32 channels of the lane
+  uint32_t v[8][D > 128 ? 2 : 1];         // positions 8 (l / 16) ..
+  uint2 vs;                               // their scale bytes
+};
+
+template <int D>
+__device__ __forceinline__ void load_step(const CacheArgs& c, int page, int head, int off, RawStep<D>& r) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const size_t values = values_at<D>(c, page, head), scales = scales_at<D>(c, page, head);
+  const int pos = off + 2 * j;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const uint8_t* from = c.k + values + static_cast<size_t>(pos + t) * (D / 2) + g * (D / 8);
+    if constexpr (D == 64) {
+      const uint2 w = *reinterpret_cast<const uint2*>(from);
+      r.k[t][0] = w.x;
+      r.k[t][1] = w.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        const uint4 w = reinterpret_cast<const uint4*>(from)[i];
+        r.k[t][4 * i] = w.x;
+        r.k[t][4 * i + 1] = w.y;
+        r.k[t][4 * i + 2] = w.z;
+        r.k[t][4 * i + 3] = w.w;
+      }
+    }
+  }
+  const int block = g * D / 128;   // of the lane's first channel
+#pragma unroll
+  for (int i = 0; i < (D > 128 ? 2 : 1); ++i)
+    r.ks[i] = *reinterpret_cast<const uint16_t*>(c.k_scale + scales + (static_cast<size_t>(block + i) << c.page_shift) + pos);
+  const uint8_t* from = c.v + values + static_cast<size_t>(off + 8 * g) * (D / 2) + j * (D / 32);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (D == 64) {
+      r.v[e][0] = *reinterpret_cast<const uint16_t*>(from + e * (D / 2));
+    } else if constexpr (D == 128) {
+      r.v[e][0] = *reinterpret_cast<const uint32_t*>(from + e * (D / 2));
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(from + e * (D / 2));
+      r.v[e][0] = w.x;
+      r.v[e][1] = w.y;
+    }
+  }
+  r.vs = *reinterpret_cast<const uint2*>(c.v_scale + scales + (static_cast<size_t>(j * D / 512) << c.page_shift) + off + 8 * g);
+}
+
+__device__ __forceinline__ float scale_of(uint32_t bytes, int i) {
+  return __uint_as_float(((bytes >> (8 * i)) & 0xffu) << 23);
+}
+
+template <int B>
+__device__ __forceinline__ uint32_t widen(uint32_t w, float s) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
+}
+
+// 8 codes as the bf16 values they stand for, in their order.
+__device__ __forceinline__ bf16x8 widen8(uint32_t w, float s) {
+  return __builtin_bit_cast(bf16x8, make_uint4(widen<0>(w, s), widen<1>(w, s), widen<2>(w, s), widen<3>(w, s)));
+}
+
+// Rows' accumulators of one wave: MT tiles of 16 rows, this lane's row l % 16 of each.
+template <int D, int MT>
+struct Rows {
+  f32x4 o[MT][D / 16];   // channel (4 (l / 16) + i) * D / 16 + c of o[.][c][i]
+  float m[MT], l[MT];    // running maximum (of the row), sum of this lane's weights
+};
+
+template <int D, int MT, int QP, int PP, bool MASKED>
+__device__ __forceinline__ void attend_step(const RawStep<D>& r, const SplitN<QP> (&q)[MT][D / 32], float scale,
+                                            int64_t at, const int64_t (&sees)[MT], const CacheArgs& c, int page,
+                                            int head, int off, Rows<D, MT>& acc) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  f32x4 s[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) s[m][0] = s[m][1] = zero4();
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const bf16x8 k = widen8(r.k[t][i], scale_of(D > 128 && i >= 4 ? r.ks[D > 128 ? 1 : 0] : r.ks[0], t));
+#pragma unroll
+      for (int p = QP - 1; p >= 0; --p)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s[m][t] = mfma(k, q[m][i].v[p], s[m][t]);
+    }
+  uint32_t w[MT][4][PP];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    float x[8];   // position 8 g + e
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = s[m][e & 1][e >> 1] * scale;
+      if constexpr (MASKED) x[e] = at + 8 * g + e < sees[m] ? x[e] : neg_inf();
+    }
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+    if (__any(top > acc.m[m] + kRaise)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float up = fmaxf(acc.m[m], top);
+      const float down = up == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(acc.m[m] - up);
+      acc.m[m] = up;
+      acc.l[m] *= down;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) acc.o[m][i] *= down;
+    }
+    const float base = acc.m[m] == neg_inf() ? 0.0f : acc.m[m];
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = __builtin_amdgcn_exp2f(x[e] - base);
+      sum += x[e];
+    }
+    acc.l[m] += sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_pair<PP>(x[2 * e], x[2 * e + 1], w[m][e]);
+  }
+  float vs[8];
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t byte = ((e < 4 ? r.vs.x : r.vs.y) >> (8 * (e & 3))) & 0xffu;
+    // what not every row sees must not meet a weight of 0 as a NaN or an infinity
+    const bool out = MASKED && byte >= 253;
+    bad |= out;
+    vs[e] = __uint_as_float(out ? 0u : byte << 23);
+  }
+#pragma unroll
+  for (int b = 0; b < D / 32; ++b) {   // a byte: two channels
+    uint32_t x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t word = r.v[e][b >> 2];
+      x[e] = (b & 3) == 0 ? widen<0>(word, vs[e]) : (b & 3) == 1 ? widen<1>(word, vs[e])
+             : (b & 3) == 2 ? widen<2>(word, vs[e]) : widen<3>(word, vs[e]);
+    }
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[e] = __builtin_amdgcn_perm(x[2 * e + 1], x[2 * e], 0x05040100u);
+      hi[e] = __builtin_amdgcn_perm(x[2 * e + 1], x[2 * e], 0x07060302u);
+    }
+    const bf16x8 v0 = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    const bf16x8 v1 = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+#pragma unroll
+    for (int p = PP - 1; p >= 0; --p)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const bf16x8 pw = __builtin_bit_cast(bf16x8, make_uint4(w[m][0][p], w[m][1][p], w[m][2][p], w[m][3][p]));
+        acc.o[m][2 * b] = mfma(v0, pw, acc.o[m][2 * b]);
+        acc.o[m][2 * b + 1] = mfma(v1, pw, acc.o[m][2 * b + 1]);
+      }
+  }
+  if constexpr (MASKED) {
+    if (__any(bad)) {   // a row that sees such a value has NaN in its 32 channels
+      const uint8_t* scales = c.v_scale + scales_at<D>(c, page, head) + off;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* of = scales + (static_cast<size_t>((4 * g + i) * D / 512) << c.page_shift);
+        for (int e = 0; e < kStep; ++e) {
+          if (of[e] < 253) continue;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            if (at + e < sees[m])
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) acc.o[m][x][i] = __uint_as_float(0x7fc00000u);
+        }
+      }
+    }
+  }
+}
+
+// A row's sums to its place: the output, or a piece of the workspace.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+}  // namespace
+
+template <int D, int MT, int QP, int PP>
+__global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged_attention_kernel(
+    CacheArgs c, const void* __restrict__ q, int group, float scale, void* __restrict__ o, float* __restrict__ lse,
+    Split* __restrict__ splits, float* __restrict__ pieces) {
+  constexpr int kRows = 16 * MT;
+  constexpr int kPitch = D + 4;
+  __shared__ float meet[kWaves][16][kPitch];
+  __shared__ float tops[kWaves][kRows][2];
+  extern __shared__ int64_t before[];   // [N + 1]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
+  const int Hq = c.heads * group;
+  lay_out(c, group, kRows, before, reinterpret_cast<int64_t*>(meet));
+  const int64_t total = before[c.N];
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t start = share * blockIdx.x;
+  const int64_t end = start + share < total ? start + share : total;
+  Split split = {0, 0, 0, 0};
+
+  // sequences that hold nothing: their rows see nothing
+  for (int n = blockIdx.x; n < c.N; n += gridDim.x) {
+    const Sequence s = sequence(c, n);
+    if (s.length > 0) continue;
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq * (D / 8); i += blockDim.x) {
+      const float zero[8] = {};
+      store_n<PP == 2, 8>(o, static_cast<size_t>(s.first) * Hq * D + i * 8, zero);
+    }
+    if (lse)
+      for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq; i += blockDim.x)
+        lse[static_cast<size_t>(s.first) * Hq + i] = neg_inf();
+  }
+
+  for (int64_t cur = start; cur < end;) {
+    int n = 0;
+    for (int hi = c.N; hi - n > 1;) {   // the last with before[n] <= cur
+      const int mid = (n + hi) >> 1;
+      if (before[mid] <= cur) n = mid;
+      else hi = mid;
+    }
+    const Sequence s = sequence(c, n);
+    const int64_t blocks = (s.length + kBlockPos - 1) / kBlockPos;
+    const int rows = s.tokens * group;
+    const int tiles = (rows + kRows - 1) / kRows;
+    const int64_t local = cur - before[n];
+    const int64_t unit = local / blocks;
+    const int64_t b0 = local - unit * blocks;
+    const int64_t b1 = b0 + (end - cur) < blocks ? b0 + (end - cur) : blocks;
+    const int head = static_cast<int>(unit / tiles), tile = static_cast<int>(unit - static_cast<int64_t>(head) * tiles);
+    // this lane's rows
+    SplitN<QP> qf[MT][D / 32];
+    int64_t sees[MT];
+    int64_t least = INT64_MAX, most = 0;   // positions that every row sees, and that any does
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = tile * kRows + m * 16 + j;
+      const int r = row < rows ? row : rows - 1;
+      const int t = r / group;
+      const size_t from = (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D + g * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        if constexpr (QP == 1) {
+          qf[m][i].v[0] = load_bf16x8(static_cast<const uint16_t*>(q) + from + 8 * i);
+        } else {
+          qf[m][i] = load_split<QP>(static_cast<const float*>(q) + from + 8 * i);
+        }
+      }
+      sees[m] = s.length - s.tokens + t + 1;
+    }
+    {
+      const int last = (tile + 1) * kRows < rows ? (tile + 1) * kRows : rows;
+      least = s.length - s.tokens + tile * kRows / group + 1;
+      most = s.length - s.tokens + (last - 1) / group + 1;
+    }
+    Rows<D, MT> acc;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      acc.m[m] = neg_inf();
+      acc.l[m] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) acc.o[m][i] = zero4();
+    }
+    for (int64_t b = b0; b < b1; ++b) {
+      const int64_t at = b * kBlockPos + wave * kStep;
+      if (at >= most) break;
+      const int page = __builtin_amdgcn_readfirstlane(page_of(c, n, at));
+      if (page < 0) continue;
+      const int off = static_cast<int>(at & ((1 << c.page_shift) - 1));
+      RawStep<D> raw;
+      load_step<D>(c, page, head, off, raw);
+      if (at + kStep <= least)
+        attend_step<D, MT, QP, PP, false>(raw, qf, scale, at, sees, c, page, head, off, acc);
+      else
+        attend_step<D, MT, QP, PP, true>(raw, qf, scale, at, sees, c, page, head, off, acc);
+    }
+    // the waves' sums joined, 16 rows at a time
+    const bool whole = b0 == 0 && b1 == blocks;
+    float* piece = piece_at<D, kRows>(pieces, 2 * static_cast<int64_t>(blockIdx.x) + (b0 == 0));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      acc.l[m] += __shfl_xor(acc.l[m], 16);
+      acc.l[m] += __shfl_xor(acc.l[m], 32);
+      if (g == 0) {
+        tops[wave][m * 16 + j][0] = acc.m[m];
+        tops[wave][m * 16 + j][1] = acc.l[m];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float up = tops[0][m * 16 + j][0];
+#pragma unroll
+      for (int x = 1; x < kWaves; ++x) up = fmaxf(up, tops[x][m * 16 + j][0]);
+      const float f = acc.m[m] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(acc.m[m] - up);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < D / 16; x += 4)
+          *reinterpret_cast<float4*>(&meet[wave][j][(4 * g + i) * (D / 16) + x]) =
+              make_float4(acc.o[m][x][i] * f, acc.o[m][x + 1][i] * f, acc.o[m][x + 2][i] * f, acc.o[m][x + 3][i] * f);
+      __syncthreads();
+      for (int i = threadIdx.x; i < 16 * (D / 8); i += kWaves * 64) {
+        const int rr = i / (D / 8), ch = (i - rr * (D / 8)) * 8;
+        const int row = tile * kRows + m * 16 + rr;
+        if (row >= rows) continue;
+        float up2 = tops[0][m * 16 + rr][0], l = 0.f, x[8] = {};
+#pragma unroll
+        for (int y = 1; y < kWaves; ++y) up2 = fmaxf(up2, tops[y][m * 16 + rr][0]);
+#pragma unroll
+        for (int y = 0; y < kWaves; ++y) {
+          const float my = tops[y][m * 16 + rr][0];
+          l += my == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(my - up2) * tops[y][m * 16 + rr][1];
+          float part[8];
+          load_n<false, 8>(&meet[y][rr][0], ch, part);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += part[e];
+        }
+        if (whole) {
+          const int t = row / group;
+          const size_t to = static_cast<size_t>(s.first + t) * Hq + head * group + (row - t * group);
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = l == 0.0f ? 0.0f : x[e] * inv;
+          store_n<PP == 2, 8>(o, to * D + ch, x);
+          if (lse && ch == 0) lse[to] = row_lse(up2, l);
+        } else {
+          store_n<false, 8>(piece, static_cast<size_t>(m * 16 + rr) * D + ch, x);
+          if (ch == 0) {
+            piece[kRows * D + 2 * (m * 16 + rr)] = up2;
+            piece[kRows * D + 2 * (m * 16 + rr) + 1] = l;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole && b0 == 0)
+      split = {n, head, tile, 1 + static_cast<int>((blocks - b1 + share - 1) / share)};
+    cur += b1 - b0;
+  }
+  if (threadIdx.x == 0) splits[blockIdx.x] = split;
+}
+
+// Joins the pieces of the unit that began in workgroup blockIdx.x of the first
+// kernel: a wave to a row.
+template <int D, int ROWS, bool OUT_BF16>
+__global__ __launch_bounds__(256) void join_pieces_kernel(CacheArgs c, int group, void* __restrict__ o,
+                                                          float* __restrict__ lse, const Split* __restrict__ splits,
+                                                          float* __restrict__ pieces) {
+  const Split split = splits[blockIdx.x];
+  if (split.pieces == 0) return;
+  const Sequence s = sequence(c, split.seq);
+  const int rr = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int row = split.tile * ROWS + rr;
+  if (row >= s.tokens * group) return;
+  // the first piece is its workgroup's second, the others their workgroups' first
+  auto at = [&](int i) { return piece_at<D, ROWS>(pieces, 2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0)); };
+  float up = neg_inf();
+  for (int i = lane; i < split.pieces; i += 64) up = fmaxf(up, at(i)[ROWS * D + 2 * rr]);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) up = fmaxf(up, __shfl_xor(up, m));
+  constexpr int E = D / 64;
+  float x[E] = {}, l = 0.f;
+  for (int i = 0; i < split.pieces; ++i) {
+    const float* p = at(i);
+    const float m = p[ROWS * D + 2 * rr];
+    const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - up);
+    l = fmaf(f, p[ROWS * D + 2 * rr + 1], l);
+    float y[E];
+    load_n<false, E>(p, static_cast<size_t>(rr) * D + lane * E, y);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = fmaf(f, y[e], x[e]);
+  }
+  const int t = row / group;
+  const size_t to = static_cast<size_t>(s.first + t) * (c.heads * group) + split.head * group + (row - t * group);
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = l == 0.0f ? 0.0f : x[e] / l;
+  store_n<OUT_BF16, E>(o, to * D + lane * E, x);
+  if (lse && lane == 0) lse[to] = row_lse(up, l);
+}
+
+namespace {
+
+// Row tiles of 16 that a workgroup takes: as many as the rows of a key head
+// fill, while the accumulators fit the registers.
+int row_tiles(int D, bool exact, int64_t rows) {
+  if (exact || rows <= 16) return 1;
+  if (D == 256 || rows <= 32) return 2;
+  return 4;
+}
+
+int workgroups(int D, int mt) { return D / 16 * mt > 16 ? 256 : 512; }
+
+int64_t rows_of(const CacheArgs& c, int group, int max_q) {
+  return (max_q > 0 ? std::min<int64_t>(max_q, c.n_tokens) : c.n_tokens) * group;
+}
+
+}  // namespace
+
+size_t paged_attention_ws(int D, int heads, int group, int64_t n_tokens, int max_q, bool exact) {
+  CacheArgs c{};
+  c.n_tokens = n_tokens;
+  const int mt = row_tiles(D, exact, rows_of(c, group, max_q));
+  const size_t wgs = workgroups(D, mt);
+  return wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4;
+}
+
+hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
+                                  float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st) {
+  const int mt = row_tiles(D, !(in_bf16 && out_bf16), rows_of(c, group, max_q));
+  const int wgs = workgroups(D, mt);
+  Split* splits = static_cast<Split*>(ws);
+  float* pieces = reinterpret_cast<float*>(splits + wgs);
+  const size_t shared = (static_cast<size_t>(c.N) + 1) * 8;
+  auto go = [&](auto d, auto t, auto qp, auto pp) {
+    constexpr int kD = decltype(d)::value, kT = decltype(t)::value, kPP = decltype(pp)::value;
+    paged_attention_kernel<kD, kT, decltype(qp)::value, kPP>
+        <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    join_pieces_kernel<kD, 16 * kT, kPP == 2><<<dim3(wgs, 4 * kT), 256, 0, st>>>(c, group, o, lse, splits, pieces);
+    return hipGetLastError();
+  };
+  using std::integral_constant;
+  auto by_type = [&](auto d) {
+    constexpr int kD = decltype(d)::value;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 3> three;
+    if (!in_bf16) return out_bf16 ? go(d, one, three, two) : go(d, one, three, three);
+    if (!out_bf16) return go(d, one, one, three);
+    if (mt == 1) return go(d, one, one, two);
+    if (mt == 2) return go(d, two, one, two);
+    if constexpr (kD < 256) return go(d, integral_constant<int, 4>{}, one, two);
+    return hipErrorInvalidValue;
+  };
+  switch (D) {
+    case 64: return by_type(integral_constant<int, 64>{});
+    case 128: return by_type(integral_constant<int, 128>{});
+    case 256: return by_type(integral_constant<int, 256>{});
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace kda

@@ -177,6 +177,56 @@ hipError_t launch_add_rmsnorm_bwd(int64_t n, int hidden, const void* h, const fl
 hipError_t launch_fp8_matmul(int64_t M, int N, int K, const uint8_t* a, const float* sa, const uint8_t* w,
                              const float* sw, void* y, bool out_bf16, hipStream_t st);
 
+// Rotation of a head's first rotary_dim channels (rope.h).
+struct RopeArgs {
+  int rotary_dim, interleaved, num_axes;
+  const float* inv_freq;     // [rotary_dim / 2]
+  const int32_t* axis;       // [rotary_dim / 2] or null
+  const int32_t* positions;  // [num_axes][n_tokens]; null in kda_append_kv: the cache position
+  int64_t n_tokens;
+};
+
+// Query heads (index 0) and key heads (1).
+struct QkArgs {
+  int heads[2];
+  const void* in[2];     // rows of [heads][D], stride elements apart
+  int64_t stride[2];
+  const float* w[2];     // [D] or null: no norm
+  const void* dy[2];     // backward: [n][heads][D]
+  void* out[2];          // [n][heads][D]: y, or fp32 gradients
+};
+
+hipError_t launch_qk_norm_rope(int D, const RopeArgs& r, const QkArgs& x, float eps, bool in_bf16, bool out_bf16,
+                               hipStream_t st);
+// part holds qk_norm_rope_bwd_parts rows of [2][D] partial sums of dw.
+int qk_norm_rope_bwd_parts(int D, int64_t n, int heads);
+hipError_t launch_qk_norm_rope_bwd(int D, const RopeArgs& r, const QkArgs& x, float eps, float* d_weight, float* part,
+                                   bool in_bf16, bool out_bf16, hipStream_t st);
+
+// A paged cache of 4-bit keys and values and a call's sequences in it (kda_kv_cache_t).
+struct CacheArgs {
+  uint8_t* k;
+  uint8_t* k_scale;
+  uint8_t* v;
+  uint8_t* v_scale;
+  int num_pages, page_shift, heads, max_pages;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* cu;
+  int N;
+  int64_t n_tokens;
+};
+
+hipError_t launch_append_kv(int D, const RopeArgs& r, const CacheArgs& cache, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const float* k_weight, float eps, bool in_bf16,
+                            hipStream_t st);
+hipError_t launch_read_kv(int D, const CacheArgs& cache, void* k_out, void* v_out, bool out_bf16, hipStream_t st);
+
+// Attention over the cache: `exact` is fp32 queries or outputs; max_q 0: not known.
+size_t paged_attention_ws(int D, int heads, int group, int64_t n_tokens, int max_q, bool exact);
+hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
+                                  float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st);
+
 struct DecodeIO {
   const void* q;
   const void* k;

@@ -1,0 +1,264 @@
+// Norm of the query and key heads and their rotation by position,
+//   y = rotate(x / sqrt(mean x^2 + eps) * w),
+// and its backward pass: with g the upstream gradient rotated back, n = x /
+// sqrt(mean x^2 + eps) and u = g * w,
+//   dx = (u - n * mean(u n)) / sqrt(mean x^2 + eps),  dw = sum g * n.
+//
+// HBM-bound: each head is read once and kept in the registers of D / 16 lanes
+// (rope.h).  Such a group of lanes takes a token and a run of its heads, whose
+// sines it forms once (in fp32 from an angle reduced in 64 bits: v_sin_f32 and
+// v_cos_f32 take turns and were at most 1.2e-7 off over one turn).
+#include <algorithm>
+
+#include "kda_device.h"
+#include "kda_internal.h"
+#include "rope.h"
+#include "vec_io.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAtOnce = 4;   // heads whose loads are in flight together
+
+template <int D, bool INTER>
+__device__ __forceinline__ void sines(const RopeArgs& r, const PairRates& p, int64_t token, float (&c)[8],
+                                      float (&s)[8]) {
+  const Places at(r, token);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = static_cast<float>(turns(p, at, e));
+    c[e] = __builtin_amdgcn_cosf(t);
+    s[e] = __builtin_amdgcn_sinf(t);
+  }
+}
+
+}  // namespace
+
+// Group g of lanes takes token g / runs and the run g % runs of its heads: the
+// runs of q's heads, then those of k's.
+template <int D, bool IN_BF16, bool OUT_BF16, bool INTER>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs r, QkArgs x, int run_len, float eps) {
+  constexpr int L = D / 16;
+  const int lane = threadIdx.x % L;
+  const HeadRuns<D, INTER> runs(lane, r.rotary_dim);
+  const PairRates rates = pair_rates<D, INTER>(r, runs);
+  const int q_runs = (x.heads[0] + run_len - 1) / run_len;
+  const int n_runs = q_runs + (x.heads[1] + run_len - 1) / run_len;
+  const int64_t groups = r.n_tokens * n_runs;
+  for (int64_t g = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L; g < groups;
+       g += static_cast<int64_t>(gridDim.x) * kThreads / L) {
+    const int64_t token = g / n_runs;
+    const int run = static_cast<int>(g - token * n_runs);
+    const int which = run >= q_runs;
+    const int h0 = (which ? run - q_runs : run) * run_len;
+    const int heads = which ? x.heads[1] : x.heads[0];
+    const int h1 = h0 + run_len < heads ? h0 + run_len : heads;
+    const void* from = which ? x.in[1] : x.in[0];
+    void* to = which ? x.out[1] : x.out[0];
+    const float* w = which ? x.w[1] : x.w[0];
+    const size_t in0 = static_cast<size_t>(token) * (which ? x.stride[1] : x.stride[0]);
+    const size_t out0 = static_cast<size_t>(token) * heads * D;
+    float c[8], s[8], wa[8], wb[8];
+    if (r.rotary_dim) sines<D, INTER>(r, rates, token, c, s);
+    if (w) {
+      load_n<false, 8>(w, runs.a, wa);
+      load_n<false, 8>(w, runs.b, wb);
+    }
+    for (int h = h0; h < h1; h += kAtOnce) {
+      float a[kAtOnce][8], b[kAtOnce][8];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const size_t at = in0 + static_cast<size_t>(h + i < h1 ? h + i : h1 - 1) * D;
+        load_n<IN_BF16, 8>(from, at + runs.a, a[i]);
+        load_n<IN_BF16, 8>(from, at + runs.b, b[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (h + i >= h1) break;
+        if (w) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(a[i][e], a[i][e], fmaf(b[i][e], b[i][e], ss));
+          const float inv = rsqrt_precise(dpp_group_sum<L>(ss) * (1.0f / D) + eps);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            a[i][e] *= inv * wa[e];
+            b[i][e] *= inv * wb[e];
+          }
+        }
+        rotate<D, INTER>(runs, a[i], b[i], c, s);
+        const size_t at = out0 + static_cast<size_t>(h + i) * D;
+        store_n<OUT_BF16, 8>(to, at + runs.a, a[i]);
+        store_n<OUT_BF16, 8>(to, at + runs.b, b[i]);
+      }
+    }
+  }
+}
+
+// Groups take tokens and runs of heads as above, first all of q's and then all
+// of k's; a lane keeps its channels, so both weights' gradients gather in its
+// registers.  A workgroup joins its lanes in LDS and leaves one row of `part`,
+// [2][D].  Groups and the order of every sum depend on the sizes alone.
+template <int D, bool IN_BF16, bool OUT_BF16, bool INTER>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, QkArgs x, int run_len, float eps,
+                                                                    float* __restrict__ part) {
+  constexpr int L = D / 16;
+  __shared__ float red[kThreads][8];
+  const int lane = threadIdx.x % L;
+  const HeadRuns<D, INTER> runs(lane, r.rotary_dim);
+  const PairRates rates = pair_rates<D, INTER>(r, runs);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float da[8] = {}, db[8] = {}, wa[8], wb[8];
+    const float* w = x.w[which];
+    if (w) {
+      load_n<false, 8>(w, runs.a, wa);
+      load_n<false, 8>(w, runs.b, wb);
+    }
+    const int heads = x.heads[which];
+    const int n_runs = (heads + run_len - 1) / run_len;
+    const int64_t groups = r.n_tokens * n_runs;
+    for (int64_t g = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L; g < groups;
+         g += static_cast<int64_t>(gridDim.x) * kThreads / L) {
+      const int64_t token = g / n_runs;
+      const int h0 = static_cast<int>(g - token * n_runs) * run_len;
+      const int h1 = h0 + run_len < heads ? h0 + run_len : heads;
+      const size_t in0 = static_cast<size_t>(token) * x.stride[which];
+      const size_t out0 = static_cast<size_t>(token) * heads * D;
+      float c[8], s[8];
+      if (r.rotary_dim) {
+        sines<D, INTER>(r, rates, token, c, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = -s[e];   // back
+      }
+      constexpr int kPair = 2;
+      for (int h = h0; h < h1; h += kPair) {
+        float a[kPair][8], b[kPair][8], ga[kPair][8], gb[kPair][8];
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          const int hi = h + i < h1 ? h + i : h1 - 1;
+          const size_t in = in0 + static_cast<size_t>(hi) * D, out = out0 + static_cast<size_t>(hi) * D;
+          load_n<IN_BF16, 8, true>(x.in[which], in + runs.a, a[i]);
+          load_n<IN_BF16, 8, true>(x.in[which], in + runs.b, b[i]);
+          load_n<OUT_BF16, 8, true>(x.dy[which], out + runs.a, ga[i]);
+          load_n<OUT_BF16, 8, true>(x.dy[which], out + runs.b, gb[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          if (h + i >= h1) break;
+          rotate<D, INTER>(runs, ga[i], gb[i], c, s);
+          if (w) {
+            float ss = 0.f, sg = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              ss = fmaf(a[i][e], a[i][e], fmaf(b[i][e], b[i][e], ss));
+              sg = fmaf(ga[i][e] * wa[e], a[i][e], fmaf(gb[i][e] * wb[e], b[i][e], sg));
+            }
+            ss = dpp_group_sum<L>(ss);
+            sg = dpp_group_sum<L>(sg);
+            const float inv = rsqrt_precise(ss * (1.0f / D) + eps);
+            // n * mean(u n) = x * k; 0 where the squares pass fp32's range, as n is
+            const float k = inv == 0.f ? 0.f : sg * (1.0f / D) * inv * inv;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              da[e] = fmaf(ga[i][e], a[i][e] * inv, da[e]);
+              db[e] = fmaf(gb[i][e], b[i][e] * inv, db[e]);
+              ga[i][e] = inv * fmaf(-a[i][e], k, ga[i][e] * wa[e]);
+              gb[i][e] = inv * fmaf(-b[i][e], k, gb[i][e] * wb[e]);
+            }
+          }
+          const size_t at = out0 + static_cast<size_t>(h + i) * D;
+          store_n<false, 8>(x.out[which], at + runs.a, ga[i]);
+          store_n<false, 8>(x.out[which], at + runs.b, gb[i]);
+        }
+      }
+    }
+    // the lanes of a channel joined: lane l of every group, a run at a time
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      __syncthreads();
+      store_n<false, 8>(&red[threadIdx.x][0], 0, half ? db : da);
+      __syncthreads();
+      if (threadIdx.x < 8 * L) {
+        const int l = threadIdx.x / 8, e = threadIdx.x % 8;
+        const HeadRuns<D, INTER> to(l, r.rotary_dim);
+        float t = 0.f;
+        for (int k = l; k < kThreads; k += L) t += red[k][e];
+        part[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + (half ? to.b : to.a) + e] = t;
+      }
+    }
+  }
+}
+
+namespace {
+
+// Heads of a group's run: one while the groups are few (latency), then as many
+// as leave 8192 waves, 8 at most (the sines are formed once a run).
+int run_length(int D, int64_t n, int heads) {
+  const int64_t waves = n * heads * (D / 16) / 64;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, waves / 8192)));
+}
+
+template <class F>
+hipError_t with_shape(int D, bool in_bf16, bool out_bf16, bool inter, F&& f) {
+  using std::false_type;
+  using std::true_type;
+  auto by_pairs = [&](auto d, auto ib, auto ob) {
+    if (inter) f(d, ib, ob, true_type{});
+    else f(d, ib, ob, false_type{});
+    return hipGetLastError();
+  };
+  auto by_type = [&](auto d) {
+    if (in_bf16 && out_bf16) return by_pairs(d, true_type{}, true_type{});
+    if (in_bf16) return by_pairs(d, true_type{}, false_type{});
+    if (out_bf16) return by_pairs(d, false_type{}, true_type{});
+    return by_pairs(d, false_type{}, false_type{});
+  };
+  switch (D) {
+    case 64: return by_type(std::integral_constant<int, 64>{});
+    case 128: return by_type(std::integral_constant<int, 128>{});
+    case 256: return by_type(std::integral_constant<int, 256>{});
+    default: return hipErrorInvalidValue;
+  }
+}
+
+int64_t groups_of(const QkArgs& x, int64_t n, int run) {
+  return n * ((x.heads[0] + run - 1) / run + (x.heads[1] + run - 1) / run);
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(int D, const RopeArgs& r, const QkArgs& x, float eps, bool in_bf16, bool out_bf16,
+                               hipStream_t st) {
+  const int run = run_length(D, r.n_tokens, x.heads[0] + x.heads[1]);
+  const int64_t blocks = (groups_of(x, r.n_tokens, run) * (D / 16) + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20)));
+  return with_shape(D, in_bf16, out_bf16, r.interleaved, [&](auto d, auto ib, auto ob, auto inter) {
+    qk_norm_rope_kernel<decltype(d)::value, decltype(ib)::value, decltype(ob)::value, decltype(inter)::value>
+        <<<grid, kThreads, 0, st>>>(r, x, run, eps);
+  });
+}
+
+// Workgroups of the backward, each with a row of partial sums: three a CU at most.
+int qk_norm_rope_bwd_parts(int D, int64_t n, int heads) {
+  const int64_t blocks = (n * heads * (D / 16) + kThreads - 1) / kThreads;
+  return static_cast<int>(std::min<int64_t>(blocks, 768));
+}
+
+hipError_t launch_qk_norm_rope_bwd(int D, const RopeArgs& r, const QkArgs& x, float eps, float* d_weight, float* part,
+                                   bool in_bf16, bool out_bf16, hipStream_t st) {
+  const int parts = qk_norm_rope_bwd_parts(D, r.n_tokens, x.heads[0] + x.heads[1]);
+  if (parts > 0) {
+    const int run = run_length(D, r.n_tokens, x.heads[0] + x.heads[1]);
+    const hipError_t e = with_shape(D, in_bf16, out_bf16, r.interleaved, [&](auto d, auto ib, auto ob, auto inter) {
+      qk_norm_rope_bwd_kernel<decltype(d)::value, decltype(ib)::value, decltype(ob)::value, decltype(inter)::value>
+          <<<dim3(parts), kThreads, 0, st>>>(r, x, run, eps, part);
+    });
+    if (e != hipSuccess) return e;
+  }
+  return launch_column_sums(parts, 2 * D, part, d_weight, st);
+}
+
+}  // namespace kda

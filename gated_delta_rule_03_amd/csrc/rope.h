@@ -1,0 +1,130 @@
+// A head's channels over lanes, and the angles of its rotated pairs.
+//
+// A head of D channels belongs to D / 16 lanes, each with two runs of 8
+// channels (16-byte loads in bf16), a and b, laid out so that both members of
+// a rotated pair are the same lane's: with pairs (i, i + R / 2) the first
+// R / 16 lanes hold 8 l .. and R / 2 + 8 l .., the others the two halves of the
+// channels behind R in the same way; with pairs (2 i, 2 i + 1) the runs are
+// 8 l .. and D / 2 + 8 l ...  So the rotation moves nothing between lanes, a lane
+// needs the sines of 8 pairs at most, and neighbouring lanes' loads join.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+constexpr int kMaxAxes = 4;
+
+template <int D, bool INTER>
+struct HeadRuns {
+  int a, b;            // first channels of the two runs
+  bool turn_a, turn_b; // whether their pairs are rotated (the same unless INTER)
+
+  __device__ __forceinline__ HeadRuns(int lane, int R) {
+    if constexpr (INTER) {
+      a = 8 * lane;
+      b = D / 2 + 8 * lane;
+      turn_a = a < R;
+      turn_b = b < R;
+    } else {
+      const int first = R >> 4;
+      turn_a = turn_b = lane < first;
+      a = turn_a ? 8 * lane : R + 8 * (lane - first);
+      b = turn_a ? (R >> 1) + 8 * lane : R + ((D - R) >> 1) + 8 * (lane - first);
+    }
+  }
+  // The pair that sine e of a lane belongs to.
+  __device__ __forceinline__ int pair(int e) const {
+    if constexpr (INTER) return e < 4 ? (a >> 1) + e : (b >> 1) + e - 4;
+    else return a + e;
+  }
+  __device__ __forceinline__ bool turned(int e) const { return INTER && e >= 4 ? turn_b : turn_a; }
+};
+
+// A lane's 8 pairs: turns per position in 64 bits, and their axes, two bits each.
+struct PairRates {
+  double rate[8];
+  uint32_t axes;
+};
+
+template <int D, bool INTER>
+__device__ __forceinline__ PairRates pair_rates(const RopeArgs& r, const HeadRuns<D, INTER>& runs) {
+  constexpr double kPerTurn = 0.15915494309189533577;   // 1 / (2 pi)
+  PairRates p;
+  p.axes = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    p.rate[e] = 0.0;
+    if (runs.turned(e)) {
+      p.rate[e] = static_cast<double>(r.inv_freq[runs.pair(e)]) * kPerTurn;
+      if (r.axis) {
+        const int ax = r.axis[runs.pair(e)];
+        p.axes |= static_cast<uint32_t>(ax < 0 ? 0 : ax >= r.num_axes ? r.num_axes - 1 : ax) << (2 * e);
+      }
+    }
+  }
+  return p;
+}
+
+// The token's positions on every axis.
+struct Places {
+  int32_t at[kMaxAxes];
+
+  __device__ __forceinline__ Places(const RopeArgs& r, int64_t token) {
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x) at[x] = x < r.num_axes ? r.positions[x * r.n_tokens + token] : 0;
+  }
+  __device__ __forceinline__ explicit Places(int32_t everywhere) {
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x) at[x] = everywhere;
+  }
+  __device__ __forceinline__ int32_t on(uint32_t axis) const {
+    return axis < 2 ? (axis == 0 ? at[0] : at[1]) : (axis == 2 ? at[2] : at[3]);
+  }
+};
+
+// Pair e's angle at the token, in turns within half a turn.  The product of a
+// 31-bit position and a 24-bit frequency is exact in 64 bits but for the one
+// rounding of the rate: 1e-10 turns at position 10^6.
+__device__ __forceinline__ double turns(const PairRates& p, const Places& at, int e) {
+  const double t = static_cast<double>(at.on((p.axes >> (2 * e)) & 3)) * p.rate[e];
+  return t - rint(t);
+}
+
+// (a, b) rotated by the pairs' sines: the runs of one lane, T float or double.
+template <int D, bool INTER, class T>
+__device__ __forceinline__ void rotate(const HeadRuns<D, INTER>& runs, T (&a)[8], T (&b)[8], const T (&c)[8],
+                                       const T (&s)[8]) {
+  if constexpr (INTER) {
+    if (runs.turn_a) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const T x = a[2 * i], y = a[2 * i + 1];
+        a[2 * i] = x * c[i] - y * s[i];
+        a[2 * i + 1] = x * s[i] + y * c[i];
+      }
+    }
+    if (runs.turn_b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const T x = b[2 * i], y = b[2 * i + 1];
+        b[2 * i] = x * c[4 + i] - y * s[4 + i];
+        b[2 * i + 1] = x * s[4 + i] + y * c[4 + i];
+      }
+    }
+  } else {
+    if (runs.turn_a) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const T x = a[i], y = b[i];
+        a[i] = x * c[i] - y * s[i];
+        b[i] = x * s[i] + y * c[i];
+      }
+    }
+  }
+}
+
+}  // namespace kda

@@ -34,8 +34,12 @@
  * core: kda_add_rmsnorm (the residual's addition and the norm in front of the
  * layer), kda_fp8_matmul (its projections, e4m3 operands with block scales),
  * kda_add_rmsnorm_fp8 and kda_output_gate_fp8 (the producers of such operands),
- * kda_add_rmsnorm_backward and kda_output_gate_backward.  Plus the workspace
- * queries, the version and status strings.
+ * kda_add_rmsnorm_backward and kda_output_gate_backward.  For the decoder's
+ * full-attention layers, which stand between the KDA layers: kda_qk_norm_rope
+ * and its backward (norm and rotation of the query and key heads),
+ * kda_append_kv and kda_read_kv (a paged cache of 4-bit keys and values) and
+ * kda_paged_attention.  Plus the workspace queries, the version and status
+ * strings.
  *
  * Conventions for every entry point:
  *  - All tensor pointers are DEVICE pointers, contiguous, row-major in the
@@ -99,7 +103,10 @@ typedef enum kda_stage {
     KDA_STAGE_BACKWARD = 6,     /* the backward pass's kernels (after its chunk table)        */
     KDA_STAGE_NORM = 7,         /* the residual's addition and the RMS norm                   */
     KDA_STAGE_MATMUL = 8,       /* the block-scaled e4m3 product                              */
-    KDA_NUM_STAGES = 9
+    KDA_STAGE_ROPE = 9,         /* norm and rotation of query and key heads                   */
+    KDA_STAGE_CACHE = 10,       /* kda_append_kv, kda_read_kv                                 */
+    KDA_STAGE_ATTENTION = 11,   /* kda_paged_attention                                        */
+    KDA_NUM_STAGES = 12
 } kda_stage_t;
 
 typedef struct kda_config {
@@ -136,7 +143,8 @@ typedef struct kda_config {
  * core (kda_add_rmsnorm and those after it) came without a new one: a caller
  * that opens the library at run time looks for their symbols.  The arrays of
  * stage_events that callers of the core made for 7 stages stay valid for its
- * calls, which record no others. */
+ * calls, which record no others; those made for 9 for the calls up to
+ * kda_fp8_matmul. */
 int32_t kda_version(void);
 
 /* Human-readable name of a status code (static storage). */
@@ -542,6 +550,171 @@ kda_status_t kda_fp8_matmul(const kda_config_t *cfg, int64_t M, int32_t N, int32
                             const void *a, const float *a_scale,
                             const void *w, const float *w_scale,
                             void *y, void *stream);
+
+/*
+ * ---- The full-attention layers -------------------------------------------
+ *
+ * In the hybrid decoders every fourth to sixth layer is full attention
+ * (AliceAI page, section 三: 16 query and 2 key / value heads, an RMS norm of q
+ * and k per head, rotary positions on a quarter of the channels, base 1e6).
+ * The entry points below are that layer's steps between its projections.  Of
+ * cfg they use num_heads (the query heads Hq), head_k_dim (the size d of every
+ * head, query, key and value: 64, 128 or 256, else KDA_ERR_UNSUPPORTED),
+ * head_v_dim (the same), io_dtype, out_dtype and stage_events.
+ */
+
+/* A rotation of the first rotary_dim channels of a head in pairs (a, b):
+ *   (a cos t - b sin t, a sin t + b cos t),
+ *   t = positions[axis[i]][token] * inv_freq[i]  for pair i < rotary_dim / 2.
+ * The product is formed in 64 bits, so far positions keep their angle. */
+typedef struct kda_rope {
+    int32_t rotary_dim;      /* a multiple of 16, 0 .. d; 0 rotates nothing            */
+    int32_t interleaved;     /* 0: pair i is channels (i, i + rotary_dim / 2);
+                                1: channels (2 i, 2 i + 1)                             */
+    int32_t num_axes;        /* position axes, 1 .. 4 (text has one; images time,
+                                height and width)                                      */
+    const float *inv_freq;   /* [rotary_dim / 2] fp32, device                          */
+    const int32_t *axis;     /* [rotary_dim / 2] int32, device: the axis of each pair
+                                (clamped to 0 .. num_axes - 1), or NULL: axis 0        */
+} kda_rope_t;
+
+/*
+ * Norm of each query and key head, and its rotation:
+ *   y = rotate(x / sqrt(mean x^2 + eps) * weight)   over the d channels of a head
+ *   q              [n_tokens] rows of [Hq][d] io_dtype, q_stride elements apart
+ *                  (a multiple of 8, >= Hq * d: a view into a wider projection)
+ *   k              [n_tokens] rows of [num_kv_heads][d], k_stride apart; unused
+ *                  with num_kv_heads == 0
+ *   q_weight, k_weight  [d] fp32, or NULL: no norm of q / of k, the rotation alone
+ *   eps            >= 0 (NaN or negative: KDA_ERR_INVALID_ARGUMENT); with 0 a row
+ *                  of zeros gives NaN.  A row whose squares sum to more than
+ *                  3.4e38 gives 0
+ *   rope           host struct; NULL rotates nothing
+ *   positions      [num_axes][n_tokens] int32 (any value); unused without rotation
+ *   q_out          [n_tokens][Hq][d] out_dtype; may alias q when q_stride ==
+ *                  Hq * d and both have the same type
+ *   k_out          [n_tokens][num_kv_heads][d], likewise
+ * num_kv_heads 0 .. 65535.  Needs no workspace.  n_tokens == 0 is a no-op.
+ */
+kda_status_t kda_qk_norm_rope(const kda_config_t *cfg, const kda_rope_t *rope, int64_t n_tokens,
+                              int32_t num_kv_heads, const void *q, int64_t q_stride,
+                              const void *k, int64_t k_stride,
+                              const float *q_weight, const float *k_weight, float eps,
+                              const int32_t *positions, void *q_out, void *k_out, void *stream);
+
+/*
+ * Gradient of kda_qk_norm_rope.  With n = x / sqrt(mean x^2 + eps), g the
+ * upstream gradient rotated back and u = g * weight, per head:
+ *   dx = (u - n * mean(u * n)) / sqrt(mean x^2 + eps)   (without a weight: dx = g)
+ *   dweight[j] = sum over tokens and heads of g * n
+ *   q, k, weights, eps, rope, positions   as given to the forward
+ *   dq_out, dk_out  [n_tokens][heads][d] out_dtype: dLoss/dq_out, dLoss/dk_out
+ *   dq, dk          [n_tokens][heads][d] fp32; alias nothing.  0 on a row whose
+ *                   squares sum to more than 3.4e38 (its y is 0)
+ *   d_weight        [2][d] fp32, of q_weight then of k_weight; zeros where the
+ *                   weight is NULL or there is no head or token
+ *   workspace       kda_qk_norm_rope_backward_workspace_bytes(); calls that
+ *                   overlap in time need one each
+ * The same inputs give the same bits on every run.
+ */
+size_t kda_qk_norm_rope_backward_workspace_bytes(const kda_config_t *cfg, int64_t n_tokens, int32_t num_kv_heads);
+
+kda_status_t kda_qk_norm_rope_backward(const kda_config_t *cfg, const kda_rope_t *rope, int64_t n_tokens,
+                                       int32_t num_kv_heads, const void *q, int64_t q_stride,
+                                       const void *k, int64_t k_stride,
+                                       const float *q_weight, const float *k_weight, float eps,
+                                       const int32_t *positions, const void *dq_out, const void *dk_out,
+                                       float *dq, float *dk, float *d_weight,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A paged cache of keys and values in 4 bits (OCP microscaling fp4): e2m1
+ * values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign; code 0 .. 7, bit 3 the sign)
+ * and one e8m0 scale 2^(byte - 127) for each 32 channels of a head,
+ *   E = the least with max|x| <= 6 * 2^(E - 127), at least 1;
+ *   value = x / 2^(E - 127) rounded to nearest even.
+ * A NaN or a magnitude of 2^127 or more in a block makes its byte 255, and the
+ * block reads as NaN (253 and 254 are not written; their values may overflow).
+ * A page holds page_size positions of one sequence, for all heads:
+ *   k, v           [num_pages][num_kv_heads][page_size][d / 2]   two values a
+ *                  byte, the even channel in the low half
+ *   k_scale, v_scale  [num_pages][num_kv_heads][d / 32][page_size]
+ * (16-byte aligned, e8m0 bytes 8-byte).  Position p of sequence n is position
+ * p % page_size of page page_table[n * max_pages + p / page_size].  Table
+ * entries outside 0 .. num_pages - 1 hold nothing: nothing is written there,
+ * and attention leaves their positions out.
+ */
+typedef struct kda_kv_cache {
+    void *k;
+    void *k_scale;
+    void *v;
+    void *v_scale;
+    int32_t num_pages;       /* any pages of one call's sequences; 0 .. 2^31 - 1       */
+    int32_t page_size;       /* 32, 64, 128 or 256                                     */
+    int32_t num_kv_heads;    /* 1 .. 65535; for attention a divisor of num_heads       */
+    int32_t max_pages;       /* entries of a row of page_table, >= 0                   */
+    const int32_t *page_table;   /* [N][max_pages], device                             */
+    const int32_t *lengths;      /* [N], device: positions held of each sequence, the
+                                    call's own tokens among them (what lies behind
+                                    max_pages * page_size is not held)                 */
+    const int32_t *cu_seqlens;   /* [N + 1], device, 0 first, nondecreasing: sequence
+                                    n's tokens are rows cu[n] .. cu[n + 1] - 1 of the
+                                    call's tensors; NULL: row n alone.  Rows from
+                                    cu[N] on belong to no sequence and stay as they
+                                    were                                               */
+} kda_kv_cache_t;
+
+/*
+ * Appends keys and values: token j of the q_n tokens of sequence n goes to
+ * position lengths[n] - q_n + j (a negative one is left out).
+ *   k, v           [n_tokens] rows of [num_kv_heads][d] io_dtype, k_stride and
+ *                  v_stride elements apart (multiples of 8, >= num_kv_heads * d)
+ *   k_weight, eps, rope, positions  norm and rotation of the keys, as in
+ *                  kda_qk_norm_rope; positions NULL: the cache position, on every
+ *                  axis.  Keys are computed in 64 bits, so each is held as the
+ *                  nearest value of its block's scale
+ * Two tokens of one call must not go to one position of one page (a page that
+ * two sequences share is appended to by one of them).  N == 0 or n_tokens == 0
+ * is a no-op.  N up to 2^24.  Needs no workspace.
+ */
+kda_status_t kda_append_kv(const kda_config_t *cfg, const kda_rope_t *rope, const kda_kv_cache_t *cache, int32_t N,
+                           int64_t n_tokens, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           const float *k_weight, float eps, const int32_t *positions, void *stream);
+
+/*
+ * Reads rows back: k_out, v_out [n_tokens][num_kv_heads][d] out_dtype (either
+ * may be NULL), token j of sequence n from position lengths[n] - q_n + j.  Rows
+ * of positions that are not held are 0.
+ */
+kda_status_t kda_read_kv(const kda_config_t *cfg, const kda_kv_cache_t *cache, int32_t N, int64_t n_tokens,
+                         void *k_out, void *v_out, void *stream);
+
+/*
+ * Attention of each sequence's newest tokens over its cache, causal among them:
+ *   token j of the q_n tokens of sequence n sees positions 0 .. lengths[n] - q_n + j
+ *   o = sum_p w_p v_p,  w = softmax over those positions of scale * q . k_p
+ * where query head h reads key / value head h * num_kv_heads / num_heads.
+ *   q              [n_tokens][Hq][d] io_dtype (16-byte aligned)
+ *   scale          finite, e.g. 1 / sqrt(d)
+ *   max_q          at least the largest q_n, or 0 if not known: only the choice
+ *                  of the kernel and of the workspace goes by it
+ *   o              [n_tokens][Hq][d] out_dtype; 0 for a token that sees nothing
+ *   lse            [n_tokens][Hq] fp32: log(sum exp(scale * q . k_p)), -infinity
+ *                  for a token that sees nothing; or NULL
+ *   workspace      kda_paged_attention_workspace_bytes(); calls that overlap in
+ *                  time need one each.  Nothing in it is kept between calls
+ * Positions that a token does not see, whatever their bytes, have no effect on
+ * it.  Sums and the softmax are fp32; q and the weights enter the matrix cores
+ * as bf16 (as sums of bf16 values where io_dtype or out_dtype is fp32).  N up to
+ * 4096 (else KDA_ERR_UNSUPPORTED).  Nothing aliases.  The same inputs give the
+ * same bits on every run.
+ */
+size_t kda_paged_attention_workspace_bytes(const kda_config_t *cfg, int32_t num_kv_heads, int32_t N,
+                                           int64_t n_tokens, int32_t max_q);
+
+kda_status_t kda_paged_attention(const kda_config_t *cfg, const kda_kv_cache_t *cache, int32_t N, int64_t n_tokens,
+                                 int32_t max_q, const void *q, float scale, void *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
