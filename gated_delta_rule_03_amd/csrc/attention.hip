@@ -63,8 +63,15 @@ struct Split {
 struct Sequence {
   int first;          // its first row of q
   int tokens;         // new tokens
-  int64_t length;     // positions held
+  int length;         // positions held
 };
+
+// A value that is the same in every lane, as the compiler cannot see.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = uniform(static_cast<int>(x)), hi = uniform(static_cast<int>(x >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 __device__ __forceinline__ Sequence sequence(const CacheArgs& c, int n) {
   Sequence s;
@@ -73,21 +80,22 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& c, int n) {
   const int64_t last = end < c.n_tokens ? end : c.n_tokens;
   s.tokens = s.first < 0 || last <= s.first ? 0 : static_cast<int>(last - s.first);
   const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
-  const int64_t len = c.lengths[n];
-  s.length = len < 0 ? 0 : len < most ? len : most;
+  const int len = c.lengths[n];
+  s.length = len < 0 ? 0 : len < most ? len : static_cast<int>(most);
   return s;
 }
 
 // The line of all units' blocks: before[n] blocks in front of sequence n's.
 __device__ __forceinline__ void lay_out(const CacheArgs& c, int group, int rows, int64_t* before, int64_t* sums) {
   // each thread a run of neighbouring sequences, then the threads' sums
-  const int per = (c.N + blockDim.x - 1) / blockDim.x;
+  constexpr int kThreads = kWaves * 64;
+  const int per = (c.N + kThreads - 1) / kThreads;
   const int n0 = threadIdx.x * per, n1 = n0 + per < c.N ? n0 + per : c.N;
   int64_t mine = 0;
   for (int n = n0; n < n1; ++n) {
     const Sequence s = sequence(c, n);
     const int64_t tiles = (static_cast<int64_t>(s.tokens) * group + rows - 1) / rows;
-    before[n + 1] = mine += tiles * c.heads * ((s.length + kBlockPos - 1) / kBlockPos);
+    before[n + 1] = mine += tiles * c.heads * ((static_cast<int64_t>(s.length) + kBlockPos - 1) / kBlockPos);
   }
   sums[threadIdx.x] = mine;
   __syncthreads();
@@ -116,54 +124,95 @@ __device__ __forceinline__ void lay_out(const CacheArgs& c, int group, int rows,
 
 // A wave's step of 32 positions as it lies in memory.
 template <int D>
-struct RawStep {
-  uint32_t k[2][D / 32];                  // positions 2 (l % 16) and the next
-  uint32_t ks[D > 128 ? 2 : 1];           // their scale bytes, for each 32 channels of the lane
-  uint32_t v[8][D > 128 ? 2 : 1];         // positions 8 (l / 16) ..
-  uint2 vs;                               // their scale bytes
+struct RawKeys {
+  uint32_t w[2][D / 32];            // positions 2 (l % 16) and the next
+  uint32_t scale[D > 128 ? 2 : 1];  // their scale bytes, for each 32 channels of the lane
+};
+template <int D>
+struct RawValues {
+  uint32_t w[8][D > 128 ? 2 : 1];   // positions 8 (l / 16) ..
+  uint2 scale;                      // their scale bytes
 };
 
+// Where a lane's bytes of a step are, from the step's first byte.
 template <int D>
-__device__ __forceinline__ void load_step(const CacheArgs& c, int page, int head, int off, RawStep<D>& r) {
-  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const size_t values = values_at<D>(c, page, head), scales = scales_at<D>(c, page, head);
-  const int pos = off + 2 * j;
+struct LaneOffsets {
+  uint32_t k, ks[D > 128 ? 2 : 1], v, vs;
+
+  __device__ __forceinline__ explicit LaneOffsets(int page_shift) {
+    const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+    k = 2 * j * (D / 2) + g * (D / 8);
+#pragma unroll
+    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) ks[i] = ((g * D / 128 + i) << page_shift) + 2 * j;
+    v = 8 * g * (D / 2) + j * (D / 32);
+    vs = ((j * D / 512) << page_shift) + 8 * g;
+  }
+};
+
+// A step's first bytes in the cache; the same in every lane.
+struct StepAt {
+  int64_t values, scales;
+  bool held;
+};
+
+// Where a head's steps are: page_bytes apart from page to page.
+template <int D>
+__device__ __forceinline__ StepAt step_at(const CacheArgs& c, int seq, int64_t page_bytes, int64_t head_bytes,
+                                          uint32_t pos, bool inside) {
+  // through the scalar cache: a vector load here would wait for all those in flight
+  typedef const __attribute__((address_space(4))) int32_t* Scalar;
+  const int i = static_cast<int>(pos >> c.page_shift);
+  int page = -1;
+  if (inside && i < c.max_pages) page = ((Scalar)(c.table + static_cast<int64_t>(seq) * c.max_pages))[i];
+  const bool held = static_cast<uint32_t>(page) < static_cast<uint32_t>(c.num_pages);
+  const int64_t first = (held ? page : 0) * page_bytes + head_bytes;
+  const int off = static_cast<int>(pos & ((1u << c.page_shift) - 1));
+  return {first + static_cast<int64_t>(off) * (D / 2), (first >> 4) + off, held};
+}
+
+template <int D>
+__device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, const LaneOffsets<D>& lane, RawKeys<D>& r) {
+  const uint8_t* row = c.k + at.values;
+  const uint8_t* scales = c.k_scale + at.scales;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const uint8_t* from = c.k + values + static_cast<size_t>(pos + t) * (D / 2) + g * (D / 8);
     if constexpr (D == 64) {
-      const uint2 w = *reinterpret_cast<const uint2*>(from);
-      r.k[t][0] = w.x;
-      r.k[t][1] = w.y;
+      const uint2 w = *reinterpret_cast<const uint2*>(row + lane.k + t * (D / 2));
+      r.w[t][0] = w.x;
+      r.w[t][1] = w.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
-        const uint4 w = reinterpret_cast<const uint4*>(from)[i];
-        r.k[t][4 * i] = w.x;
-        r.k[t][4 * i + 1] = w.y;
-        r.k[t][4 * i + 2] = w.z;
-        r.k[t][4 * i + 3] = w.w;
+        const uint4 w = *reinterpret_cast<const uint4*>(row + lane.k + t * (D / 2) + 16 * i);
+        r.w[t][4 * i] = w.x;
+        r.w[t][4 * i + 1] = w.y;
+        r.w[t][4 * i + 2] = w.z;
+        r.w[t][4 * i + 3] = w.w;
       }
     }
   }
-  const int block = g * D / 128;   // of the lane's first channel
 #pragma unroll
-  for (int i = 0; i < (D > 128 ? 2 : 1); ++i)
-    r.ks[i] = *reinterpret_cast<const uint16_t*>(c.k_scale + scales + (static_cast<size_t>(block + i) << c.page_shift) + pos);
-  const uint8_t* from = c.v + values + static_cast<size_t>(off + 8 * g) * (D / 2) + j * (D / 32);
+  for (int i = 0; i < (D > 128 ? 2 : 1); ++i) r.scale[i] = *reinterpret_cast<const uint16_t*>(scales + lane.ks[i]);
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const CacheArgs& c, const StepAt& at, const LaneOffsets<D>& lane,
+                                            RawValues<D>& r) {
+  const uint8_t* row = c.v + at.values;
+  r.scale = *reinterpret_cast<const uint2*>(c.v_scale + at.scales + lane.vs);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    const uint8_t* from = row + lane.v + e * (D / 2);
     if constexpr (D == 64) {
-      r.v[e][0] = *reinterpret_cast<const uint16_t*>(from + e * (D / 2));
+      r.w[e][0] = *reinterpret_cast<const uint16_t*>(from);
     } else if constexpr (D == 128) {
-      r.v[e][0] = *reinterpret_cast<const uint32_t*>(from + e * (D / 2));
+      r.w[e][0] = *reinterpret_cast<const uint32_t*>(from);
     } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(from + e * (D / 2));
-      r.v[e][0] = w.x;
-      r.v[e][1] = w.y;
+      const uint2 w = *reinterpret_cast<const uint2*>(from);
+      r.w[e][0] = w.x;
+      r.w[e][1] = w.y;
     }
   }
-  r.vs = *reinterpret_cast<const uint2*>(c.v_scale + scales + (static_cast<size_t>(j * D / 512) << c.page_shift) + off + 8 * g);
 }
 
 __device__ __forceinline__ float scale_of(uint32_t bytes, int i) {
@@ -187,32 +236,39 @@ struct Rows {
   float m[MT], l[MT];    // running maximum (of the row), sum of this lane's weights
 };
 
-template <int D, int MT, int QP, int PP, bool MASKED>
-__device__ __forceinline__ void attend_step(const RawStep<D>& r, const SplitN<QP> (&q)[MT][D / 32], float scale,
-                                            int64_t at, const int64_t (&sees)[MT], const CacheArgs& c, int page,
-                                            int head, int off, Rows<D, MT>& acc) {
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  f32x4 s[MT][2];
+// S^T of a step: element (position 8 g + e, row j) in s[.][e & 1][e >> 1].
+template <int D, int MT, int QP>
+__device__ __forceinline__ void scores(const RawKeys<D>& r, const SplitN<QP> (&q)[MT][D / 32], f32x4 (&s)[MT][2]) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) s[m][0] = s[m][1] = zero4();
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const bf16x8 k = widen8(r.k[t][i], scale_of(D > 128 && i >= 4 ? r.ks[D > 128 ? 1 : 0] : r.ks[0], t));
+    for (int t = 0; t < 2; ++t) {
+      const bf16x8 k = widen8(r.w[t][i], scale_of(D > 128 && i >= 4 ? r.scale[D > 128 ? 1 : 0] : r.scale[0], t));
 #pragma unroll
       for (int p = QP - 1; p >= 0; --p)
 #pragma unroll
         for (int m = 0; m < MT; ++m) s[m][t] = mfma(k, q[m][i].v[p], s[m][t]);
     }
+}
+
+// The step's weights, and its values' part of the sums.
+// `whole`: every row sees all of its positions.
+template <int D, int MT, int PP>
+__device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT][2], float scale, bool whole,
+                                      uint32_t at, const uint32_t (&sees)[MT], const uint8_t* v_scales, int page_shift,
+                                      Rows<D, MT>& acc) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
   uint32_t w[MT][4][PP];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     float x[8];   // position 8 g + e
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = s[m][e & 1][e >> 1] * scale;
-      if constexpr (MASKED) x[e] = at + 8 * g + e < sees[m] ? x[e] : neg_inf();
+    for (int e = 0; e < 8; ++e) x[e] = s[m][e & 1][e >> 1] * scale;
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = at + 8 * g + e < sees[m] ? x[e] : neg_inf();
     }
     float top = x[0];
 #pragma unroll
@@ -239,21 +295,24 @@ __device__ __forceinline__ void attend_step(const RawStep<D>& r, const SplitN<QP
     for (int e = 0; e < 4; ++e) split_pair<PP>(x[2 * e], x[2 * e + 1], w[m][e]);
   }
   float vs[8];
-  bool bad = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t byte = ((e < 4 ? r.vs.x : r.vs.y) >> (8 * (e & 3))) & 0xffu;
-    // what not every row sees must not meet a weight of 0 as a NaN or an infinity
-    const bool out = MASKED && byte >= 253;
-    bad |= out;
-    vs[e] = __uint_as_float(out ? 0u : byte << 23);
+  for (int e = 0; e < 8; ++e) vs[e] = scale_of(e < 4 ? r.scale.x : r.scale.y, e & 3);
+  bool bad = false;
+  if (!whole) {   // what not every row sees must not meet a weight of 0 as a NaN or an infinity
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool out = vs[e] >= 0x1p126f;   // bytes 253 and up
+      bad |= out;
+      vs[e] = out ? 0.0f : vs[e];
+    }
   }
 #pragma unroll
   for (int b = 0; b < D / 32; ++b) {   // a byte: two channels
+    __builtin_amdgcn_sched_barrier(0);
     uint32_t x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t word = r.v[e][b >> 2];
+      const uint32_t word = r.w[e][b >> 2];
       x[e] = (b & 3) == 0 ? widen<0>(word, vs[e]) : (b & 3) == 1 ? widen<1>(word, vs[e])
              : (b & 3) == 2 ? widen<2>(word, vs[e]) : widen<3>(word, vs[e]);
     }
@@ -274,20 +333,18 @@ __device__ __forceinline__ void attend_step(const RawStep<D>& r, const SplitN<QP
         acc.o[m][2 * b + 1] = mfma(v1, pw, acc.o[m][2 * b + 1]);
       }
   }
-  if constexpr (MASKED) {
-    if (__any(bad)) {   // a row that sees such a value has NaN in its 32 channels
-      const uint8_t* scales = c.v_scale + scales_at<D>(c, page, head) + off;
+  if (!whole && __any(bad)) {   // a row that sees such a value has NaN in its 32 channels
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* of = scales + (static_cast<size_t>((4 * g + i) * D / 512) << c.page_shift);
-        for (int e = 0; e < kStep; ++e) {
-          if (of[e] < 253) continue;
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* of = v_scales + (static_cast<uint32_t>((4 * g + i) * D / 512) << page_shift);
+#pragma unroll 1
+      for (int e = 0; e < kStep; ++e) {
+        if (of[e] < 253) continue;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-            if (at + e < sees[m])
+        for (int m = 0; m < MT; ++m)
+          if (at + e < sees[m])
 #pragma unroll
-              for (int x = 0; x < D / 16; ++x) acc.o[m][x][i] = __uint_as_float(0x7fc00000u);
-        }
+            for (int x = 0; x < D / 16; ++x) acc.o[m][x][i] = __uint_as_float(0x7fc00000u);
       }
     }
   }
@@ -309,7 +366,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   __shared__ float meet[kWaves][16][kPitch];
   __shared__ float tops[kWaves][kRows][2];
   extern __shared__ int64_t before[];   // [N + 1]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
   const int Hq = c.heads * group;
   lay_out(c, group, kRows, before, reinterpret_cast<int64_t*>(meet));
   const int64_t total = before[c.N];
@@ -317,17 +374,19 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   const int64_t start = share * blockIdx.x;
   const int64_t end = start + share < total ? start + share : total;
   Split split = {0, 0, 0, 0};
+  const LaneOffsets<D> lanes(c.page_shift);
+  const int64_t page_bytes = static_cast<int64_t>(c.heads) * (D / 2) << c.page_shift;
 
   // sequences that hold nothing: their rows see nothing
   for (int n = blockIdx.x; n < c.N; n += gridDim.x) {
     const Sequence s = sequence(c, n);
     if (s.length > 0) continue;
-    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq * (D / 8); i += blockDim.x) {
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq * (D / 8); i += kWaves * 64) {
       const float zero[8] = {};
       store_n<PP == 2, 8>(o, static_cast<size_t>(s.first) * Hq * D + i * 8, zero);
     }
     if (lse)
-      for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq; i += blockDim.x)
+      for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq; i += kWaves * 64)
         lse[static_cast<size_t>(s.first) * Hq + i] = neg_inf();
   }
 
@@ -338,19 +397,23 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
       if (before[mid] <= cur) n = mid;
       else hi = mid;
     }
+    n = uniform(n);
     const Sequence s = sequence(c, n);
-    const int64_t blocks = (s.length + kBlockPos - 1) / kBlockPos;
+    const int blocks = static_cast<int>((static_cast<int64_t>(s.length) + kBlockPos - 1) / kBlockPos);
     const int rows = s.tokens * group;
     const int tiles = (rows + kRows - 1) / kRows;
-    const int64_t local = cur - before[n];
+    const int64_t local = uniform(cur - before[n]);
     const int64_t unit = local / blocks;
-    const int64_t b0 = local - unit * blocks;
-    const int64_t b1 = b0 + (end - cur) < blocks ? b0 + (end - cur) : blocks;
+    const int b0 = static_cast<int>(local - unit * blocks);
+    const int b1 = end - cur < blocks - b0 ? b0 + static_cast<int>(end - cur) : blocks;
     const int head = static_cast<int>(unit / tiles), tile = static_cast<int>(unit - static_cast<int64_t>(head) * tiles);
     // this lane's rows
     SplitN<QP> qf[MT][D / 32];
-    int64_t sees[MT];
-    int64_t least = INT64_MAX, most = 0;   // positions that every row sees, and that any does
+    uint32_t sees[MT];
+    auto seen = [&](int row) {   // positions that a row sees
+      const int x = s.length - s.tokens + row / group + 1;
+      return static_cast<uint32_t>(x < 0 ? 0 : x);
+    };
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = tile * kRows + m * 16 + j;
@@ -365,13 +428,10 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
           qf[m][i] = load_split<QP>(static_cast<const float*>(q) + from + 8 * i);
         }
       }
-      sees[m] = s.length - s.tokens + t + 1;
+      sees[m] = seen(r);
     }
-    {
-      const int last = (tile + 1) * kRows < rows ? (tile + 1) * kRows : rows;
-      least = s.length - s.tokens + tile * kRows / group + 1;
-      most = s.length - s.tokens + (last - 1) / group + 1;
-    }
+    // positions that every row sees, and that any does
+    const uint32_t least = seen(tile * kRows), most = seen(((tile + 1) * kRows < rows ? (tile + 1) * kRows : rows) - 1);
     Rows<D, MT> acc;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -380,18 +440,34 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc.o[m][i] = zero4();
     }
-    for (int64_t b = b0; b < b1; ++b) {
-      const int64_t at = b * kBlockPos + wave * kStep;
-      if (at >= most) break;
-      const int page = __builtin_amdgcn_readfirstlane(page_of(c, n, at));
-      if (page < 0) continue;
-      const int off = static_cast<int>(at & ((1 << c.page_shift) - 1));
-      RawStep<D> raw;
-      load_step<D>(c, page, head, off, raw);
-      if (at + kStep <= least)
-        attend_step<D, MT, QP, PP, false>(raw, qf, scale, at, sees, c, page, head, off, acc);
-      else
-        attend_step<D, MT, QP, PP, true>(raw, qf, scale, at, sees, c, page, head, off, acc);
+    // A step's values are on their way while its scores are formed, the next
+    // step's keys while its values are weighed, the page after that meanwhile.
+    const int64_t head_bytes = static_cast<int64_t>(head) * (D / 2) << c.page_shift;
+    const uint32_t first_pos = wave * kStep;
+    int stop = most > first_pos ? static_cast<int>((most - first_pos + kBlockPos - 1) / kBlockPos) : 0;
+    stop = c.num_pages == 0 ? b0 : stop < b1 ? stop : b1;   // blocks in front of it have a step to be seen
+    if (b0 < stop) {
+      auto place = [&](int b) {
+        return step_at<D>(c, n, page_bytes, head_bytes, static_cast<uint32_t>(b) * kBlockPos + first_pos, b < stop);
+      };
+      StepAt here = place(b0);
+      RawKeys<D> keys;
+      load_keys<D>(c, here, lanes, keys);
+      StepAt next = place(b0 + 1);
+      for (int b = b0; b < stop; ++b) {
+        const uint32_t at = static_cast<uint32_t>(b) * kBlockPos + first_pos;
+        RawValues<D> values;
+        load_values<D>(c, here, lanes, values);
+        f32x4 s4[MT][2];
+        scores<D, MT, QP>(keys, qf, s4);
+        __builtin_amdgcn_sched_barrier(0);
+        load_keys<D>(c, next, lanes, keys);
+        const StepAt after = place(b + 2);
+        if (here.held)
+          weigh<D, MT, PP>(values, s4, scale, at + kStep <= least, at, sees, c.v_scale + here.scales, c.page_shift, acc);
+        here = next;
+        next = after;
+      }
     }
     // the waves' sums joined, 16 rows at a time
     const bool whole = b0 == 0 && b1 == blocks;

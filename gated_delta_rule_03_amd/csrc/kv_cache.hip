@@ -291,7 +291,7 @@ hipError_t with_head(int D, bool bf16, F&& f) {
 }
 
 dim3 grid_of(int D, int64_t groups) {
-  return dim3(static_cast<unsigned>(std::min<int64_t>((groups * (D / 16) + kThreads - 1) / kThreads, 1 << 20)));
+  return dim3(static_cast<unsigned>(std::min<int64_t>((groups * (D / 16) + kThreads - 1) / kThreads, 256 * 16)));
 }
 
 }  // namespace

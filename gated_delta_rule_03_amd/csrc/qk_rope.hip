@@ -20,7 +20,6 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAtOnce = 4;   // heads whose loads are in flight together
 
 template <int D, bool INTER>
 __device__ __forceinline__ void sines(const RopeArgs& r, const PairRates& p, int64_t token, float (&c)[8],
@@ -37,8 +36,9 @@ __device__ __forceinline__ void sines(const RopeArgs& r, const PairRates& p, int
 }  // namespace
 
 // Group g of lanes takes token g / runs and the run g % runs of its heads: the
-// runs of q's heads, then those of k's.
-template <int D, bool IN_BF16, bool OUT_BF16, bool INTER>
+// runs of q's heads, then those of k's.  kAtOnce: heads whose loads are in flight
+// together.
+template <int D, bool IN_BF16, bool OUT_BF16, bool INTER, int kAtOnce>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs r, QkArgs x, int run_len, float eps) {
   constexpr int L = D / 16;
   const int lane = threadIdx.x % L;
@@ -101,11 +101,11 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs r, QkAr
 // of k's; a lane keeps its channels, so both weights' gradients gather in its
 // registers.  A workgroup joins its lanes in LDS and leaves one row of `part`,
 // [2][D].  Groups and the order of every sum depend on the sizes alone.
-template <int D, bool IN_BF16, bool OUT_BF16, bool INTER>
+template <int D, bool IN_BF16, bool OUT_BF16, bool INTER, int kPair>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, QkArgs x, int run_len, float eps,
                                                                     float* __restrict__ part) {
   constexpr int L = D / 16;
-  __shared__ float red[kThreads][8];
+  __shared__ float red[4][kThreads][8];   // q's and k's weight, the two runs of each
   const int lane = threadIdx.x % L;
   const HeadRuns<D, INTER> runs(lane, r.rotary_dim);
   const PairRates rates = pair_rates<D, INTER>(r, runs);
@@ -133,7 +133,6 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, 
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = -s[e];   // back
       }
-      constexpr int kPair = 2;
       for (int h = h0; h < h1; h += kPair) {
         float a[kPair][8], b[kPair][8], ga[kPair][8], gb[kPair][8];
 #pragma unroll
@@ -175,20 +174,20 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, 
         }
       }
     }
-    // the lanes of a channel joined: lane l of every group, a run at a time
+    store_n<false, 8>(&red[2 * which][threadIdx.x][0], 0, da);
+    store_n<false, 8>(&red[2 * which + 1][threadIdx.x][0], 0, db);
+  }
+  // the lanes of a channel joined: lane l of every group
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const int set = i / (8 * L), l = i / 8 % L, e = i % 8;
+    const HeadRuns<D, INTER> to(l, r.rotary_dim);
+    float t[4] = {};
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      __syncthreads();
-      store_n<false, 8>(&red[threadIdx.x][0], 0, half ? db : da);
-      __syncthreads();
-      if (threadIdx.x < 8 * L) {
-        const int l = threadIdx.x / 8, e = threadIdx.x % 8;
-        const HeadRuns<D, INTER> to(l, r.rotary_dim);
-        float t = 0.f;
-        for (int k = l; k < kThreads; k += L) t += red[k][e];
-        part[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + (half ? to.b : to.a) + e] = t;
-      }
-    }
+    for (int k = 0; k < kThreads / L; k += 4)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) t[x] += red[set][(k + x) * L + l][e];
+    part[(static_cast<size_t>(blockIdx.x) * 2 + set / 2) * D + (set & 1 ? to.b : to.a) + e] = (t[0] + t[1]) + (t[2] + t[3]);
   }
 }
 
@@ -234,10 +233,12 @@ hipError_t launch_qk_norm_rope(int D, const RopeArgs& r, const QkArgs& x, float 
                                hipStream_t st) {
   const int run = run_length(D, r.n_tokens, x.heads[0] + x.heads[1]);
   const int64_t blocks = (groups_of(x, r.n_tokens, run) * (D / 16) + kThreads - 1) / kThreads;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20)));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 256 * 16)));
   return with_shape(D, in_bf16, out_bf16, r.interleaved, [&](auto d, auto ib, auto ob, auto inter) {
-    qk_norm_rope_kernel<decltype(d)::value, decltype(ib)::value, decltype(ob)::value, decltype(inter)::value>
-        <<<grid, kThreads, 0, st>>>(r, x, run, eps);
+    constexpr int kD = decltype(d)::value;
+    constexpr bool kIn = decltype(ib)::value, kOut = decltype(ob)::value, kInter = decltype(inter)::value;
+    if (run == 1) qk_norm_rope_kernel<kD, kIn, kOut, kInter, 1><<<grid, kThreads, 0, st>>>(r, x, run, eps);
+    else qk_norm_rope_kernel<kD, kIn, kOut, kInter, 4><<<grid, kThreads, 0, st>>>(r, x, run, eps);
   });
 }
 
@@ -253,8 +254,10 @@ hipError_t launch_qk_norm_rope_bwd(int D, const RopeArgs& r, const QkArgs& x, fl
   if (parts > 0) {
     const int run = run_length(D, r.n_tokens, x.heads[0] + x.heads[1]);
     const hipError_t e = with_shape(D, in_bf16, out_bf16, r.interleaved, [&](auto d, auto ib, auto ob, auto inter) {
-      qk_norm_rope_bwd_kernel<decltype(d)::value, decltype(ib)::value, decltype(ob)::value, decltype(inter)::value>
-          <<<dim3(parts), kThreads, 0, st>>>(r, x, run, eps, part);
+      constexpr int kD = decltype(d)::value;
+      constexpr bool kIn = decltype(ib)::value, kOut = decltype(ob)::value, kInter = decltype(inter)::value;
+      if (run == 1) qk_norm_rope_bwd_kernel<kD, kIn, kOut, kInter, 1><<<dim3(parts), kThreads, 0, st>>>(r, x, run, eps, part);
+      else qk_norm_rope_bwd_kernel<kD, kIn, kOut, kInter, 2><<<dim3(parts), kThreads, 0, st>>>(r, x, run, eps, part);
     });
     if (e != hipSuccess) return e;
   }

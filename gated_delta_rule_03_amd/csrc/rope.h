@@ -16,8 +16,6 @@
 
 namespace kda {
 
-constexpr int kMaxAxes = 4;
-
 template <int D, bool INTER>
 struct HeadRuns {
   int a, b;            // first channels of the two runs
@@ -50,39 +48,46 @@ struct PairRates {
   uint32_t axes;
 };
 
+// (Every load is made, of pair 0 where a lane turns nothing, so that none waits
+// for another: under conditions these 16 took 10 us of a small call.)
 template <int D, bool INTER>
 __device__ __forceinline__ PairRates pair_rates(const RopeArgs& r, const HeadRuns<D, INTER>& runs) {
   constexpr double kPerTurn = 0.15915494309189533577;   // 1 / (2 pi)
-  PairRates p;
-  p.axes = 0;
+  PairRates p = {};
+  if (r.rotary_dim == 0) return p;
+  float f[8];
+  int ax[8] = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = r.inv_freq[runs.turned(e) ? runs.pair(e) : 0];
+  if (r.axis) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ax[e] = r.axis[runs.turned(e) ? runs.pair(e) : 0];
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    p.rate[e] = 0.0;
-    if (runs.turned(e)) {
-      p.rate[e] = static_cast<double>(r.inv_freq[runs.pair(e)]) * kPerTurn;
-      if (r.axis) {
-        const int ax = r.axis[runs.pair(e)];
-        p.axes |= static_cast<uint32_t>(ax < 0 ? 0 : ax >= r.num_axes ? r.num_axes - 1 : ax) << (2 * e);
-      }
-    }
+    p.rate[e] = runs.turned(e) ? static_cast<double>(f[e]) * kPerTurn : 0.0;
+    p.axes |= static_cast<uint32_t>(ax[e] < 0 ? 0 : ax[e] >= r.num_axes ? r.num_axes - 1 : ax[e]) << (2 * e);
   }
   return p;
 }
 
-// The token's positions on every axis.
+// The token's positions on every axis.  (Four scalars: an array that is indexed
+// at run time goes to LDS, whose address then takes the workgroup's size from
+// the dispatch packet in host memory, which cost 8 us of a small call.)
 struct Places {
-  int32_t at[kMaxAxes];
+  int32_t x0, x1, x2, x3;
 
   __device__ __forceinline__ Places(const RopeArgs& r, int64_t token) {
-#pragma unroll
-    for (int x = 0; x < kMaxAxes; ++x) at[x] = x < r.num_axes ? r.positions[x * r.n_tokens + token] : 0;
+    const int32_t* p = r.positions + token;
+    x0 = p[0];
+    x1 = p[r.num_axes > 1 ? r.n_tokens : 0];
+    x2 = p[r.num_axes > 2 ? 2 * r.n_tokens : 0];
+    x3 = p[r.num_axes > 3 ? 3 * r.n_tokens : 0];
   }
-  __device__ __forceinline__ explicit Places(int32_t everywhere) {
-#pragma unroll
-    for (int x = 0; x < kMaxAxes; ++x) at[x] = everywhere;
-  }
+  __device__ __forceinline__ explicit Places(int32_t everywhere) : x0(everywhere), x1(everywhere), x2(everywhere), x3(everywhere) {}
   __device__ __forceinline__ int32_t on(uint32_t axis) const {
-    return axis < 2 ? (axis == 0 ? at[0] : at[1]) : (axis == 2 ? at[2] : at[3]);
+    const int32_t lo = axis & 1 ? x1 : x0, hi = axis & 1 ? x3 : x2;
+    return axis & 2 ? hi : lo;
   }
 };
 
