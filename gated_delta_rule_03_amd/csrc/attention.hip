@@ -16,9 +16,17 @@
 // The running maximum of a row is raised only when a score passes it by 2^8:
 // weights then reach 256, which neither fp32 sums nor bf16 operands mind, and
 // the accumulators are rescaled a few times a row instead of at every step.
-// Weights enter the matrix cores as the sum of PP bf16 values (2 for bf16
-// outputs: their rounding alone costs as much as the output's own; 3 for fp32),
-// queries as QP (1 or 3); keys and values are exact in bf16.
+//
+// Precision, by the output's type.  bf16: keys enter the matrix cores as they
+// lie in the cache (4-bit operands with their e8m0 scales), queries as the sum of
+// three 6-bit values (e2m3) with a scale for 32 channels, each the rounding of
+// what the last one left: every product and every sum of eight is exact, and a
+// query is off by at most 2^-14 of its block's largest (a bf16 one by nothing
+// above 2^-7 of it).  Next to widened keys that takes half the matrix cores'
+// time and none of the vector units'.  The weights are the sum of two bf16
+// values up to 16 rows, where the cache's bytes set the time, and one above; the
+// sum that divides is then of the rounded weights.  fp32: keys widened to bf16
+// (exact), queries as one or three bf16 values, weights as three.
 //
 // Work: all (sequence, key head, row tile) units are laid end to end in blocks
 // of 128 positions, and every workgroup takes an equal share of that line, so
@@ -122,10 +130,19 @@ __device__ __forceinline__ void lay_out(const CacheArgs& c, int group, int rows,
   __syncthreads();
 }
 
-// A wave's step of 32 positions as it lies in memory.
-template <int D>
+// How queries and keys meet: 6-bit pieces of queries and the keys' own 4 bits, or
+// one or three bf16 pieces and keys widened to bf16.
+enum class Qk { kF6 = 0, kBf16 = 1, kFp32 = 3 };
+
+// A wave's step of 32 positions as it lies in memory.  Of a position's key a lane
+// reads d / 4 channels (with 64 channels and 4-bit operands 32, lanes 32 and up
+// what lanes 0 and up do, against queries of 0).
+template <int D, Qk QK>
+constexpr int kKeyWords = QK == Qk::kF6 && D == 64 ? 4 : D / 32;
+
+template <int D, Qk QK>
 struct RawKeys {
-  uint32_t w[2][D / 32];            // positions 2 (l % 16) and the next
+  uint32_t w[2][kKeyWords<D, QK>];  // positions 2 (l % 16) and the next
   uint32_t scale[D > 128 ? 2 : 1];  // their scale bytes, for each 32 channels of the lane
 };
 template <int D>
@@ -135,15 +152,16 @@ struct RawValues {
 };
 
 // Where a lane's bytes of a step are, from the step's first byte.
-template <int D>
+template <int D, Qk QK>
 struct LaneOffsets {
   uint32_t k, ks[D > 128 ? 2 : 1], v, vs;
 
   __device__ __forceinline__ explicit LaneOffsets(int page_shift) {
     const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-    k = 2 * j * (D / 2) + g * (D / 8);
+    const int part = QK == Qk::kF6 && D == 64 ? 2 * (g & 1) : g;   // quarter of the head
+    k = 2 * j * (D / 2) + part * (D / 8);
 #pragma unroll
-    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) ks[i] = ((g * D / 128 + i) << page_shift) + 2 * j;
+    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) ks[i] = ((part * D / 128 + i) << page_shift) + 2 * j;
     v = 8 * g * (D / 2) + j * (D / 32);
     vs = ((j * D / 512) << page_shift) + 8 * g;
   }
@@ -170,19 +188,21 @@ __device__ __forceinline__ StepAt step_at(const CacheArgs& c, int seq, int64_t p
   return {first + static_cast<int64_t>(off) * (D / 2), (first >> 4) + off, held};
 }
 
-template <int D>
-__device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, const LaneOffsets<D>& lane, RawKeys<D>& r) {
+template <int D, Qk QK>
+__device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, const LaneOffsets<D, QK>& lane,
+                                          RawKeys<D, QK>& r) {
   const uint8_t* row = c.k + at.values;
   const uint8_t* scales = c.k_scale + at.scales;
+  constexpr int kWords = kKeyWords<D, QK>;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    if constexpr (D == 64) {
+    if constexpr (kWords == 2) {
       const uint2 w = *reinterpret_cast<const uint2*>(row + lane.k + t * (D / 2));
       r.w[t][0] = w.x;
       r.w[t][1] = w.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < D / 128; ++i) {
+      for (int i = 0; i < kWords / 4; ++i) {
         const uint4 w = *reinterpret_cast<const uint4*>(row + lane.k + t * (D / 2) + 16 * i);
         r.w[t][4 * i] = w.x;
         r.w[t][4 * i + 1] = w.y;
@@ -195,8 +215,8 @@ __device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, 
   for (int i = 0; i < (D > 128 ? 2 : 1); ++i) r.scale[i] = *reinterpret_cast<const uint16_t*>(scales + lane.ks[i]);
 }
 
-template <int D>
-__device__ __forceinline__ void load_values(const CacheArgs& c, const StepAt& at, const LaneOffsets<D>& lane,
+template <int D, Qk QK>
+__device__ __forceinline__ void load_values(const CacheArgs& c, const StepAt& at, const LaneOffsets<D, QK>& lane,
                                             RawValues<D>& r) {
   const uint8_t* row = c.v + at.values;
   r.scale = *reinterpret_cast<const uint2*>(c.v_scale + at.scales + lane.vs);
@@ -236,25 +256,144 @@ struct Rows {
   float m[MT], l[MT];    // running maximum (of the row), sum of this lane's weights
 };
 
+// Queries of 16 rows as operands: a lane holds the channels of its keys.
+template <int D, Qk QK>
+struct Queries {
+  SplitN<static_cast<int>(QK)> v[D / 32];
+};
+
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
+
+template <int D>
+struct Queries<D, Qk::kF6> {
+  static constexpr int kBlocks = D > 128 ? 2 : 1;
+  u32x6 v[kBlocks][3];         // 32 channels each
+  uint32_t scale[kBlocks];     // their e8m0 scales, a byte a piece
+};
+
+// x as three 6-bit pieces.  With max|x| = 1.m 2^p the first's unit is 2^(p - 2)
+// where 1.m <= 1.875 (e2m3 reaches 7.5) and 2^(p - 1) above; what it leaves is at
+// most 4 units of 2^-4 of its own, and so on.
+__device__ __forceinline__ void split_e2m3(float (&x)[32], u32x6 (&v)[3], uint32_t& scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const uint32_t b = __float_as_uint(x[e]) & 0x7fffffffu;
+    top = b > top ? b : top;
+  }
+  const int p = static_cast<int>(top >> 23);
+  int byte = p - 2 + ((top & 0x7fffffu) > 0x700000u);
+  byte = byte < 9 ? 9 : byte;
+  if (p == 255) {   // NaN, infinity: every product with the block is NaN
+    scale = 0xffffffu;
+    v[0] = v[1] = v[2] = u32x6{0, 0, 0, 0, 0, 0};
+    return;
+  }
+  scale = static_cast<uint32_t>(byte) | static_cast<uint32_t>(byte - 4) << 8 | static_cast<uint32_t>(byte - 8) << 16;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const float s = __uint_as_float(static_cast<uint32_t>(byte - 4 * i) << 23);
+    f32x16 even, odd;   // the conversion takes its elements from two vectors in turn
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      even[e] = x[2 * e];
+      odd[e] = x[2 * e + 1];
+    }
+    v[i] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, s);
+    if (i < 2) {
+      const f32x32 got = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(v[i], s);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] -= got[e];
+    }
+  }
+}
+
+// row: the first element of the row's head; flip: 0x80008000 turns every sign.
+template <int D, Qk QK, bool BF16>
+__device__ __forceinline__ void load_queries(const void* q, size_t row, uint32_t flip, Queries<D, QK>& r) {
+  const int g = (threadIdx.x & 63) >> 4;
+  if constexpr (QK == Qk::kF6) {
+#pragma unroll
+    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) {
+      float x[32];
+      const size_t at = row + (D == 64 ? 32 * (g & 1) : g * (D / 4) + 32 * i);
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        float y[8];
+        load_n<BF16, 8>(q, at + e, y);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) x[e + z] = D == 64 && g >= 2 ? 0.0f : __uint_as_float(__float_as_uint(y[z]) ^ (flip & 0x80000000u));
+      }
+      split_e2m3(x, r.v[i], r.scale[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const size_t at = row + g * (D / 4) + 8 * i;
+      if constexpr (BF16) r.v[i].v[0] = load_bf16x8(static_cast<const uint16_t*>(q) + at);
+      else r.v[i] = load_split<3>(static_cast<const float*>(q) + at);
+#pragma unroll
+      for (int p = 0; p < static_cast<int>(QK); ++p) {
+        uint4 w = __builtin_bit_cast(uint4, r.v[i].v[p]);
+        w.x ^= flip;
+        w.y ^= flip;
+        w.z ^= flip;
+        w.w ^= flip;
+        r.v[i].v[p] = __builtin_bit_cast(bf16x8, w);
+      }
+    }
+  }
+}
+
+// c += the keys of position t of each pair (4 bits) times piece P of the queries.
+template <int T, int P>
+__device__ __forceinline__ f32x4 mfma_f4f6(const uint32_t* k, uint32_t k_scale, const u32x6& q, uint32_t q_scale, f32x4 c) {
+  const i32x8 a = {static_cast<int>(k[0]), static_cast<int>(k[1]), static_cast<int>(k[2]), static_cast<int>(k[3]), 0, 0, 0, 0};
+  const i32x8 b = {static_cast<int>(q[0]), static_cast<int>(q[1]), static_cast<int>(q[2]), static_cast<int>(q[3]),
+                   static_cast<int>(q[4]), static_cast<int>(q[5]), 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 2, T, static_cast<int>(k_scale), P,
+                                                          static_cast<int>(q_scale));
+}
+
 // S^T of a step: element (position 8 g + e, row j) in s[.][e & 1][e >> 1].
-template <int D, int MT, int QP>
-__device__ __forceinline__ void scores(const RawKeys<D>& r, const SplitN<QP> (&q)[MT][D / 32], f32x4 (&s)[MT][2]) {
+template <int D, int MT, Qk QK>
+__device__ __forceinline__ void scores(const RawKeys<D, QK>& r, const Queries<D, QK> (&q)[MT], f32x4 (&s)[MT][2]) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) s[m][0] = s[m][1] = zero4();
+  if constexpr (QK == Qk::kF6) {
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) {
+      auto piece = [&](auto p) {
+        constexpr int P = decltype(p)::value;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const bf16x8 k = widen8(r.w[t][i], scale_of(D > 128 && i >= 4 ? r.scale[D > 128 ? 1 : 0] : r.scale[0], t));
-#pragma unroll
-      for (int p = QP - 1; p >= 0; --p)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) s[m][t] = mfma(k, q[m][i].v[p], s[m][t]);
+        for (int m = 0; m < MT; ++m) {
+          s[m][0] = mfma_f4f6<0, P>(&r.w[0][4 * i], r.scale[i], q[m].v[i][P], q[m].scale[i], s[m][0]);
+          s[m][1] = mfma_f4f6<1, P>(&r.w[1][4 * i], r.scale[i], q[m].v[i][P], q[m].scale[i], s[m][1]);
+        }
+      };
+      piece(std::integral_constant<int, 2>{});
+      piece(std::integral_constant<int, 1>{});
+      piece(std::integral_constant<int, 0>{});
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const bf16x8 k = widen8(r.w[t][i], scale_of(D > 128 && i >= 4 ? r.scale[D > 128 ? 1 : 0] : r.scale[0], t));
+#pragma unroll
+        for (int p = static_cast<int>(QK) - 1; p >= 0; --p)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) s[m][t] = mfma(k, q[m].v[i].v[p], s[m][t]);
+      }
+  }
 }
 
 // The step's weights, and its values' part of the sums.
-// `whole`: every row sees all of its positions.
+// scale > 0 (queries carry its sign); `whole`: every row sees all of the positions.
 template <int D, int MT, int PP>
 __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT][2], float scale, bool whole,
                                       uint32_t at, const uint32_t (&sees)[MT], const uint8_t* v_scales, int page_shift,
@@ -265,7 +404,7 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
   for (int m = 0; m < MT; ++m) {
     float x[8];   // position 8 g + e
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = s[m][e & 1][e >> 1] * scale;
+    for (int e = 0; e < 8; ++e) x[e] = s[m][e & 1][e >> 1];
     if (!whole) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = at + 8 * g + e < sees[m] ? x[e] : neg_inf();
@@ -273,6 +412,7 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
     float top = x[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+    top *= scale;
     if (__any(top > acc.m[m] + kRaise)) {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -284,15 +424,21 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
       for (int i = 0; i < D / 16; ++i) acc.o[m][i] *= down;
     }
     const float base = acc.m[m] == neg_inf() ? 0.0f : acc.m[m];
-    float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = __builtin_amdgcn_exp2f(x[e] - base);
-      sum += x[e];
-    }
-    acc.l[m] += sum;
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], scale, -base));
 #pragma unroll
     for (int e = 0; e < 4; ++e) split_pair<PP>(x[2 * e], x[2 * e + 1], w[m][e]);
+    float sum = 0.f;
+    if constexpr (PP == 1) {   // of the weights as they are used
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[m][e][0]),
+                                              __builtin_bit_cast(bf16x2, sreg(0x3f803f80u)), sum, false);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += x[e];
+    }
+    acc.l[m] += sum;
   }
   float vs[8];
 #pragma unroll
@@ -357,7 +503,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 }  // namespace
 
-template <int D, int MT, int QP, int PP>
+template <int D, int MT, Qk QK, int PP, bool IN_BF16, bool OUT_BF16>
 __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged_attention_kernel(
     CacheArgs c, const void* __restrict__ q, int group, float scale, void* __restrict__ o, float* __restrict__ lse,
     Split* __restrict__ splits, float* __restrict__ pieces) {
@@ -368,13 +514,16 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   extern __shared__ int64_t before[];   // [N + 1]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
   const int Hq = c.heads * group;
+  // a negative scale turns the queries' sign; of 0 every score is 0, as of the least (where -infinity stays what it is)
+  const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
+  scale = fminf(fmaxf(fabsf(scale), 1.17549435e-38f), 3.4028235e38f);
   lay_out(c, group, kRows, before, reinterpret_cast<int64_t*>(meet));
   const int64_t total = before[c.N];
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   const int64_t start = share * blockIdx.x;
   const int64_t end = start + share < total ? start + share : total;
   Split split = {0, 0, 0, 0};
-  const LaneOffsets<D> lanes(c.page_shift);
+  const LaneOffsets<D, QK> lanes(c.page_shift);
   const int64_t page_bytes = static_cast<int64_t>(c.heads) * (D / 2) << c.page_shift;
 
   // sequences that hold nothing: their rows see nothing
@@ -383,7 +532,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
     if (s.length > 0) continue;
     for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq * (D / 8); i += kWaves * 64) {
       const float zero[8] = {};
-      store_n<PP == 2, 8>(o, static_cast<size_t>(s.first) * Hq * D + i * 8, zero);
+      store_n<OUT_BF16, 8>(o, static_cast<size_t>(s.first) * Hq * D + i * 8, zero);
     }
     if (lse)
       for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.tokens) * Hq; i += kWaves * 64)
@@ -408,7 +557,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
     const int b1 = end - cur < blocks - b0 ? b0 + static_cast<int>(end - cur) : blocks;
     const int head = static_cast<int>(unit / tiles), tile = static_cast<int>(unit - static_cast<int64_t>(head) * tiles);
     // this lane's rows
-    SplitN<QP> qf[MT][D / 32];
+    Queries<D, QK> qf[MT];
     uint32_t sees[MT];
     auto seen = [&](int row) {   // positions that a row sees
       const int x = s.length - s.tokens + row / group + 1;
@@ -419,15 +568,8 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
       const int row = tile * kRows + m * 16 + j;
       const int r = row < rows ? row : rows - 1;
       const int t = r / group;
-      const size_t from = (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D + g * (D / 4);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        if constexpr (QP == 1) {
-          qf[m][i].v[0] = load_bf16x8(static_cast<const uint16_t*>(q) + from + 8 * i);
-        } else {
-          qf[m][i] = load_split<QP>(static_cast<const float*>(q) + from + 8 * i);
-        }
-      }
+      load_queries<D, QK, IN_BF16>(q, (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D, flip,
+                                      qf[m]);
       sees[m] = seen(r);
     }
     // positions that every row sees, and that any does
@@ -451,17 +593,17 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
         return step_at<D>(c, n, page_bytes, head_bytes, static_cast<uint32_t>(b) * kBlockPos + first_pos, b < stop);
       };
       StepAt here = place(b0);
-      RawKeys<D> keys;
-      load_keys<D>(c, here, lanes, keys);
+      RawKeys<D, QK> keys;
+      load_keys<D, QK>(c, here, lanes, keys);
       StepAt next = place(b0 + 1);
       for (int b = b0; b < stop; ++b) {
         const uint32_t at = static_cast<uint32_t>(b) * kBlockPos + first_pos;
         RawValues<D> values;
-        load_values<D>(c, here, lanes, values);
+        load_values<D, QK>(c, here, lanes, values);
         f32x4 s4[MT][2];
-        scores<D, MT, QP>(keys, qf, s4);
+        scores<D, MT, QK>(keys, qf, s4);
         __builtin_amdgcn_sched_barrier(0);
-        load_keys<D>(c, next, lanes, keys);
+        load_keys<D, QK>(c, next, lanes, keys);
         const StepAt after = place(b + 2);
         if (here.held)
           weigh<D, MT, PP>(values, s4, scale, at + kStep <= least, at, sees, c.v_scale + here.scales, c.page_shift, acc);
@@ -517,7 +659,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = l == 0.0f ? 0.0f : x[e] * inv;
-          store_n<PP == 2, 8>(o, to * D + ch, x);
+          store_n<OUT_BF16, 8>(o, to * D + ch, x);
           if (lse && ch == 0) lse[to] = row_lse(up2, l);
         } else {
           store_n<false, 8>(piece, static_cast<size_t>(m * 16 + rr) * D + ch, x);
@@ -602,32 +744,41 @@ size_t paged_attention_ws(int D, int heads, int group, int64_t n_tokens, int max
 
 hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
                                   float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st) {
-  const int mt = row_tiles(D, !(in_bf16 && out_bf16), rows_of(c, group, max_q));
+  const int mt = row_tiles(D, !out_bf16, rows_of(c, group, max_q));
   const int wgs = workgroups(D, mt);
   Split* splits = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(splits + wgs);
   const size_t shared = (static_cast<size_t>(c.N) + 1) * 8;
-  auto go = [&](auto d, auto t, auto qp, auto pp) {
+  auto go = [&](auto d, auto t, auto qk, auto pp, auto ib, auto ob) {
     constexpr int kD = decltype(d)::value, kT = decltype(t)::value, kPP = decltype(pp)::value;
-    paged_attention_kernel<kD, kT, decltype(qp)::value, kPP>
+    constexpr bool kIn = decltype(ib)::value, kOut = decltype(ob)::value;
+    paged_attention_kernel<kD, kT, decltype(qk)::value, kPP, kIn, kOut>
         <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    join_pieces_kernel<kD, 16 * kT, kPP == 2><<<dim3(wgs, 4 * kT), 256, 0, st>>>(c, group, o, lse, splits, pieces);
+    join_pieces_kernel<kD, 16 * kT, kOut><<<dim3(wgs, 4 * kT), 256, 0, st>>>(c, group, o, lse, splits, pieces);
     return hipGetLastError();
   };
   using std::integral_constant;
+  using std::false_type;
+  using std::true_type;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  const integral_constant<int, 3> three;
   auto by_type = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    const integral_constant<int, 1> one;
-    const integral_constant<int, 2> two;
-    const integral_constant<int, 3> three;
-    if (!in_bf16) return out_bf16 ? go(d, one, three, two) : go(d, one, three, three);
-    if (!out_bf16) return go(d, one, one, three);
-    if (mt == 1) return go(d, one, one, two);
-    if (mt == 2) return go(d, two, one, two);
-    if constexpr (kD < 256) return go(d, integral_constant<int, 4>{}, one, two);
-    return hipErrorInvalidValue;
+    const integral_constant<Qk, Qk::kF6> f6;
+    if (!out_bf16) {
+      if (in_bf16) return go(d, one, integral_constant<Qk, Qk::kBf16>{}, three, true_type{}, false_type{});
+      return go(d, one, integral_constant<Qk, Qk::kFp32>{}, three, false_type{}, false_type{});
+    }
+    auto by_rows = [&](auto ib) {
+      if (mt == 1) return go(d, one, f6, two, ib, true_type{});
+      if (mt == 2) return go(d, two, f6, one, ib, true_type{});
+      if constexpr (kD < 256) return go(d, integral_constant<int, 4>{}, f6, one, ib, true_type{});
+      return hipErrorInvalidValue;
+    };
+    return in_bf16 ? by_rows(true_type{}) : by_rows(false_type{});
   };
   switch (D) {
     case 64: return by_type(integral_constant<int, 64>{});

@@ -95,8 +95,6 @@ kda::CacheArgs cache_args(const kda_kv_cache_t* c, int32_t N, int64_t n_tokens) 
           c->lengths, c->cu_seqlens, N, n_tokens};
 }
 
-bool exact_attention(const kda_config_t* cfg) { return cfg->io_dtype == KDA_FP32 || cfg->out_dtype == KDA_FP32; }
-
 kda_status_t check_attention(const kda_config_t* cfg, int32_t kv_heads, int32_t N, int64_t n_tokens, int32_t max_q) {
   const kda_status_t s = check_shape(cfg, n_tokens, kv_heads, 1);
   if (s != KDA_OK) return s;
@@ -213,7 +211,7 @@ size_t kda_paged_attention_workspace_bytes(const kda_config_t* cfg, int32_t num_
                                            int32_t max_q) {
   if (check_attention(cfg, num_kv_heads, N, n_tokens, max_q) != KDA_OK) return 0;
   return align_up(kda::paged_attention_ws(cfg->head_k_dim, num_kv_heads, cfg->num_heads / num_kv_heads, n_tokens, max_q,
-                                          exact_attention(cfg)));
+                                          cfg->out_dtype == KDA_FP32));
 }
 
 kda_status_t kda_paged_attention(const kda_config_t* cfg, const kda_kv_cache_t* cache, int32_t N, int64_t n_tokens,

@@ -106,11 +106,13 @@ def stored(pages, table, length):
 
 def attention(q, k, v, length, scale):
     """q [t, Hq, d], k, v [heads, length, d] in 64 bits, the last t of `length` positions being q's own.
-    Returns (o, lse, sum w|v|, the largest sum |scale q k| of each row)."""
+    Returns (o, lse, sum w|v|, (the largest sum |scale q k| of each row, the largest sum over blocks of 32 channels of
+    max|q| sum|k| times scale))."""
     t, Hq, d = q.shape
     heads = k.shape[0]
     o, m = torch.zeros(t, Hq, d, dtype=torch.float64), torch.zeros(t, Hq, d, dtype=torch.float64)
-    lse, top = torch.full((t, Hq), -torch.inf, dtype=torch.float64), torch.zeros(t, Hq, dtype=torch.float64)
+    lse, top = torch.full((t, Hq), -torch.inf, dtype=torch.float64), torch.zeros(2, t, Hq, dtype=torch.float64)
+    block = k.abs().unflatten(-1, (-1, BLOCK)).sum(-1)
     for j in range(t):
         sees = min(length, length - t + j + 1)
         if sees <= 0:
@@ -121,14 +123,24 @@ def attention(q, k, v, length, scale):
             s = kk @ q[j, h] * scale
             w = torch.softmax(s, 0)
             o[j, h], m[j, h], lse[j, h] = w @ vv, w @ vv.abs(), torch.logsumexp(s, 0)
-            top[j, h] = (kk.abs() @ q[j, h].abs()).max() * abs(scale)
+            top[0, j, h] = (kk.abs() @ q[j, h].abs()).max() * abs(scale)
+            top[1, j, h] = (block[g, :sees] @ q[j, h].abs().unflatten(-1, (-1, BLOCK)).amax(-1)).max() * abs(scale)
     return o, lse, m, top
 
 
-def attention_rel(d, length, top, q_dtype, out_dtype):
-    """Error of o relative to sum w|v|, and of lse: a score has d products summed and is scaled (d + 2 roundings of its
-    terms' sum), and moves by as much again when the maximum is taken off; the exponential 2.  Each moves weight and sum.
-    The weights' pieces: 2^-16 (two) or 2^-24; a step sums 32 products, a row at most length / 32 steps and their joins."""
-    score = (d + 2 + 3) * U * top + 4 * U
-    pieces = 2.0 ** -16 if out_dtype == torch.bfloat16 else U
-    return 2 * score + pieces + (32 + length / 32 + 600) * U, score + (length / 8 + 600) * U
+def attention_rel(d, length, top, q_dtype, out_dtype, rows):
+    """Error of o relative to sum w|v| (as [.., 1]), and of lse, for a key head's `rows` rows of one sequence (0: not known).
+
+    A score has d products summed and is scaled (d + 2 roundings of its terms' sum), and moves by as much again when the
+    maximum is taken off; the exponential 2.  Each moves weight and sum.  For bf16 outputs a query's three 6-bit pieces
+    leave half a step of the last, 2^-12 of the first's unit, which is less than its block's largest / 3.75; the pieces'
+    products are exact.  The weights' pieces: two bf16 leave 2^-16, one 2^-8 (in the sum that divides too; the most for
+    rows above 16), three 2^-24.  A step sums 32 products, a row at most length / 32 steps and their joins."""
+    score = (d + 2 + 3) * U * top[0] + 4 * U
+    if out_dtype == torch.bfloat16:
+        score = score + 2.0 ** -12 / 3.75 * top[1]
+        pieces = 2.0 ** -16 if 0 < rows <= 16 else 2 * 2.0 ** -8
+    else:
+        pieces = U
+    lse = 0.0 if pieces < 2.0 ** -15 else 2.0 ** -8
+    return (2 * score + pieces + (32 + length / 32 + 600) * U)[..., None], score + lse + (length / 8 + 600) * U

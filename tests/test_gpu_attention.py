@@ -11,25 +11,31 @@ from tests.test_gpu_rope import EPS, expected, kda, make_cfg, make_rope  # noqa:
 pytestmark = pytest.mark.gpu
 
 
-def check_attention(o, lse, b, q, scale, rows=None, note=""):
-    """Every sequence (or the given rows of each) against 64 bits."""
-    cu = b.cu.tolist()
+def check_attention(o, lse, b, q, scale, max_q=0, note=""):
+    """Every sequence against 64 bits; max_q as the call had it (0: not known)."""
+    cu, total = b.cu.tolist(), [0.0, 0.0, 0]
+    rows = max_q * q.shape[1] // b.heads
     for i, (t, n) in enumerate(b.seqs):
         if t == 0:
             continue
         k, v = b.held(i)
         x = q[cu[i]:cu[i + 1]].double().cpu()
         e, el, m, top = ref.attention(x, k, v, n, scale)
-        rel, rl = ref.attention_rel(q.shape[2], n, top[..., None], q.dtype, o.dtype)
+        rel, rl = ref.attention_rel(q.shape[2], n, top, q.dtype, o.dtype, rows)
         got = o[cu[i]:cu[i + 1]].cpu()
         check(got, e, m, rel, f"{note} sequence {i}")
+        total = [total[0] + (got.double() - e).square().sum(), total[1] + e.square().sum(), total[2] + e.numel()]
         if lse is not None:
             g = lse[cu[i]:cu[i + 1]].double().cpu()
             none = el.isinf()
             assert torch.equal(g.isinf(), none) and (g[none] < 0).all()
             off = (g - el)[~none].abs()
-            lim = (rl + 4 * 2.0 ** -24 * el.abs().nan_to_num(posinf=0)[..., None])[..., 0][~none]
+            lim = (rl + 4 * 2.0 ** -24 * el.abs().nan_to_num(posinf=0))[~none]
             assert (off <= lim).all(), f"{note} lse of sequence {i}: {float((off / lim).max())} of the bound"
+    if o.dtype == torch.bfloat16 and total[2] >= 1000:
+        # in the 2-norm: the output's rounding, and the weights' where they are one bf16 value, which moves an output by
+        # as much where the values are independent of each other, as here; and what else there is by a tenth of that
+        assert (total[0] / total[1]) ** 0.5 <= (2.0 ** 0.5 + 0.1) * 2.0 ** -8 / 3 ** 0.5, note
 
 
 SEQS = {
@@ -54,10 +60,10 @@ def test_attention(kda, seqs, d, heads, group, page, io, out):  # noqa: F811
     o, ok = guarded(q.shape, out)
     lse, ok2 = guarded(q.shape[:2], F32)
     scale = d ** -0.5
-    kda.kda_paged_attention(make_cfg(kda, heads * group, d, io, out), b.cache, q, *b.where, max_q=max(t for t, _ in b.seqs), o=o,
-                            lse=lse)
+    max_q = max(t for t, _ in b.seqs)
+    kda.kda_paged_attention(make_cfg(kda, heads * group, d, io, out), b.cache, q, *b.where, max_q=max_q, o=o, lse=lse)
     assert ok() and ok2()
-    check_attention(o, lse, b, q, scale)
+    check_attention(o, lse, b, q, scale, max_q)
     # the largest count not known: another kernel may take it
     o2 = kda.kda_paged_attention(make_cfg(kda, heads * group, d, io, out), b.cache, q, *b.where, scale)
     check_attention(o2, None, b, q, scale, note="max_q 0")
@@ -146,14 +152,14 @@ def test_pages_that_are_not_held(kda):  # noqa: F811
     o = kda.kda_paged_attention(cfg, b.cache, q, *b.where, lse=lse)
     keep = torch.tensor([p for p in range(200) if p // 64 != 1])
     e, _, m, top = ref.attention(q[:1].double().cpu(), k[:, keep], v[:, keep], len(keep), d ** -0.5)
-    check(o[:1].cpu(), e, m, ref.attention_rel(d, 200, top[..., None], F32, F32)[0])
+    check(o[:1].cpu(), e, m, ref.attention_rel(d, 200, top, F32, F32, 0)[0])
     assert (o[3] == 0).all() and (lse[3] == -torch.inf).all()
     # the table holds 4 pages: positions 128 .. 255 of sequence 1 are pages of -1; both its tokens see all of them
     k, v = b.held(1)
     b.seqs[1] = (2, 128)
     for j in range(2):
         e, _, m, top = ref.attention(q[1 + j:2 + j].double().cpu(), k, v, 128, d ** -0.5)
-        check(o[1 + j:2 + j].cpu(), e, m, ref.attention_rel(d, 128, top[..., None], F32, F32)[0])
+        check(o[1 + j:2 + j].cpu(), e, m, ref.attention_rel(d, 128, top, F32, F32, 0)[0])
 
 
 def test_padded_batch_streams_and_graph(kda):  # noqa: F811
@@ -166,13 +172,13 @@ def test_padded_batch_streams_and_graph(kda):  # noqa: F811
     r = Rand(5)
     q = r(9, heads * group, d, dtype=BF)
     o = torch.full_like(q, 7.0)
-    kda.kda_paged_attention(cfg, b.cache, q, *b.where, o=o)
+    kda.kda_paged_attention(cfg, b.cache, q, *b.where, max_q=1, o=o)   # (one kernel for all of these: the same bits)
     assert (o[4:] == 7).all()
-    check_attention(o, None, b, q, d ** -0.5)
+    check_attention(o, None, b, q, d ** -0.5, 1)
     assert torch.equal(kda.kda_paged_attention(cfg, b.cache, q[:4], None, b.table, b.lengths), o[:4])
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    s = kda.kda_paged_attention(cfg, b.cache, q[:4], *b.where, stream=side)
+    s = kda.kda_paged_attention(cfg, b.cache, q[:4], *b.where, max_q=1, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(s, o[:4])
     ws = torch.empty(kda.kda_paged_attention_workspace_bytes(cfg, heads, 4, 4, 1), dtype=torch.uint8, device="cuda")
