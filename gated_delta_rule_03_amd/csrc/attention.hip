@@ -36,98 +36,18 @@
 // order.
 #include <algorithm>
 
-#include "kda_device.h"
-#include "kda_internal.h"
-#include "kv_cache.h"
-#include "mfma.h"
-#include "vec_io.h"
+#include "attention.h"
 
 namespace kda {
 
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kStep = 32;                   // positions of a wave's step
 constexpr int kBlockPos = kWaves * kStep;   // positions of a block
-constexpr float kRaise = 8.0f;              // log2 by which a score may pass the running maximum
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
-
 // A piece's place in the workspace: its rows' sums, then maxima and weights' sums.
 template <int D, int ROWS>
 __device__ __forceinline__ float* piece_at(float* pieces, int64_t slot) {
   return pieces + slot * (static_cast<int64_t>(ROWS) * (D + 2));
-}
-
-// What the joining kernel has to know of a workgroup's last unit, if it began
-// there and goes on in the next workgroups.
-struct Split {
-  int seq, head, tile;
-  int pieces;   // 0: nothing to join
-};
-
-struct Sequence {
-  int first;          // its first row of q
-  int tokens;         // new tokens
-  int length;         // positions held
-};
-
-// A value that is the same in every lane, as the compiler cannot see.
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-  const uint32_t lo = uniform(static_cast<int>(x)), hi = uniform(static_cast<int>(x >> 32));
-  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
-}
-
-__device__ __forceinline__ Sequence sequence(const CacheArgs& c, int n) {
-  Sequence s;
-  s.first = c.cu ? c.cu[n] : n;
-  const int64_t end = c.cu ? c.cu[n + 1] : n + 1;
-  const int64_t last = end < c.n_tokens ? end : c.n_tokens;
-  s.tokens = s.first < 0 || last <= s.first ? 0 : static_cast<int>(last - s.first);
-  const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
-  const int len = c.lengths[n];
-  s.length = len < 0 ? 0 : len < most ? len : static_cast<int>(most);
-  return s;
-}
-
-// The line of all units' blocks: before[n] blocks in front of sequence n's.
-__device__ __forceinline__ void lay_out(const CacheArgs& c, int group, int rows, int64_t* before, int64_t* sums) {
-  // each thread a run of neighbouring sequences, then the threads' sums
-  constexpr int kThreads = kWaves * 64;
-  const int per = (c.N + kThreads - 1) / kThreads;
-  const int n0 = threadIdx.x * per, n1 = n0 + per < c.N ? n0 + per : c.N;
-  int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) {
-    const Sequence s = sequence(c, n);
-    const int64_t tiles = (static_cast<int64_t>(s.tokens) * group + rows - 1) / rows;
-    before[n + 1] = mine += tiles * c.heads * ((static_cast<int64_t>(s.length) + kBlockPos - 1) / kBlockPos);
-  }
-  sums[threadIdx.x] = mine;
-  __syncthreads();
-  if (threadIdx.x < 64) {   // four threads' sums a lane
-    int64_t four[4], t = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      four[i] = t;
-      t += sums[threadIdx.x * 4 + i];
-    }
-    int64_t run = t;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int64_t up = __shfl_up(run, m);
-      if (threadIdx.x >= m) run += up;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sums[threadIdx.x * 4 + i] = run - t + four[i];
-  }
-  __syncthreads();
-  const int64_t front = sums[threadIdx.x];
-  for (int n = n0; n < n1; ++n) before[n + 1] += front;
-  if (threadIdx.x == 0) before[0] = 0;
-  __syncthreads();
 }
 
 // How queries and keys meet: 6-bit pieces of queries and the keys' own 4 bits, or
@@ -166,27 +86,6 @@ struct LaneOffsets {
     vs = ((j * D / 512) << page_shift) + 8 * g;
   }
 };
-
-// A step's first bytes in the cache; the same in every lane.
-struct StepAt {
-  int64_t values, scales;
-  bool held;
-};
-
-// Where a head's steps are: page_bytes apart from page to page.
-template <int D>
-__device__ __forceinline__ StepAt step_at(const CacheArgs& c, int seq, int64_t page_bytes, int64_t head_bytes,
-                                          uint32_t pos, bool inside) {
-  // through the scalar cache: a vector load here would wait for all those in flight
-  typedef const __attribute__((address_space(4))) int32_t* Scalar;
-  const int i = static_cast<int>(pos >> c.page_shift);
-  int page = -1;
-  if (inside && i < c.max_pages) page = ((Scalar)(c.table + static_cast<int64_t>(seq) * c.max_pages))[i];
-  const bool held = static_cast<uint32_t>(page) < static_cast<uint32_t>(c.num_pages);
-  const int64_t first = (held ? page : 0) * page_bytes + head_bytes;
-  const int off = static_cast<int>(pos & ((1u << c.page_shift) - 1));
-  return {first + static_cast<int64_t>(off) * (D / 2), (first >> 4) + off, held};
-}
 
 template <int D, Qk QK>
 __device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, const LaneOffsets<D, QK>& lane,
@@ -235,20 +134,6 @@ __device__ __forceinline__ void load_values(const CacheArgs& c, const StepAt& at
   }
 }
 
-__device__ __forceinline__ float scale_of(uint32_t bytes, int i) {
-  return __uint_as_float(((bytes >> (8 * i)) & 0xffu) << 23);
-}
-
-template <int B>
-__device__ __forceinline__ uint32_t widen(uint32_t w, float s) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
-}
-
-// 8 codes as the bf16 values they stand for, in their order.
-__device__ __forceinline__ bf16x8 widen8(uint32_t w, float s) {
-  return __builtin_bit_cast(bf16x8, make_uint4(widen<0>(w, s), widen<1>(w, s), widen<2>(w, s), widen<3>(w, s)));
-}
-
 // Rows' accumulators of one wave: MT tiles of 16 rows, this lane's row l % 16 of each.
 template <int D, int MT>
 struct Rows {
@@ -262,54 +147,12 @@ struct Queries {
   SplitN<static_cast<int>(QK)> v[D / 32];
 };
 
-typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x32 __attribute__((ext_vector_type(32)));
-
 template <int D>
 struct Queries<D, Qk::kF6> {
   static constexpr int kBlocks = D > 128 ? 2 : 1;
   u32x6 v[kBlocks][3];         // 32 channels each
   uint32_t scale[kBlocks];     // their e8m0 scales, a byte a piece
 };
-
-// x as three 6-bit pieces.  With max|x| = 1.m 2^p the first's unit is 2^(p - 2)
-// where 1.m <= 1.875 (e2m3 reaches 7.5) and 2^(p - 1) above; what it leaves is at
-// most 4 units of 2^-4 of its own, and so on.
-__device__ __forceinline__ void split_e2m3(float (&x)[32], u32x6 (&v)[3], uint32_t& scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    const uint32_t b = __float_as_uint(x[e]) & 0x7fffffffu;
-    top = b > top ? b : top;
-  }
-  const int p = static_cast<int>(top >> 23);
-  int byte = p - 2 + ((top & 0x7fffffu) > 0x700000u);
-  byte = byte < 9 ? 9 : byte;
-  if (p == 255) {   // NaN, infinity: every product with the block is NaN
-    scale = 0xffffffu;
-    v[0] = v[1] = v[2] = u32x6{0, 0, 0, 0, 0, 0};
-    return;
-  }
-  scale = static_cast<uint32_t>(byte) | static_cast<uint32_t>(byte - 4) << 8 | static_cast<uint32_t>(byte - 8) << 16;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const float s = __uint_as_float(static_cast<uint32_t>(byte - 4 * i) << 23);
-    f32x16 even, odd;   // the conversion takes its elements from two vectors in turn
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      even[e] = x[2 * e];
-      odd[e] = x[2 * e + 1];
-    }
-    v[i] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, s);
-    if (i < 2) {
-      const f32x32 got = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(v[i], s);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x[e] -= got[e];
-    }
-  }
-}
 
 // row: the first element of the row's head; flip: 0x80008000 turns every sign.
 template <int D, Qk QK, bool BF16>
@@ -406,8 +249,9 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = s[m][e & 1][e >> 1];
     if (!whole) {
+      const int rel = static_cast<int>(sees[m] - at) - 8 * g;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = at + 8 * g + e < sees[m] ? x[e] : neg_inf();
+      for (int e = 0; e < 8; ++e) x[e] = e < rel ? x[e] : neg_inf();
     }
     float top = x[0];
 #pragma unroll
@@ -496,11 +340,6 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
   }
 }
 
-// A row's sums to its place: the output, or a piece of the workspace.
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
-}
-
 }  // namespace
 
 template <int D, int MT, Qk QK, int PP, bool IN_BF16, bool OUT_BF16>
@@ -517,7 +356,11 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   // a negative scale turns the queries' sign; of 0 every score is 0, as of the least (where -infinity stays what it is)
   const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
   scale = fminf(fmaxf(fabsf(scale), 1.17549435e-38f), 3.4028235e38f);
-  lay_out(c, group, kRows, before, reinterpret_cast<int64_t*>(meet));
+  lay_out<kWaves * 64>(c.N, before, reinterpret_cast<int64_t*>(meet), [&](int n) {
+    const Sequence s = sequence(c, n);
+    const int64_t tiles = (static_cast<int64_t>(s.tokens) * group + kRows - 1) / kRows;
+    return tiles * c.heads * ((static_cast<int64_t>(s.length) + kBlockPos - 1) / kBlockPos);
+  });
   const int64_t total = before[c.N];
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   const int64_t start = share * blockIdx.x;
@@ -678,9 +521,10 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   if (threadIdx.x == 0) splits[blockIdx.x] = split;
 }
 
-// Joins the pieces of the unit that began in workgroup blockIdx.x of the first
-// kernel: a wave to a row.
-template <int D, int ROWS, bool OUT_BF16>
+// Joins the pieces of a unit, a wave to a row: PARTS: of unit blockIdx.x of the
+// chunk kernel, one after the other; otherwise of the unit that began in
+// workgroup blockIdx.x of the kernel above.
+template <int D, int ROWS, bool OUT_BF16, bool PARTS>
 __global__ __launch_bounds__(256) void join_pieces_kernel(CacheArgs c, int group, void* __restrict__ o,
                                                           float* __restrict__ lse, const Split* __restrict__ splits,
                                                           float* __restrict__ pieces) {
@@ -690,8 +534,10 @@ __global__ __launch_bounds__(256) void join_pieces_kernel(CacheArgs c, int group
   const int rr = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int row = split.tile * ROWS + rr;
   if (row >= s.tokens * group) return;
-  // the first piece is its workgroup's second, the others their workgroups' first
-  auto at = [&](int i) { return piece_at<D, ROWS>(pieces, 2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0)); };
+  auto at = [&](int i) {   // (in a workgroup's two, a unit that begins there is the second)
+    return piece_at<D, ROWS>(pieces, PARTS ? static_cast<int64_t>(blockIdx.x) * split.pieces + i
+                                           : 2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0));
+  };
   float up = neg_inf();
   for (int i = lane; i < split.pieces; i += 64) up = fmaxf(up, at(i)[ROWS * D + 2 * rr]);
 #pragma unroll
@@ -726,6 +572,9 @@ int row_tiles(int D, bool exact, int64_t rows) {
   return 4;
 }
 
+// Whether the chunk kernel takes a call.
+bool in_chunks(bool exact, int64_t rows) { return !exact && rows > 64; }
+
 int workgroups(int D, int mt) { return D / 16 * mt > 16 ? 256 : 512; }
 
 int64_t rows_of(const CacheArgs& c, int group, int max_q) {
@@ -734,9 +583,25 @@ int64_t rows_of(const CacheArgs& c, int group, int max_q) {
 
 }  // namespace
 
-size_t paged_attention_ws(int D, int heads, int group, int64_t n_tokens, int max_q, bool exact) {
+hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, float* lse, const Split* joins,
+                             float* pieces, int units, hipStream_t st) {
+  constexpr int kRows = kChunkRows;
+  const dim3 grid(units, kRows / 4);
+  switch (D) {
+    case 64: join_pieces_kernel<64, kRows, true, true><<<grid, 256, 0, st>>>(c, group, o, lse, joins, pieces); break;
+    case 128: join_pieces_kernel<128, kRows, true, true><<<grid, 256, 0, st>>>(c, group, o, lse, joins, pieces); break;
+    case 256: join_pieces_kernel<256, kRows, true, true><<<grid, 256, 0, st>>>(c, group, o, lse, joins, pieces); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, int max_q, bool exact) {
   CacheArgs c{};
   c.n_tokens = n_tokens;
+  c.N = N;
+  c.heads = heads;
+  if (in_chunks(exact, rows_of(c, group, max_q))) return attention_chunk_ws(D, c, group);
   const int mt = row_tiles(D, exact, rows_of(c, group, max_q));
   const size_t wgs = workgroups(D, mt);
   return wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4;
@@ -744,6 +609,8 @@ size_t paged_attention_ws(int D, int heads, int group, int64_t n_tokens, int max
 
 hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
                                   float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st) {
+  if (in_chunks(!out_bf16, rows_of(c, group, max_q)))
+    return launch_attention_chunk(D, c, q, group, scale * kLog2e, o, lse, ws, in_bf16, st);
   const int mt = row_tiles(D, !out_bf16, rows_of(c, group, max_q));
   const int wgs = workgroups(D, mt);
   Split* splits = static_cast<Split*>(ws);
@@ -756,7 +623,7 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
         <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    join_pieces_kernel<kD, 16 * kT, kOut><<<dim3(wgs, 4 * kT), 256, 0, st>>>(c, group, o, lse, splits, pieces);
+    join_pieces_kernel<kD, 16 * kT, kOut, false><<<dim3(wgs, 4 * kT), 256, 0, st>>>(c, group, o, lse, splits, pieces);
     return hipGetLastError();
   };
   using std::integral_constant;
