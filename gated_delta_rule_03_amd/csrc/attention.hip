@@ -324,7 +324,8 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
       }
   }
   if (!whole && __any(bad)) {   // a row that sees such a value has NaN in its 32 channels
-#pragma unroll
+    uint32_t with = 0;   // bit 4 m + i: the lane's channels i of row tile m
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) {
       const uint8_t* of = v_scales + (static_cast<uint32_t>((4 * g + i) * D / 512) << page_shift);
 #pragma unroll 1
@@ -332,11 +333,16 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
         if (of[e] < 253) continue;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          if (at + e < sees[m])
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) acc.o[m][x][i] = __uint_as_float(0x7fc00000u);
+          if (at + e < sees[m]) with |= 1u << (4 * m + i);
       }
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          acc.o[m][x][i] = with >> (4 * m + i) & 1 ? __uint_as_float(0x7fc00000u) : acc.o[m][x][i];
   }
 }
 
@@ -454,7 +460,10 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
         next = after;
       }
     }
-    // the waves' sums joined, 16 rows at a time
+    // The waves' sums joined, 16 rows at a time.  (A row's single values are
+    // stored in front of its channels: where such a branch ended together with
+    // the one around it, the compiler brought registers back from where it had
+    // put them aside for the branch's lanes alone, and rows came out wrong.)
     const bool whole = b0 == 0 && b1 == blocks;
     float* piece = piece_at<D, kRows>(pieces, 2 * static_cast<int64_t>(blockIdx.x) + (b0 == 0));
 #pragma unroll
@@ -490,7 +499,8 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
 #pragma unroll
         for (int y = 0; y < kWaves; ++y) {
           const float my = tops[y][m * 16 + rr][0];
-          l += my == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(my - up2) * tops[y][m * 16 + rr][1];
+          // (nothing seen: 0; NaN scores alone leave no maximum either, and a sum of NaN)
+          l = fmaf(my == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(my - up2), tops[y][m * 16 + rr][1], l);
           float part[8];
           load_n<false, 8>(&meet[y][rr][0], ch, part);
 #pragma unroll
@@ -502,14 +512,14 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = l == 0.0f ? 0.0f : x[e] * inv;
-          store_n<OUT_BF16, 8>(o, to * D + ch, x);
           if (lse && ch == 0) lse[to] = row_lse(up2, l);
+          store_n<OUT_BF16, 8>(o, to * D + ch, x);
         } else {
-          store_n<false, 8>(piece, static_cast<size_t>(m * 16 + rr) * D + ch, x);
           if (ch == 0) {
             piece[kRows * D + 2 * (m * 16 + rr)] = up2;
             piece[kRows * D + 2 * (m * 16 + rr) + 1] = l;
           }
+          store_n<false, 8>(piece, static_cast<size_t>(m * 16 + rr) * D + ch, x);
         }
       }
       __syncthreads();
@@ -521,45 +531,81 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   if (threadIdx.x == 0) splits[blockIdx.x] = split;
 }
 
-// Joins the pieces of a unit, a wave to a row: PARTS: of unit blockIdx.x of the
-// chunk kernel, one after the other; otherwise of the unit that began in
-// workgroup blockIdx.x of the kernel above.
+// Joins the pieces of a unit: PARTS: of unit blockIdx.x of the chunk kernel, of
+// `stride` places; otherwise of the unit that began in workgroup blockIdx.x of
+// the kernel above.  Four waves share a row's pieces, each with eight of them in
+// flight; a workgroup takes four rows.
 template <int D, int ROWS, bool OUT_BF16, bool PARTS>
-__global__ __launch_bounds__(256) void join_pieces_kernel(CacheArgs c, int group, void* __restrict__ o,
-                                                          float* __restrict__ lse, const Split* __restrict__ splits,
-                                                          float* __restrict__ pieces) {
+__global__ __launch_bounds__(1024) void join_pieces_kernel(CacheArgs c, int group, void* __restrict__ o,
+                                                           float* __restrict__ lse, const Split* __restrict__ splits,
+                                                           const float* __restrict__ pieces, int stride) {
+  constexpr int E = D / 64, kTogether = 8;   // channels of a lane; pieces whose loads are in flight
+  __shared__ float meet[16][64][E], tops[16][2];
   const Split split = splits[blockIdx.x];
   if (split.pieces == 0) return;
+  const int wave = uniform(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+  const int rr = blockIdx.y * 4 + (wave >> 2), row = split.tile * ROWS + rr;
   const Sequence s = sequence(c, split.seq);
-  const int rr = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int row = split.tile * ROWS + rr;
-  if (row >= s.tokens * group) return;
+  const bool mine = row < s.tokens * group;
   auto at = [&](int i) {   // (in a workgroup's two, a unit that begins there is the second)
-    return piece_at<D, ROWS>(pieces, PARTS ? static_cast<int64_t>(blockIdx.x) * split.pieces + i
-                                           : 2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0));
+    return pieces + (PARTS ? static_cast<int64_t>(blockIdx.x) * stride + i
+                           : 2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0)) * (static_cast<int64_t>(ROWS) * (D + 2));
   };
-  float up = neg_inf();
-  for (int i = lane; i < split.pieces; i += 64) up = fmaxf(up, at(i)[ROWS * D + 2 * rr]);
+  float up = neg_inf(), l = 0.f, x[E] = {};
+  for (int i = wave & 3; mine && i < split.pieces; i += 4 * kTogether) {
+    float m[kTogether], w[kTogether], y[kTogether][E];
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) up = fmaxf(up, __shfl_xor(up, m));
-  constexpr int E = D / 64;
-  float x[E] = {}, l = 0.f;
-  for (int i = 0; i < split.pieces; ++i) {
-    const float* p = at(i);
-    const float m = p[ROWS * D + 2 * rr];
-    const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - up);
-    l = fmaf(f, p[ROWS * D + 2 * rr + 1], l);
-    float y[E];
-    load_n<false, E>(p, static_cast<size_t>(rr) * D + lane * E, y);
+    for (int k = 0; k < kTogether; ++k) {
+      const bool there = i + 4 * k < split.pieces;
+      const float* p = at(there ? i + 4 * k : i);
+      m[k] = p[ROWS * D + 2 * rr];
+      w[k] = p[ROWS * D + 2 * rr + 1];
+      load_n<false, E>(p, static_cast<size_t>(rr) * D + lane * E, y[k]);
+      m[k] = there ? m[k] : neg_inf();
+    }
+    float top = up;
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(f, y[e], x[e]);
+    for (int k = 0; k < kTogether; ++k) top = fmaxf(top, m[k]);
+    const float down = up == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(up - top);
+    up = top;
+    l *= down;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] *= down;
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      // (a piece in which the row saw nothing holds zeros; a NaN maximum stays NaN)
+      const float f = m[k] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m[k] - up);
+      l = fmaf(f, w[k], l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = fmaf(f, y[k][e], x[e]);
+    }
+  }
+  store_n<false, E>(&meet[wave][lane][0], 0, x);
+  if (lane == 0) {
+    tops[wave][0] = up;
+    tops[wave][1] = l;
+  }
+  __syncthreads();
+  if ((wave & 3) != 0 || !mine) return;
+  float top = up;
+#pragma unroll
+  for (int k = 1; k < 4; ++k) top = fmaxf(top, tops[wave + k][0]);
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float f = tops[wave + k][0] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(tops[wave + k][0] - top);
+    l = fmaf(f, tops[wave + k][1], l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = fmaf(f, meet[wave + k][lane][e], x[e]);
   }
   const int t = row / group;
   const size_t to = static_cast<size_t>(s.first + t) * (c.heads * group) + split.head * group + (row - t * group);
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = l == 0.0f ? 0.0f : x[e] / l;
   store_n<OUT_BF16, E>(o, to * D + lane * E, x);
-  if (lse && lane == 0) lse[to] = row_lse(up, l);
+  if (lse && lane == 0) lse[to] = row_lse(top, l);
 }
 
 namespace {
@@ -584,13 +630,13 @@ int64_t rows_of(const CacheArgs& c, int group, int max_q) {
 }  // namespace
 
 hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, float* lse, const Split* joins,
-                             float* pieces, int units, hipStream_t st) {
+                             float* pieces, int units, int stride, hipStream_t st) {
   constexpr int kRows = kChunkRows;
   const dim3 grid(units, kRows / 4);
   switch (D) {
-    case 64: join_pieces_kernel<64, kRows, true, true><<<grid, 256, 0, st>>>(c, group, o, lse, joins, pieces); break;
-    case 128: join_pieces_kernel<128, kRows, true, true><<<grid, 256, 0, st>>>(c, group, o, lse, joins, pieces); break;
-    case 256: join_pieces_kernel<256, kRows, true, true><<<grid, 256, 0, st>>>(c, group, o, lse, joins, pieces); break;
+    case 64: join_pieces_kernel<64, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, stride); break;
+    case 128: join_pieces_kernel<128, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, stride); break;
+    case 256: join_pieces_kernel<256, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, stride); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -623,7 +669,7 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
         <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    join_pieces_kernel<kD, 16 * kT, kOut, false><<<dim3(wgs, 4 * kT), 256, 0, st>>>(c, group, o, lse, splits, pieces);
+    join_pieces_kernel<kD, 16 * kT, kOut, false><<<dim3(wgs, 4 * kT), 1024, 0, st>>>(c, group, o, lse, splits, pieces, 0);
     return hipGetLastError();
   };
   using std::integral_constant;

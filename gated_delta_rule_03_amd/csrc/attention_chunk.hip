@@ -21,8 +21,8 @@
 // products.
 //
 // A workgroup takes one (sequence, key head, row tile), the last tiles (which
-// see the most) first, or one of `splits` equal parts of its positions where
-// there are fewer tiles than CUs; the parts meet in the join kernel.
+// see the most) first, or one of up to `splits` equal parts of its positions
+// where the tiles do not fill the CUs; the parts meet in the join kernel.
 #include <algorithm>
 
 #include "attention.h"
@@ -96,6 +96,7 @@ template <int D>
 struct ChunkShape {
   static constexpr int kPos = D == 256 ? 64 : 128;       // positions of a block
   static constexpr int kSteps = kPos / kStep;
+  static constexpr int kLeast = D == 256 ? 8 : 4;        // blocks of a part: its rows' sums are written and read again
   static constexpr int kAhead = 4;                       // blocks' raw bytes in LDS
   static constexpr int kAtOnce = D == 256 ? 1 : 2;       // steps whose scores a wave forms together
   static constexpr int kRowBytes = D / 2;
@@ -204,8 +205,10 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   const int64_t head_bytes = static_cast<int64_t>(head) * (D / 2) << c.page_shift;
   // the part's blocks
   const int blocks = c.num_pages > 0 ? static_cast<int>((static_cast<int64_t>(most_all) + S::kPos - 1) / S::kPos) : 0;
-  const int b0 = uniform(static_cast<int>(static_cast<int64_t>(blocks) * part / splits));
-  const int b1 = uniform(static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / splits));
+  const int shares = blocks < S::kLeast * splits ? (blocks < 2 * S::kLeast ? 1 : blocks / S::kLeast) : splits;
+  if (part >= shares) return;
+  const int b0 = uniform(static_cast<int>(static_cast<int64_t>(blocks) * part / shares));
+  const int b1 = uniform(static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / shares));
 
   auto pages_of = [&](int b) {
     const uint32_t pos = static_cast<uint32_t>(b) * S::kPos;
@@ -327,32 +330,26 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
     for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
   float top_of_row = neg_inf(), sum_of_row = 0.f;
 
+  // Block b's bytes are in place (b - b0) % 4; keys are fetched three blocks before
+  // they are used, values four (they are widened one before).  The first four
+  // turns only fetch and widen: in one loop with the others, since a workgroup's
+  // first run through any code waits for it to come from memory.
   if (b0 < b1) {
-    // block b's bytes are in place (b - b0) % 4; keys are fetched three blocks
-    // before they are used, values four (they are widened one before)
-    Pages now = pages_of(b0), p1 = pages_of(b0 + 1), p2 = pages_of(b0 + 2), p3 = pages_of(b0 + 3), p4 = pages_of(b0 + 4);
-    fetch(now, b0, true, 0);
-    fetch(now, b0, false, 0);
-    fetch(p1, b0 + 1, true, 1);
-    fetch(p1, b0 + 1, false, 1);
-    fetch(p2, b0 + 2, true, 2);
-    fetch(p2, b0 + 2, false, 2);
-    fetch(p3, b0 + 3, false, 3);
-    lds_barrier(0);
-    if (wave < S::kTaskWaves) widen_words(b0, 0, 0, wave);
-    lds_barrier(0);
-    // this wave's loads of two iterations
+    Pages now, p1, p2, p3, p4 = pages_of(b0);
+    now = p1 = p2 = p3 = {-1, -1, -1, -1};
+    // this wave's loads of two turns
     const int in_flight = 2 * (2 * (wave < S::kChunks) + (wave < S::kScaleLoads) +
                                (wave >= W / 2 && wave < W / 2 + S::kScaleLoads));
-    for (int b = b0; b < b1; ++b) {
+#pragma unroll 1
+    for (int b = b0 - 4; b < b1; ++b) {
       const int buf = (b - b0) & 1, raw = (b - b0) & 3;
-      fetch(p3, b + 3, true, (raw + 3) & 3);
+      if (b + 3 >= b0) fetch(p3, b + 3, true, (raw + 3) & 3);
       fetch(p4, b + 4, false, raw);
       const Pages p5 = pages_of(b + 5);
       const int task_wave = (wave + 4 * buf) & (W - 1);   // the other half of the waves each time
-      if (b + 1 < b1 && task_wave < S::kTaskWaves) widen_words(b + 1, (raw + 1) & 3, buf ^ 1, task_wave);
+      if (b + 1 >= b0 && b + 1 < b1 && task_wave < S::kTaskWaves) widen_words(b + 1, (raw + 1) & 3, buf ^ 1, task_wave);
 #pragma unroll 1
-      for (int step = 0; step < S::kSteps; step += S::kAtOnce) {
+      for (int step = b < b0 ? S::kSteps : 0; step < S::kSteps; step += S::kAtOnce) {
         const uint32_t at = static_cast<uint32_t>(b) * S::kPos + step * kStep;
         if (at >= most) break;
         f32x16 sc[S::kAtOnce];
@@ -437,16 +434,19 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
           for (int z = 0; z < S::kAtOnce; ++z) {
             if (now.of(step + z) < 0) continue;
             const uint8_t* of_step = c.v_scale + scales_of(now.of(step + z), b, step + z);
-#pragma unroll
+            uint32_t rows_with = 0;   // elements of the lane whose 32 channels hold one
+#pragma unroll 1
             for (int e = 0; e < 16; ++e) {
               const int ch = (8 * (e >> 2) + 4 * h + (e & 3)) * NC;   // of tile 0
               const uint8_t* of = of_step + (static_cast<uint32_t>(ch >> 5) << c.page_shift);
 #pragma unroll 1
               for (int x = 0; x < kStep; ++x)
-                if (of[x] >= 253 && at + z * kStep + x < sees)
-#pragma unroll
-                  for (int i = 0; i < NC; ++i) acc[i][e] = __uint_as_float(0x7fc00000u);
+                if (of[x] >= 253 && at + z * kStep + x < sees) rows_with |= 1u << e;
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+#pragma unroll
+              for (int i = 0; i < NC; ++i) acc[i][e] = rows_with >> e & 1 ? __uint_as_float(0x7fc00000u) : acc[i][e];
           }
         }
       }
@@ -461,7 +461,9 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   }
 
   sum_of_row += __shfl_xor(sum_of_row, 32);
-  if (splits > 1) {
+  if (splits > 1 && part == 0 && threadIdx.x == 0) joins[id] = {n, head, tile, shares > 1 ? shares : 0};
+  if (row >= rows) return;
+  if (shares > 1) {
     float* piece = pieces + (static_cast<int64_t>(id) * splits + part) * (static_cast<int64_t>(kRows) * (D + 2));
     const int at = wave * 32 + row32;
 #pragma unroll
@@ -476,8 +478,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
       piece[kRows * D + 2 * at] = top_of_row;
       piece[kRows * D + 2 * at + 1] = sum_of_row;
     }
-    if (part == 0 && threadIdx.x == 0) joins[id] = {n, head, tile, splits};
-  } else if (row < rows) {
+  } else {
     const int t = row / group;
     const size_t to = static_cast<size_t>(s.first + t) * Hq + head * group + (row - t * group);
     const float inv = sum_of_row == 0.0f ? 0.0f : 1.0f / sum_of_row;
@@ -500,13 +501,14 @@ int64_t most_units(const CacheArgs& c, int group) {
   return (c.n_tokens * group / kChunkRows + c.N) * c.heads;
 }
 
-// Equal parts of each unit's positions: as many as fill the CUs (a workgroup
-// each) best, where a part costs what it adds to a row's joining.
+// Equal parts of each unit's positions at most: what fills the CUs (a workgroup
+// each) best, where a part costs a hundredth of a unit to join.  The kernel takes
+// fewer where the positions are few.
 int parts_of(int64_t units) {
   int best = 1;
   double least = 1e30;
-  for (int s = 1; s <= 16 && units * s <= 512; ++s) {
-    const double cost = static_cast<double>((units * s + 255) / 256) / s + 0.02 * (s - 1);
+  for (int s = 1; s <= 32 && units * s <= 768; ++s) {
+    const double cost = static_cast<double>((units * s + 255) / 256) / s + 0.01 * (s - 1);
     if (cost < least) {
       least = cost;
       best = s;
@@ -538,7 +540,7 @@ hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int 
         c, q, group, scale, parts, static_cast<int>(units), o, lse, joins, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1) return e;
-    return launch_join_parts(kD, c, group, o, lse, joins, pieces, static_cast<int>(units), st);
+    return launch_join_parts(kD, c, group, o, lse, joins, pieces, static_cast<int>(units), parts, st);
   };
   auto by_type = [&](auto d) { return in_bf16 ? go(d, std::true_type{}) : go(d, std::false_type{}); };
   switch (D) {

@@ -113,6 +113,26 @@ def test_nan_inside_reaches_every_row_that_sees_it(kda):  # noqa: F811
     assert kda.kda_paged_attention(cfg, b.cache, q, *b.where).isnan().all()
 
 
+@pytest.mark.parametrize("io,out", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("tokens", [1, 9, 90])
+def test_queries_with_nan_and_infinity(kda, io, out, tokens):  # noqa: F811
+    """They make their own row NaN, and no other; so does a NaN in the only key that a row sees."""
+    d, group = 128, 2
+    b = Batch(kda, [(tokens, tokens + 50), (1, 1)], 2, d, 32)
+    b.fill()
+    q = Rand(7)(b.n, 2 * group, d, dtype=io)
+    cfg = make_cfg(kda, 2 * group, d, io, out)
+    o = kda.kda_paged_attention(cfg, b.cache, q, *b.where, max_q=tokens)
+    q[0, 1, 5], q[tokens - 1, 2, 100] = float("nan"), float("inf")
+    b.cache.k_scale[int(b.table[1, 0]), 1, 3, 0] = 255
+    lse = torch.zeros(b.n, 2 * group, device="cuda")
+    p = kda.kda_paged_attention(cfg, b.cache, q, *b.where, max_q=tokens, lse=lse)
+    bad = torch.zeros(b.n, 2 * group, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[tokens - 1, 2] = bad[tokens, group:] = True
+    assert p[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(p[~bad], o[~bad]) and lse[~bad].isfinite().all()
+
+
 def test_far_scores(kda):  # noqa: F811
     """Scores of hundreds that rise and fall along the positions: the running maximum moves many times."""
     d = 64
