@@ -179,9 +179,9 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // The chunk kernel (attention_chunk.hip), bf16 outputs: workspace, launch (scale
 // in base 2) and the joining of its units' parts, `stride` pieces apart.
-size_t attention_chunk_ws(int D, const CacheArgs& c, int group);
-hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale, void* o, float* lse,
-                                  void* ws, bool in_bf16, hipStream_t st);
+size_t attention_chunk_ws(int D, const CacheArgs& c, int group, int64_t max_rows);
+hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale,
+                                  int64_t max_rows, void* o, float* lse, void* ws, bool in_bf16, hipStream_t st);
 hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, float* lse, const Split* joins,
                              float* pieces, int units, int stride, hipStream_t st);
 

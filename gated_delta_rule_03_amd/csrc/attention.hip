@@ -44,6 +44,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kBlockPos = kWaves * kStep;   // positions of a block
+constexpr int kMostWorkgroups = 512;        // two a CU
 // A piece's place in the workspace: its rows' sums, then maxima and weights' sums.
 template <int D, int ROWS>
 __device__ __forceinline__ float* piece_at(float* pieces, int64_t slot) {
@@ -531,81 +532,106 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   if (threadIdx.x == 0) splits[blockIdx.x] = split;
 }
 
-// Joins the pieces of a unit: PARTS: of unit blockIdx.x of the chunk kernel, of
-// `stride` places; otherwise of the unit that began in workgroup blockIdx.x of
-// the kernel above.  Four waves share a row's pieces, each with eight of them in
-// flight; a workgroup takes four rows.
+// Joins the pieces of units: PARTS: of the chunk kernel's, of `stride` places each;
+// otherwise of those that began in one of the `units` workgroups of the kernel
+// above, found by a count over them.  Four waves share a row's pieces, each with
+// eight of them in flight; a workgroup takes four rows at a time.
 template <int D, int ROWS, bool OUT_BF16, bool PARTS>
 __global__ __launch_bounds__(1024) void join_pieces_kernel(CacheArgs c, int group, void* __restrict__ o,
                                                            float* __restrict__ lse, const Split* __restrict__ splits,
-                                                           const float* __restrict__ pieces, int stride) {
+                                                           const float* __restrict__ pieces, int units, int stride) {
   constexpr int E = D / 64, kTogether = 8;   // channels of a lane; pieces whose loads are in flight
+  constexpr int kGroups = ROWS / 4;
   __shared__ float meet[16][64][E], tops[16][2];
-  const Split split = splits[blockIdx.x];
-  if (split.pieces == 0) return;
+  __shared__ int counts[16], list[PARTS ? 1 : kMostWorkgroups];
   const int wave = uniform(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-  const int rr = blockIdx.y * 4 + (wave >> 2), row = split.tile * ROWS + rr;
-  const Sequence s = sequence(c, split.seq);
-  const bool mine = row < s.tokens * group;
-  auto at = [&](int i) {   // (in a workgroup's two, a unit that begins there is the second)
-    return pieces + (PARTS ? static_cast<int64_t>(blockIdx.x) * stride + i
-                           : 2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0)) * (static_cast<int64_t>(ROWS) * (D + 2));
-  };
-  float up = neg_inf(), l = 0.f, x[E] = {};
-  for (int i = wave & 3; mine && i < split.pieces; i += 4 * kTogether) {
-    float m[kTogether], w[kTogether], y[kTogether][E];
+  int todo = units;
+  if constexpr (!PARTS) {
+    static_assert(kMostWorkgroups <= 1024, "a thread each");
+    const bool is = static_cast<int>(threadIdx.x) < units && splits[threadIdx.x].pieces > 0;
+    const uint64_t with = __ballot(is);
+    if (lane == 0) counts[wave] = __popcll(with);
+    __syncthreads();
+    int to = __popcll(with & ((1ull << lane) - 1));
+    todo = 0;
 #pragma unroll
-    for (int k = 0; k < kTogether; ++k) {
-      const bool there = i + 4 * k < split.pieces;
-      const float* p = at(there ? i + 4 * k : i);
-      m[k] = p[ROWS * D + 2 * rr];
-      w[k] = p[ROWS * D + 2 * rr + 1];
-      load_n<false, E>(p, static_cast<size_t>(rr) * D + lane * E, y[k]);
-      m[k] = there ? m[k] : neg_inf();
+    for (int w = 0; w < 16; ++w) {
+      to += w < wave ? counts[w] : 0;
+      todo += counts[w];
     }
-    float top = up;
+    if (is) list[to] = threadIdx.x;
+    __syncthreads();
+    todo = uniform(todo);
+  }
+  for (int job = blockIdx.x; job < todo * kGroups; job += gridDim.x) {
+    const int unit = PARTS ? job / kGroups : uniform(list[job / kGroups]);
+    const Split split = splits[unit];
+    if (split.pieces == 0) continue;
+    const int rr = job % kGroups * 4 + (wave >> 2), row = split.tile * ROWS + rr;
+    const Sequence s = sequence(c, split.seq);
+    const bool mine = row < s.tokens * group;
+    auto at = [&](int i) {   // (in a workgroup's two, a unit that begins there is the second)
+      return pieces + (PARTS ? static_cast<int64_t>(unit) * stride + i : 2 * static_cast<int64_t>(unit + i) + (i == 0)) *
+                          (static_cast<int64_t>(ROWS) * (D + 2));
+    };
+    float up = neg_inf(), l = 0.f, x[E] = {};
+    for (int i = wave & 3; mine && i < split.pieces; i += 4 * kTogether) {
+      float m[kTogether], w[kTogether], y[kTogether][E];
 #pragma unroll
-    for (int k = 0; k < kTogether; ++k) top = fmaxf(top, m[k]);
-    const float down = up == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(up - top);
-    up = top;
-    l *= down;
+      for (int k = 0; k < kTogether; ++k) {
+        const bool there = i + 4 * k < split.pieces;
+        const float* p = at(there ? i + 4 * k : i);
+        m[k] = p[ROWS * D + 2 * rr];
+        w[k] = p[ROWS * D + 2 * rr + 1];
+        load_n<false, E>(p, static_cast<size_t>(rr) * D + lane * E, y[k]);
+        m[k] = there ? m[k] : neg_inf();
+      }
+      float top = up;
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] *= down;
+      for (int k = 0; k < kTogether; ++k) top = fmaxf(top, m[k]);
+      const float down = up == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(up - top);
+      up = top;
+      l *= down;
 #pragma unroll
-    for (int k = 0; k < kTogether; ++k) {
-      // (a piece in which the row saw nothing holds zeros; a NaN maximum stays NaN)
-      const float f = m[k] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m[k] - up);
-      l = fmaf(f, w[k], l);
+      for (int e = 0; e < E; ++e) x[e] *= down;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = fmaf(f, y[k][e], x[e]);
+      for (int k = 0; k < kTogether; ++k) {
+        // (a piece in which the row saw nothing holds zeros; a NaN maximum stays NaN)
+        const float f = m[k] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m[k] - up);
+        l = fmaf(f, w[k], l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = fmaf(f, y[k][e], x[e]);
+      }
     }
+    store_n<false, E>(&meet[wave][lane][0], 0, x);
+    if (lane == 0) {
+      tops[wave][0] = up;
+      tops[wave][1] = l;
+    }
+    __syncthreads();
+    if ((wave & 3) == 0 && mine) {
+      float top = up;
+#pragma unroll
+      for (int k = 1; k < 4; ++k) top = fmaxf(top, tops[wave + k][0]);
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = tops[wave + k][0] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(tops[wave + k][0] - top);
+        l = fmaf(f, tops[wave + k][1], l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = fmaf(f, meet[wave + k][lane][e], x[e]);
+      }
+      const int t = row / group;
+      const size_t to = static_cast<size_t>(s.first + t) * (c.heads * group) + split.head * group + (row - t * group);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = l == 0.0f ? 0.0f : x[e] / l;
+      if (lse && lane == 0) lse[to] = row_lse(top, l);
+      store_n<OUT_BF16, E>(o, to * D + lane * E, x);
+    }
+    __syncthreads();
   }
-  store_n<false, E>(&meet[wave][lane][0], 0, x);
-  if (lane == 0) {
-    tops[wave][0] = up;
-    tops[wave][1] = l;
-  }
-  __syncthreads();
-  if ((wave & 3) != 0 || !mine) return;
-  float top = up;
-#pragma unroll
-  for (int k = 1; k < 4; ++k) top = fmaxf(top, tops[wave + k][0]);
-  l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float f = tops[wave + k][0] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(tops[wave + k][0] - top);
-    l = fmaf(f, tops[wave + k][1], l);
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(f, meet[wave + k][lane][e], x[e]);
-  }
-  const int t = row / group;
-  const size_t to = static_cast<size_t>(s.first + t) * (c.heads * group) + split.head * group + (row - t * group);
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = l == 0.0f ? 0.0f : x[e] / l;
-  store_n<OUT_BF16, E>(o, to * D + lane * E, x);
-  if (lse && lane == 0) lse[to] = row_lse(top, l);
 }
 
 namespace {
@@ -618,10 +644,18 @@ int row_tiles(int D, bool exact, int64_t rows) {
   return 4;
 }
 
-// Whether the chunk kernel takes a call.
-bool in_chunks(bool exact, int64_t rows) { return !exact && rows > 64; }
+// Whether the chunk kernel takes a call: it reads keys and values once for 256
+// rows, but computes for 256 where there are fewer.  us there and here:
+//   d 128: 64 sequences of 4096 positions, 8 key heads, 68 rows each: 229, 268;
+//     36 rows: 230, 142; one of 131072 with 256 rows: 177, 255; of 16384 with 80: 42, 36
+//   d 256: 32 sequences of 8192, 2 key heads, 256 rows: 199, 241; 128 rows: 154, 125;
+//     4 sequences with 512 rows: 83, 83; one with 512: 52, 36
+bool in_chunks(int D, bool exact, int64_t rows, int64_t all_rows) {
+  if (exact) return false;
+  return D == 256 ? rows > 128 && all_rows >= 4096 : rows > 64;
+}
 
-int workgroups(int D, int mt) { return D / 16 * mt > 16 ? 256 : 512; }
+int workgroups(int D, int mt) { return D / 16 * mt > 16 ? kMostWorkgroups / 2 : kMostWorkgroups; }
 
 int64_t rows_of(const CacheArgs& c, int group, int max_q) {
   return (max_q > 0 ? std::min<int64_t>(max_q, c.n_tokens) : c.n_tokens) * group;
@@ -632,11 +666,11 @@ int64_t rows_of(const CacheArgs& c, int group, int max_q) {
 hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, float* lse, const Split* joins,
                              float* pieces, int units, int stride, hipStream_t st) {
   constexpr int kRows = kChunkRows;
-  const dim3 grid(units, kRows / 4);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(units) * (kRows / 4), 2 * kMostWorkgroups));
   switch (D) {
-    case 64: join_pieces_kernel<64, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, stride); break;
-    case 128: join_pieces_kernel<128, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, stride); break;
-    case 256: join_pieces_kernel<256, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, stride); break;
+    case 64: join_pieces_kernel<64, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, units, stride); break;
+    case 128: join_pieces_kernel<128, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, units, stride); break;
+    case 256: join_pieces_kernel<256, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, units, stride); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -647,7 +681,7 @@ size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, 
   c.n_tokens = n_tokens;
   c.N = N;
   c.heads = heads;
-  if (in_chunks(exact, rows_of(c, group, max_q))) return attention_chunk_ws(D, c, group);
+  if (in_chunks(D, exact, rows_of(c, group, max_q), n_tokens * heads * group)) return attention_chunk_ws(D, c, group, rows_of(c, group, max_q));
   const int mt = row_tiles(D, exact, rows_of(c, group, max_q));
   const size_t wgs = workgroups(D, mt);
   return wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4;
@@ -655,8 +689,8 @@ size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, 
 
 hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
                                   float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st) {
-  if (in_chunks(!out_bf16, rows_of(c, group, max_q)))
-    return launch_attention_chunk(D, c, q, group, scale * kLog2e, o, lse, ws, in_bf16, st);
+  if (in_chunks(D, !out_bf16, rows_of(c, group, max_q), c.n_tokens * c.heads * group))
+    return launch_attention_chunk(D, c, q, group, scale * kLog2e, rows_of(c, group, max_q), o, lse, ws, in_bf16, st);
   const int mt = row_tiles(D, !out_bf16, rows_of(c, group, max_q));
   const int wgs = workgroups(D, mt);
   Split* splits = static_cast<Split*>(ws);
@@ -669,7 +703,7 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
         <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    join_pieces_kernel<kD, 16 * kT, kOut, false><<<dim3(wgs, 4 * kT), 1024, 0, st>>>(c, group, o, lse, splits, pieces, 0);
+    join_pieces_kernel<kD, 16 * kT, kOut, false><<<kMostWorkgroups, 1024, 0, st>>>(c, group, o, lse, splits, pieces, wgs, 0);
     return hipGetLastError();
   };
   using std::integral_constant;

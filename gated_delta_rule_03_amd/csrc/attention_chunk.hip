@@ -96,7 +96,7 @@ template <int D>
 struct ChunkShape {
   static constexpr int kPos = D == 256 ? 64 : 128;       // positions of a block
   static constexpr int kSteps = kPos / kStep;
-  static constexpr int kLeast = D == 256 ? 8 : 4;        // blocks of a part: its rows' sums are written and read again
+  static constexpr int kLeast = 3;                       // blocks of a part: its rows' sums are written and read again
   static constexpr int kAhead = 4;                       // blocks' raw bytes in LDS
   static constexpr int kAtOnce = D == 256 ? 1 : 2;       // steps whose scores a wave forms together
   static constexpr int kRowBytes = D / 2;
@@ -496,19 +496,31 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
 
 namespace {
 
+constexpr int kMostParts = 128, kMostPieces = 768;
+
 // The most units that a call can have: every sequence's last tile may be a short one.
-int64_t most_units(const CacheArgs& c, int group) {
-  return (c.n_tokens * group / kChunkRows + c.N) * c.heads;
+int64_t most_units(const CacheArgs& c, int group) { return (c.n_tokens * group / kChunkRows + c.N) * c.heads; }
+
+// Units to be expected: no sequence has more than max_rows rows.  (The results
+// do not rest on it.)
+int64_t units_by(const CacheArgs& c, int group, int64_t max_rows) {
+  const int64_t tiles = std::max(c.n_tokens * group / kChunkRows, (max_rows + kChunkRows - 1) / kChunkRows * c.N);
+  return std::min(tiles * c.heads, most_units(c, group));
 }
 
-// Equal parts of each unit's positions at most: what fills the CUs (a workgroup
-// each) best, where a part costs a hundredth of a unit to join.  The kernel takes
-// fewer where the positions are few.
-int parts_of(int64_t units) {
+// Equal parts of each unit's positions at most, of the blocks that the page table
+// has room for: what takes the CUs (a workgroup each) the least time, counted in
+// blocks of 256 rows: a workgroup costs two and a half besides its own, the join
+// one and a half, and a part's sums, written and read again, a thirtieth on all
+// CUs.  The kernel takes fewer where the positions are few.
+template <int D>
+int parts_of(const CacheArgs& c, int64_t units) {
+  const int64_t room = (static_cast<int64_t>(c.max_pages) << c.page_shift) / ChunkShape<D>::kPos + 1;
   int best = 1;
   double least = 1e30;
-  for (int s = 1; s <= 32 && units * s <= 768; ++s) {
-    const double cost = static_cast<double>((units * s + 255) / 256) / s + 0.01 * (s - 1);
+  for (int s = 1; s <= kMostParts && units * s <= kMostPieces; ++s) {
+    const double cost = static_cast<double>((units * s + 255) / 256) * (static_cast<double>((room + s - 1) / s) + 2.5) +
+                        (s > 1 ? 1.5 + 0.033 * static_cast<double>(units * s) : 0.0);
     if (cost < least) {
       least = cost;
       best = s;
@@ -517,19 +529,22 @@ int parts_of(int64_t units) {
   return best;
 }
 
-}  // namespace
-
-size_t attention_chunk_ws(int D, const CacheArgs& c, int group) {
-  const int64_t units = most_units(c, group);
-  const int parts = parts_of(units);
-  if (parts == 1) return 16;
-  return units * sizeof(Split) + static_cast<size_t>(units) * parts * kChunkRows * (D + 2) * 4;
+int parts_of(int D, const CacheArgs& c, int64_t units) {
+  return D == 64 ? parts_of<64>(c, units) : D == 128 ? parts_of<128>(c, units) : parts_of<256>(c, units);
 }
 
-hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale, void* o, float* lse,
-                                  void* ws, bool in_bf16, hipStream_t st) {
+}  // namespace
+
+size_t attention_chunk_ws(int D, const CacheArgs& c, int group, int64_t max_rows) {
+  const int64_t units = units_by(c, group, max_rows), parts = units > 0 ? std::min<int64_t>(kMostParts, kMostPieces / units) : 1;
+  if (parts <= 1) return 16;
+  return most_units(c, group) * (sizeof(Split) + static_cast<size_t>(parts) * kChunkRows * (D + 2) * 4);
+}
+
+hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale,
+                                  int64_t max_rows, void* o, float* lse, void* ws, bool in_bf16, hipStream_t st) {
   const int64_t units = most_units(c, group);
-  const int parts = parts_of(units);
+  const int parts = parts_of(D, c, units_by(c, group, max_rows));
   Split* joins = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(joins + units);
   const dim3 grid(static_cast<unsigned>((units * parts + 7) / 8 * 8));
