@@ -85,9 +85,10 @@ __device__ __forceinline__ void lay_out(int N, T* before, int64_t* sums, F&& cou
 }
 
 // What the joining kernel has to know of a unit whose positions were shared out.
-struct Split {
-  int seq, head, tile;
-  int pieces;   // 0: nothing to join
+struct alignas(32) Split {
+  int first, row0, rows;   // the sequence's first token; the unit's first row in it and how many are there
+  int head;
+  int pieces;              // 0: nothing to join
 };
 
 // A step's first bytes in the cache; the same in every lane.

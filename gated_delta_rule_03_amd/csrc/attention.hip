@@ -372,7 +372,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   const int64_t start = share * blockIdx.x;
   const int64_t end = start + share < total ? start + share : total;
-  Split split = {0, 0, 0, 0};
+  Split split = {0, 0, 0, 0, 0};
   const LaneOffsets<D, QK> lanes(c.page_shift);
   const int64_t page_bytes = static_cast<int64_t>(c.heads) * (D / 2) << c.page_shift;
 
@@ -526,7 +526,8 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
       __syncthreads();
     }
     if (!whole && b0 == 0)
-      split = {n, head, tile, 1 + static_cast<int>((blocks - b1 + share - 1) / share)};
+      split = {s.first, tile * kRows, std::min(rows - tile * kRows, kRows), head,
+               1 + static_cast<int>((blocks - b1 + share - 1) / share)};
     cur += b1 - b0;
   }
   if (threadIdx.x == 0) splits[blockIdx.x] = split;
@@ -534,57 +535,84 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
 
 // Joins the pieces of units: PARTS: of the chunk kernel's, of `stride` places each;
 // otherwise of those that began in one of the `units` workgroups of the kernel
-// above, found by a count over them.  Four waves share a row's pieces, each with
-// eight of them in flight; a workgroup takes four rows at a time.
+// above, found by a count over them.  A wave takes a row, eight pieces of it in
+// flight, or four waves do where there are more than eight.
 template <int D, int ROWS, bool OUT_BF16, bool PARTS>
-__global__ __launch_bounds__(1024) void join_pieces_kernel(CacheArgs c, int group, void* __restrict__ o,
+__global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group, void* __restrict__ o,
                                                            float* __restrict__ lse, const Split* __restrict__ splits,
                                                            const float* __restrict__ pieces, int units, int stride) {
   constexpr int E = D / 64, kTogether = 8;   // channels of a lane; pieces whose loads are in flight
-  constexpr int kGroups = ROWS / 4;
   __shared__ float meet[16][64][E], tops[16][2];
-  __shared__ int counts[16], list[PARTS ? 1 : kMostWorkgroups];
+  __shared__ int counts[2][16];
+  __shared__ Split found[PARTS ? 1 : kMostWorkgroups];   // units of few pieces from the front, of many from the back
+  __shared__ int list[PARTS ? 1 : kMostWorkgroups];      // the workgroups that they are of
   const int wave = uniform(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-  int todo = units;
+  int few = stride > kTogether ? 0 : units, many = units - few;
   if constexpr (!PARTS) {
     static_assert(kMostWorkgroups <= 1024, "a thread each");
-    const bool is = static_cast<int>(threadIdx.x) < units && splits[threadIdx.x].pieces > 0;
-    const uint64_t with = __ballot(is);
-    if (lane == 0) counts[wave] = __popcll(with);
+    const Split& own = splits[static_cast<int>(threadIdx.x) < units ? threadIdx.x : 0];
+    const int first = own.first, row0 = own.row0, rows = own.rows, head = own.head;
+    const int n = static_cast<int>(threadIdx.x) < units ? own.pieces : 0;
+    const uint64_t with_few = __ballot(n > 0 && n <= kTogether), with_many = __ballot(n > kTogether);
+    if (lane == 0) {
+      counts[0][wave] = __popcll(with_few);
+      counts[1][wave] = __popcll(with_many);
+    }
     __syncthreads();
-    int to = __popcll(with & ((1ull << lane) - 1));
-    todo = 0;
+    const uint64_t below = (1ull << lane) - 1;
+    int to_few = __popcll(with_few & below), to_many = __popcll(with_many & below);
+    few = many = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
-      to += w < wave ? counts[w] : 0;
-      todo += counts[w];
+      to_few += w < wave ? counts[0][w] : 0;
+      to_many += w < wave ? counts[1][w] : 0;
+      few += counts[0][w];
+      many += counts[1][w];
     }
-    if (is) list[to] = threadIdx.x;
+    if (n > 0) {
+      const int to = n > kTogether ? kMostWorkgroups - 1 - to_many : to_few;
+      found[to].first = first;
+      found[to].row0 = row0;
+      found[to].rows = rows;
+      found[to].head = head;
+      found[to].pieces = n;
+      list[to] = threadIdx.x;
+    }
     __syncthreads();
-    todo = uniform(todo);
+    few = uniform(few);
+    many = uniform(many);
   }
-  for (int job = blockIdx.x; job < todo * kGroups; job += gridDim.x) {
-    const int unit = PARTS ? job / kGroups : uniform(list[job / kGroups]);
-    const Split split = splits[unit];
-    if (split.pieces == 0) continue;
-    const int rr = job % kGroups * 4 + (wave >> 2), row = split.tile * ROWS + rr;
-    const Sequence s = sequence(c, split.seq);
-    const bool mine = row < s.tokens * group;
+  constexpr int kFew = ROWS / 16, kMany = ROWS / 4;   // a unit's jobs
+  for (int job = blockIdx.x; job < few * kFew + many * kMany; job += gridDim.x) {
+    const bool shared = job >= few * kFew;
+    const int own = shared ? job - few * kFew : job;
+    const int at_unit = shared ? own / kMany : own / kFew;
+    const int slot = PARTS ? 0 : shared ? kMostWorkgroups - 1 - at_unit : at_unit;
+    const int unit = PARTS ? at_unit : uniform(list[slot]);
+    auto field = [&](int Split::*f) {
+      if constexpr (PARTS) return splits[unit].*f;
+      else return uniform(found[slot].*f);
+    };
+    const int n_pieces = field(&Split::pieces), rows = field(&Split::rows), row0 = field(&Split::row0);
+    if (n_pieces == 0) continue;
+    const int rr = shared ? own % kMany * 4 + (wave >> 2) : own % kFew * 16 + wave;
+    const int first = shared ? wave & 3 : 0, step = shared ? 4 : 1;
+    const bool mine = rr < rows;
     auto at = [&](int i) {   // (in a workgroup's two, a unit that begins there is the second)
       return pieces + (PARTS ? static_cast<int64_t>(unit) * stride + i : 2 * static_cast<int64_t>(unit + i) + (i == 0)) *
                           (static_cast<int64_t>(ROWS) * (D + 2));
     };
     float up = neg_inf(), l = 0.f, x[E] = {};
-    for (int i = wave & 3; mine && i < split.pieces; i += 4 * kTogether) {
-      float m[kTogether], w[kTogether], y[kTogether][E];
+    for (int i = first; mine && i < n_pieces; i += step * kTogether) {
+      float m[kTogether], w[kTogether] = {}, y[kTogether][E] = {};
 #pragma unroll
       for (int k = 0; k < kTogether; ++k) {
-        const bool there = i + 4 * k < split.pieces;
-        const float* p = at(there ? i + 4 * k : i);
+        m[k] = neg_inf();
+        if (i + step * k >= n_pieces) continue;
+        const float* p = at(i + step * k);
         m[k] = p[ROWS * D + 2 * rr];
         w[k] = p[ROWS * D + 2 * rr + 1];
         load_n<false, E>(p, static_cast<size_t>(rr) * D + lane * E, y[k]);
-        m[k] = there ? m[k] : neg_inf();
       }
       float top = up;
 #pragma unroll
@@ -603,34 +631,37 @@ __global__ __launch_bounds__(1024) void join_pieces_kernel(CacheArgs c, int grou
         for (int e = 0; e < E; ++e) x[e] = fmaf(f, y[k][e], x[e]);
       }
     }
-    store_n<false, E>(&meet[wave][lane][0], 0, x);
-    if (lane == 0) {
-      tops[wave][0] = up;
-      tops[wave][1] = l;
-    }
-    __syncthreads();
-    if ((wave & 3) == 0 && mine) {
-      float top = up;
+    float top = up;
+    if (shared) {
+      store_n<false, E>(&meet[wave][lane][0], 0, x);
+      if (lane == 0) {
+        tops[wave][0] = up;
+        tops[wave][1] = l;
+      }
+      __syncthreads();
 #pragma unroll
-      for (int k = 1; k < 4; ++k) top = fmaxf(top, tops[wave + k][0]);
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, tops[(wave & 12) + k][0]);
       l = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float f = tops[wave + k][0] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(tops[wave + k][0] - top);
-        l = fmaf(f, tops[wave + k][1], l);
+        const float m = tops[(wave & 12) + k][0], f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        l = fmaf(f, tops[(wave & 12) + k][1], l);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(f, meet[wave + k][lane][e], x[e]);
+        for (int e = 0; e < E; ++e) x[e] = fmaf(f, meet[(wave & 12) + k][lane][e], x[e]);
       }
-      const int t = row / group;
-      const size_t to = static_cast<size_t>(s.first + t) * (c.heads * group) + split.head * group + (row - t * group);
+      __syncthreads();
+    }
+    if (mine && first == 0) {
+      const int t = (row0 + rr) / group;
+      const size_t to =
+          static_cast<size_t>(field(&Split::first) + t) * heads * group + field(&Split::head) * group + (row0 + rr - t * group);
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] = l == 0.0f ? 0.0f : x[e] / l;
       if (lse && lane == 0) lse[to] = row_lse(top, l);
       store_n<OUT_BF16, E>(o, to * D + lane * E, x);
     }
-    __syncthreads();
   }
 }
 
@@ -668,9 +699,9 @@ hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, floa
   constexpr int kRows = kChunkRows;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(units) * (kRows / 4), 2 * kMostWorkgroups));
   switch (D) {
-    case 64: join_pieces_kernel<64, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, units, stride); break;
-    case 128: join_pieces_kernel<128, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, units, stride); break;
-    case 256: join_pieces_kernel<256, kRows, true, true><<<grid, 1024, 0, st>>>(c, group, o, lse, joins, pieces, units, stride); break;
+    case 64: join_pieces_kernel<64, kRows, true, true><<<grid, 1024, 0, st>>>(c.heads, group, o, lse, joins, pieces, units, stride); break;
+    case 128: join_pieces_kernel<128, kRows, true, true><<<grid, 1024, 0, st>>>(c.heads, group, o, lse, joins, pieces, units, stride); break;
+    case 256: join_pieces_kernel<256, kRows, true, true><<<grid, 1024, 0, st>>>(c.heads, group, o, lse, joins, pieces, units, stride); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -703,7 +734,7 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
         <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    join_pieces_kernel<kD, 16 * kT, kOut, false><<<kMostWorkgroups, 1024, 0, st>>>(c, group, o, lse, splits, pieces, wgs, 0);
+    join_pieces_kernel<kD, 16 * kT, kOut, false><<<kMostWorkgroups, 1024, 0, st>>>(c.heads, group, o, lse, splits, pieces, wgs, 0);
     return hipGetLastError();
   };
   using std::integral_constant;

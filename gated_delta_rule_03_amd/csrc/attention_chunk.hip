@@ -461,7 +461,8 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   }
 
   sum_of_row += __shfl_xor(sum_of_row, 32);
-  if (splits > 1 && part == 0 && threadIdx.x == 0) joins[id] = {n, head, tile, shares > 1 ? shares : 0};
+  if (splits > 1 && part == 0 && threadIdx.x == 0)
+    joins[id] = {s.first, tile * kRows, std::min(rows - tile * kRows, kRows), head, shares > 1 ? shares : 0};
   if (row >= rows) return;
   if (shares > 1) {
     float* piece = pieces + (static_cast<int64_t>(id) * splits + part) * (static_cast<int64_t>(kRows) * (D + 2));
