@@ -83,7 +83,8 @@ __device__ __forceinline__ float round_odd(double y) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(y));
   constexpr uint64_t kCut = (1ull << 29) - 1;   // bits that fp32 does not have
   const float f = static_cast<float>(__longlong_as_double(static_cast<long long>(b & ~kCut)));
-  return __uint_as_float(__float_as_uint(f) | ((b & kCut) != 0));
+  const uint32_t cut = static_cast<uint32_t>(b & kCut);
+  return __uint_as_float(__float_as_uint(f) | (cut < 1u ? cut : 1u));
 }
 
 __device__ __forceinline__ uint32_t max_bits(const float (&x)[8]) {
@@ -148,8 +149,13 @@ __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheAr
   // largest magnitudes of the runs of 8 channels, a group's in the channels' order
   __shared__ alignas(16) uint32_t most[kThreads / L][2 * L];
   const int lane = threadIdx.x % L;
+  // sines and cosines of the group's token, one a pair: each formed by one lane,
+  // pair L i + lane in its turn i
+  __shared__ double2 circle[kThreads / L][D / 2];
   const HeadRuns<D, INTER> runs(lane, r.rotary_dim);
-  const PairRates rates = pair_rates<D, INTER>(r, runs);
+  const int pairs = r.rotary_dim >> 1;
+  const PairRates rates = pair_rates(r, pairs, [&](int i) { return L * i + lane; });
+  double2* const around = circle[threadIdx.x / L];
   uint32_t* const mine = most[threadIdx.x / L];
   const int va = 8 * lane, vb = D / 2 + 8 * lane;   // the runs of the values
   const int n_runs = (c.heads + run_len - 1) / run_len;
@@ -164,11 +170,17 @@ __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheAr
     const int page = page_of(c, at.seq, at.pos);
     if (page < 0) continue;
     const int off = static_cast<int>(at.pos & ((1 << c.page_shift) - 1));
-    double cs[8], sn[8];
     if (r.rotary_dim) {
       const Places places = r.positions ? Places(r, token) : Places(static_cast<int32_t>(at.pos));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sincos_turns(turns(rates, places, e), sn[e], cs[e]);
+      for (int i = 0; i < 8; ++i) {
+        if (L * i >= pairs) break;
+        double2 cs;
+        sincos_turns(turns(rates, places, i), cs.y, cs.x);
+        around[L * i + lane] = cs;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     float wa[8], wb[8];
     if (w) {
@@ -205,7 +217,16 @@ __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheAr
           yb[e] = kb[e];
         }
       }
-      rotate<D, INTER>(runs, ya, yb, cs, sn);
+      if (runs.turn_a || runs.turn_b) {
+        double cs[8], sn[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const double2 x = around[runs.turned(e) ? runs.pair(e) : 0];
+          cs[e] = x.x;
+          sn[e] = x.y;
+        }
+        rotate<D, INTER>(runs, ya, yb, cs, sn);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         ka[e] = round_odd(ya[e]);
