@@ -45,6 +45,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kBlockPos = kWaves * kStep;   // positions of a block
 constexpr int kMostWorkgroups = 512;        // two a CU
+constexpr int64_t kMostUnits = 1 << 22;     // of the chunk kernel
 // A piece's place in the workspace: its rows' sums, then maxima and weights' sums.
 template <int D, int ROWS>
 __device__ __forceinline__ float* piece_at(float* pieces, int64_t slot) {
@@ -681,9 +682,10 @@ int row_tiles(int D, bool exact, int64_t rows) {
 //     36 rows: 230, 142; one of 131072 with 256 rows: 177, 255; of 16384 with 80: 42, 36
 //   d 256: 32 sequences of 8192, 2 key heads, 256 rows: 199, 241; 128 rows: 154, 125;
 //     4 sequences with 512 rows: 83, 83; one with 512: 52, 36
-bool in_chunks(int D, bool exact, int64_t rows, int64_t all_rows) {
-  if (exact) return false;
-  return D == 256 ? rows > 128 && all_rows >= 4096 : rows > 64;
+// (Its workgroups are the units, which have to fit a grid.)
+bool in_chunks(int D, const CacheArgs& c, int group, bool exact, int64_t rows) {
+  if (exact || (c.n_tokens * group / kChunkRows + c.N) * c.heads > kMostUnits) return false;
+  return D == 256 ? rows > 128 && c.n_tokens * c.heads * group >= 4096 : rows > 64;
 }
 
 int workgroups(int D, int mt) { return D / 16 * mt > 16 ? kMostWorkgroups / 2 : kMostWorkgroups; }
@@ -712,7 +714,7 @@ size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, 
   c.n_tokens = n_tokens;
   c.N = N;
   c.heads = heads;
-  if (in_chunks(D, exact, rows_of(c, group, max_q), n_tokens * heads * group)) return attention_chunk_ws(D, c, group, rows_of(c, group, max_q));
+  if (in_chunks(D, c, group, exact, rows_of(c, group, max_q))) return attention_chunk_ws(D, c, group, rows_of(c, group, max_q));
   const int mt = row_tiles(D, exact, rows_of(c, group, max_q));
   const size_t wgs = workgroups(D, mt);
   return wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4;
@@ -720,7 +722,7 @@ size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, 
 
 hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
                                   float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st) {
-  if (in_chunks(D, !out_bf16, rows_of(c, group, max_q), c.n_tokens * c.heads * group))
+  if (in_chunks(D, c, group, !out_bf16, rows_of(c, group, max_q)))
     return launch_attention_chunk(D, c, q, group, scale * kLog2e, rows_of(c, group, max_q), o, lse, ws, in_bf16, st);
   const int mt = row_tiles(D, !out_bf16, rows_of(c, group, max_q));
   const int wgs = workgroups(D, mt);
