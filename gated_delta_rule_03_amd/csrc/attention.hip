@@ -536,69 +536,24 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
 
 // Joins the pieces of units: PARTS: of the chunk kernel's, of `stride` places each;
 // otherwise of those that began in one of the `units` workgroups of the kernel
-// above, found by a count over them.  A wave takes a row, eight pieces of it in
-// flight, or four waves do where there are more than eight.
+// above.  A wave takes a row, eight pieces of it in flight, or four waves do where
+// there are more than eight; the workgroups take the units of few pieces by their
+// own number, and find those of many by a count over all.
 template <int D, int ROWS, bool OUT_BF16, bool PARTS>
 __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group, void* __restrict__ o,
                                                            float* __restrict__ lse, const Split* __restrict__ splits,
                                                            const float* __restrict__ pieces, int units, int stride) {
   constexpr int E = D / 64, kTogether = 8;   // channels of a lane; pieces whose loads are in flight
   __shared__ float meet[16][64][E], tops[16][2];
-  __shared__ int counts[2][16];
-  __shared__ Split found[PARTS ? 1 : kMostWorkgroups];   // units of few pieces from the front, of many from the back
-  __shared__ int list[PARTS ? 1 : kMostWorkgroups];      // the workgroups that they are of
+  __shared__ int counts[16], list[PARTS ? 1 : kMostWorkgroups];
   const int wave = uniform(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-  int few = stride > kTogether ? 0 : units, many = units - few;
-  if constexpr (!PARTS) {
-    static_assert(kMostWorkgroups <= 1024, "a thread each");
-    const Split& own = splits[static_cast<int>(threadIdx.x) < units ? threadIdx.x : 0];
-    const int first = own.first, row0 = own.row0, rows = own.rows, head = own.head;
-    const int n = static_cast<int>(threadIdx.x) < units ? own.pieces : 0;
-    const uint64_t with_few = __ballot(n > 0 && n <= kTogether), with_many = __ballot(n > kTogether);
-    if (lane == 0) {
-      counts[0][wave] = __popcll(with_few);
-      counts[1][wave] = __popcll(with_many);
-    }
-    __syncthreads();
-    const uint64_t below = (1ull << lane) - 1;
-    int to_few = __popcll(with_few & below), to_many = __popcll(with_many & below);
-    few = many = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      to_few += w < wave ? counts[0][w] : 0;
-      to_many += w < wave ? counts[1][w] : 0;
-      few += counts[0][w];
-      many += counts[1][w];
-    }
-    if (n > 0) {
-      const int to = n > kTogether ? kMostWorkgroups - 1 - to_many : to_few;
-      found[to].first = first;
-      found[to].row0 = row0;
-      found[to].rows = rows;
-      found[to].head = head;
-      found[to].pieces = n;
-      list[to] = threadIdx.x;
-    }
-    __syncthreads();
-    few = uniform(few);
-    many = uniform(many);
-  }
-  constexpr int kFew = ROWS / 16, kMany = ROWS / 4;   // a unit's jobs
-  for (int job = blockIdx.x; job < few * kFew + many * kMany; job += gridDim.x) {
-    const bool shared = job >= few * kFew;
-    const int own = shared ? job - few * kFew : job;
-    const int at_unit = shared ? own / kMany : own / kFew;
-    const int slot = PARTS ? 0 : shared ? kMostWorkgroups - 1 - at_unit : at_unit;
-    const int unit = PARTS ? at_unit : uniform(list[slot]);
-    auto field = [&](int Split::*f) {
-      if constexpr (PARTS) return splits[unit].*f;
-      else return uniform(found[slot].*f);
-    };
-    const int n_pieces = field(&Split::pieces), rows = field(&Split::rows), row0 = field(&Split::row0);
-    if (n_pieces == 0) continue;
-    const int rr = shared ? own % kMany * 4 + (wave >> 2) : own % kFew * 16 + wave;
-    const int first = shared ? wave & 3 : 0, step = shared ? 4 : 1;
-    const bool mine = rr < rows;
+
+  // row rr of a unit, of which this wave takes pieces first, first + step ..
+  auto join = [&](int unit, int rr, int first, int step) {
+    const bool shared = step > 1;
+    const Split* split = splits + unit;
+    const int n_pieces = split->pieces, row = split->row0 + rr;
+    const bool mine = rr < split->rows;
     auto at = [&](int i) {   // (in a workgroup's two, a unit that begins there is the second)
       return pieces + (PARTS ? static_cast<int64_t>(unit) * stride + i : 2 * static_cast<int64_t>(unit + i) + (i == 0)) *
                           (static_cast<int64_t>(ROWS) * (D + 2));
@@ -655,14 +610,47 @@ __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group,
       __syncthreads();
     }
     if (mine && first == 0) {
-      const int t = (row0 + rr) / group;
-      const size_t to =
-          static_cast<size_t>(field(&Split::first) + t) * heads * group + field(&Split::head) * group + (row0 + rr - t * group);
+      const int t = row / group;
+      const size_t to = static_cast<size_t>(split->first + t) * heads * group + split->head * group + (row - t * group);
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] = l == 0.0f ? 0.0f : x[e] / l;
       if (lse && lane == 0) lse[to] = row_lse(top, l);
       store_n<OUT_BF16, E>(o, to * D + lane * E, x);
     }
+  };
+
+  constexpr int kFew = ROWS / 16, kMany = ROWS / 4;   // a unit's jobs
+  if constexpr (PARTS) {
+    const bool many = stride > kTogether;
+    const int jobs = many ? kMany : kFew;
+    for (int job = blockIdx.x; job < units * jobs; job += gridDim.x) {
+      const int unit = job / jobs, own = job - unit * jobs;
+      if (splits[unit].pieces == 0) continue;
+      if (many) join(unit, own * 4 + (wave >> 2), wave & 3, 4);
+      else join(unit, own * 16 + wave, 0, 1);
+    }
+  } else {
+    static_assert(kMostWorkgroups <= 1024, "a thread each");
+    const bool many = static_cast<int>(threadIdx.x) < units && splits[threadIdx.x].pieces > kTogether;
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+      const int n = splits[unit].pieces;
+      if (n == 0 || n > kTogether) continue;
+      for (int own = 0; own < kFew; ++own) join(unit, own * 16 + wave, 0, 1);
+    }
+    const uint64_t with = __ballot(many);
+    if (lane == 0) counts[wave] = __popcll(with);
+    __syncthreads();
+    int to = __popcll(with & ((1ull << lane) - 1)), todo = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      to += w < wave ? counts[w] : 0;
+      todo += counts[w];
+    }
+    if (many) list[to] = threadIdx.x;
+    __syncthreads();
+    todo = uniform(todo) * kMany;
+    for (int job = blockIdx.x; job < todo; job += gridDim.x)
+      join(uniform(list[job / kMany]), job % kMany * 4 + (wave >> 2), wave & 3, 4);
   }
 }
 
