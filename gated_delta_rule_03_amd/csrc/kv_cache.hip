@@ -139,7 +139,32 @@ __device__ __forceinline__ void decode8(uint32_t w, int scale_byte, float (&x)[8
 
 }  // namespace
 
+// 8 elements as they are in memory, so that their loads can be under way early.
+template <bool BF16>
+struct Raw8 {
+  uint4 w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int x = 0; x < (BF16 ? 1 : 2); ++x) w[x] = from[x];
+  }
+  __device__ __forceinline__ void widen(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (BF16) {
+        const uint32_t pair = e < 2 ? w[0].x : e < 4 ? w[0].y : e < 6 ? w[0].z : w[0].w;
+        x[e] = __uint_as_float(e & 1 ? pair & 0xffff0000u : pair << 16);
+      } else {
+        const uint4& v = w[e >> 2 & (BF16 ? 0 : 1)];
+        x[e] = __uint_as_float((e & 3) == 0 ? v.x : (e & 3) == 1 ? v.y : (e & 3) == 2 ? v.z : v.w);
+      }
+    }
+  }
+};
+
 // Group g of D / 16 lanes takes token g / runs and the run g % runs of its heads.
+// A head's rows are on their way while the head before them is worked on, the
+// first one's while the token's place is looked up.
 template <int D, bool BF16, bool INTER>
 __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheArgs c, const void* __restrict__ k,
                                                              int64_t k_stride, const void* __restrict__ v,
@@ -165,6 +190,16 @@ __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheAr
     const int64_t token = g / n_runs;
     const int h0 = static_cast<int>(g - token * n_runs) * run_len;
     const int h1 = h0 + run_len < c.heads ? h0 + run_len : c.heads;
+    Raw8<BF16> raw[4];
+    auto fetch = [&](int h) {
+      const size_t ki = static_cast<size_t>(token) * k_stride + static_cast<size_t>(h) * D;
+      const size_t vi = static_cast<size_t>(token) * v_stride + static_cast<size_t>(h) * D;
+      raw[0].load(k, ki + runs.a);
+      raw[1].load(k, ki + runs.b);
+      raw[2].load(v, vi + va);
+      raw[3].load(v, vi + vb);
+    };
+    fetch(h0);
     const RowAt at = row_at(c, token);
     if (at.seq < 0) continue;
     const int page = page_of(c, at.seq, at.pos);
@@ -188,13 +223,12 @@ __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheAr
       load_n<false, 8>(w, runs.b, wb);
     }
     for (int h = h0; h < h1; ++h) {
-      const size_t ki = static_cast<size_t>(token) * k_stride + static_cast<size_t>(h) * D;
-      const size_t vi = static_cast<size_t>(token) * v_stride + static_cast<size_t>(h) * D;
       float ka[8], kb[8], xa[8], xb[8];
-      load_n<BF16, 8>(k, ki + runs.a, ka);
-      load_n<BF16, 8>(k, ki + runs.b, kb);
-      load_n<BF16, 8>(v, vi + va, xa);
-      load_n<BF16, 8>(v, vi + vb, xb);
+      raw[0].widen(ka);
+      raw[1].widen(kb);
+      raw[2].widen(xa);
+      raw[3].widen(xb);
+      fetch(h + 1 < h1 ? h + 1 : h);
       double ya[8], yb[8];
       if (w) {
         double ss = 0.0;
