@@ -174,12 +174,19 @@ __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheAr
   // largest magnitudes of the runs of 8 channels, a group's in the channels' order
   __shared__ alignas(16) uint32_t most[kThreads / L][2 * L];
   const int lane = threadIdx.x % L;
-  // sines and cosines of the group's token, one a pair: each formed by one lane,
-  // pair L i + lane in its turn i
+  // turns a position and axes of the pairs; sines and cosines of the groups'
+  // tokens, each formed by one lane
+  __shared__ double rate[D / 2];
+  __shared__ uint32_t axis[D / 2];
   __shared__ double2 circle[kThreads / L][D / 2];
   const HeadRuns<D, INTER> runs(lane, r.rotary_dim);
   const int pairs = r.rotary_dim >> 1;
-  const PairRates rates = pair_rates(r, pairs, [&](int i) { return L * i + lane; });
+  if (static_cast<int>(threadIdx.x) < pairs) {
+    const int ax = r.axis ? r.axis[threadIdx.x] : 0;
+    rate[threadIdx.x] = static_cast<double>(r.inv_freq[threadIdx.x]) * kPerTurn;
+    axis[threadIdx.x] = ax < 0 ? 0 : ax >= r.num_axes ? r.num_axes - 1 : ax;
+  }
+  __syncthreads();
   double2* const around = circle[threadIdx.x / L];
   uint32_t* const mine = most[threadIdx.x / L];
   const int va = 8 * lane, vb = D / 2 + 8 * lane;   // the runs of the values
@@ -208,12 +215,11 @@ __global__ __launch_bounds__(kThreads) void append_kv_kernel(RopeArgs r, CacheAr
     if (r.rotary_dim) {
       const Places places = r.positions ? Places(r, token) : Places(static_cast<int32_t>(at.pos));
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (L * i >= pairs) break;
+#pragma unroll 1
+      for (int i = lane; i < pairs; i += L) {
         double2 cs;
-        sincos_turns(turns(rates, places, i), cs.y, cs.x);
-        around[L * i + lane] = cs;
+        sincos_turns(turns(rate[i], places.on(axis[i])), cs.y, cs.x);
+        around[i] = cs;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }

@@ -50,31 +50,26 @@ struct PairRates {
 
 // (Every load is made, of pair 0 where a lane turns nothing, so that none waits
 // for another: under conditions these 16 took 10 us of a small call.)
-template <class PairOf>   // pair_of(e) >= pairs: none
-__device__ __forceinline__ PairRates pair_rates(const RopeArgs& r, int pairs, PairOf&& pair_of) {
-  constexpr double kPerTurn = 0.15915494309189533577;   // 1 / (2 pi)
+constexpr double kPerTurn = 0.15915494309189533577;   // 1 / (2 pi)
+
+template <int D, bool INTER>
+__device__ __forceinline__ PairRates pair_rates(const RopeArgs& r, const HeadRuns<D, INTER>& runs) {
   PairRates p = {};
-  if (pairs == 0) return p;
+  if (r.rotary_dim == 0) return p;
   float f[8];
   int ax[8] = {};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = r.inv_freq[pair_of(e) < pairs ? pair_of(e) : 0];
+  for (int e = 0; e < 8; ++e) f[e] = r.inv_freq[runs.turned(e) ? runs.pair(e) : 0];
   if (r.axis) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ax[e] = r.axis[pair_of(e) < pairs ? pair_of(e) : 0];
+    for (int e = 0; e < 8; ++e) ax[e] = r.axis[runs.turned(e) ? runs.pair(e) : 0];
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    p.rate[e] = pair_of(e) < pairs ? static_cast<double>(f[e]) * kPerTurn : 0.0;
+    p.rate[e] = runs.turned(e) ? static_cast<double>(f[e]) * kPerTurn : 0.0;
     p.axes |= static_cast<uint32_t>(ax[e] < 0 ? 0 : ax[e] >= r.num_axes ? r.num_axes - 1 : ax[e]) << (2 * e);
   }
   return p;
-}
-
-// Of a lane's own runs.
-template <int D, bool INTER>
-__device__ __forceinline__ PairRates pair_rates(const RopeArgs& r, const HeadRuns<D, INTER>& runs) {
-  return pair_rates(r, r.rotary_dim >> 1, [&](int e) { return runs.turned(e) ? runs.pair(e) : D; });
 }
 
 // The token's positions on every axis.  (Four scalars: an array that is indexed
@@ -100,9 +95,12 @@ struct Places {
 // Pair e's angle at the token, in turns within half a turn.  The product of a
 // 31-bit position and a 24-bit frequency is exact in 64 bits but for the one
 // rounding of the rate: 1e-10 turns at position 10^6.
-__device__ __forceinline__ double turns(const PairRates& p, const Places& at, int e) {
-  const double t = static_cast<double>(at.on((p.axes >> (2 * e)) & 3)) * p.rate[e];
+__device__ __forceinline__ double turns(double rate, int32_t position) {
+  const double t = static_cast<double>(position) * rate;
   return t - rint(t);
+}
+__device__ __forceinline__ double turns(const PairRates& p, const Places& at, int e) {
+  return turns(p.rate[e], at.on((p.axes >> (2 * e)) & 3));
 }
 
 // (a, b) rotated by the pairs' sines: the runs of one lane, T float or double.
