@@ -83,8 +83,7 @@ __device__ __forceinline__ float round_odd(double y) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(y));
   constexpr uint64_t kCut = (1ull << 29) - 1;   // bits that fp32 does not have
   const float f = static_cast<float>(__longlong_as_double(static_cast<long long>(b & ~kCut)));
-  const uint32_t cut = static_cast<uint32_t>(b & kCut);
-  return __uint_as_float(__float_as_uint(f) | (cut < 1u ? cut : 1u));
+  return __uint_as_float(__float_as_uint(f) | ((b & kCut) != 0));
 }
 
 __device__ __forceinline__ uint32_t max_bits(const float (&x)[8]) {

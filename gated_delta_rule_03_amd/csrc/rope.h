@@ -48,10 +48,10 @@ struct PairRates {
   uint32_t axes;
 };
 
-// (Every load is made, of pair 0 where a lane turns nothing, so that none waits
-// for another: under conditions these 16 took 10 us of a small call.)
 constexpr double kPerTurn = 0.15915494309189533577;   // 1 / (2 pi)
 
+// (Every load is made, of pair 0 where a lane turns nothing, so that none waits
+// for another: under conditions these 16 took 10 us of a small call.)
 template <int D, bool INTER>
 __device__ __forceinline__ PairRates pair_rates(const RopeArgs& r, const HeadRuns<D, INTER>& runs) {
   PairRates p = {};
