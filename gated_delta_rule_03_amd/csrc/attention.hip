@@ -656,26 +656,33 @@ __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group,
 
 namespace {
 
-// Row tiles of 16 that a workgroup takes: as many as the rows of a key head
-// fill, while the accumulators fit the registers.
+// Row tiles of 16 that a workgroup takes.  us with 1, 2, 4 (64 sequences of 4096
+// positions, 8 key heads): d 128, 20 rows each: 102, 58, 140; 64 rows: 188, 110,
+// 144 (4 fill the registers: one wave a SIMD); d 64, 40 rows: 101, 81, 67; 30: 68, 45,
+// 66; d 256 (32 of 8192, 2 key heads), 24 rows: 54, 45.  Up to 16 rows one tile is enough,
+// and its weights keep a second piece.
 int row_tiles(int D, bool exact, int64_t rows) {
   if (exact || rows <= 16) return 1;
-  if (D == 256 || rows <= 32) return 2;
-  return 4;
+  return D == 64 && rows > 32 ? 4 : 2;
 }
 
 // Whether the chunk kernel takes a call: it reads keys and values once for 256
-// rows, but computes for 256 where there are fewer.  us there and here:
-//   d 128: 64 sequences of 4096 positions, 8 key heads, 68 rows each: 229, 268;
-//     36 rows: 230, 142; one of 131072 with 256 rows: 177, 255; of 16384 with 80: 42, 36
-//   d 256: 32 sequences of 8192, 2 key heads, 256 rows: 199, 241; 128 rows: 154, 125;
-//     4 sequences with 512 rows: 83, 83; one with 512: 52, 36
+// rows, but computes for 256 where there are fewer, and takes longer to begin.  us
+// there and here (sequences x rows of a key head behind 4096 positions unless said):
+//   d 64, 8 key heads: 64 x 100: 123, 128; 64 x 40: 123, 73; 8 x 100 behind 1000: 30, 34
+//   d 128, 8 key heads: 64 x 256: 307, 411; 64 x 160: 285, 276; 64 x 68: 229, 157;
+//     1 x 4096 behind 16384: 293, 306; 1 x 1024: 99, 91; 1 x 2048 behind 512: 29, 18
+//   d 256, 2 key heads, behind 8192: 32 x 256: 199, 241; 32 x 128: 154, 125; 4 x 512:
+//     83, 83; 1 x 512: 52, 36
 // (Its workgroups are the units, which have to fit a grid.)
 bool in_chunks(int D, const CacheArgs& c, int group, bool exact, int64_t rows) {
   if (exact || (c.n_tokens * group / kChunkRows + c.N) * c.heads > kMostUnits) return false;
-  return D == 256 ? rows > 128 && c.n_tokens * c.heads * group >= 4096 : rows > 64;
+  const int64_t all = c.n_tokens * c.heads * group;
+  return D == 64 ? rows > 96 : D == 128 ? rows > 160 && all >= 32768 : rows > 128 && all >= 4096;
 }
 
+// Two a CU, or one where the registers leave room for one wave a SIMD (d 256, 24 rows
+// as above: 46 us, with two 63; d 128, 64 rows, where two fit: 112, with one 139).
 int workgroups(int D, int mt) { return D / 16 * mt > 16 ? kMostWorkgroups / 2 : kMostWorkgroups; }
 
 int64_t rows_of(const CacheArgs& c, int group, int max_q) {
@@ -743,7 +750,7 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
     auto by_rows = [&](auto ib) {
       if (mt == 1) return go(d, one, f6, two, ib, true_type{});
       if (mt == 2) return go(d, two, f6, one, ib, true_type{});
-      if constexpr (kD < 256) return go(d, integral_constant<int, 4>{}, f6, one, ib, true_type{});
+      if constexpr (kD == 64) return go(d, integral_constant<int, 4>{}, f6, one, ib, true_type{});
       return hipErrorInvalidValue;
     };
     return in_bf16 ? by_rows(true_type{}) : by_rows(false_type{});

@@ -36,25 +36,25 @@ __device__ __forceinline__ void sines(const RopeArgs& r, const PairRates& p, int
 }  // namespace
 
 // Group g of lanes takes token g / runs and the run g % runs of its heads: the
-// runs of q's heads, then those of k's.  kAtOnce: heads whose loads are in flight
+// runs of q's heads, then those of k's, kRun of them, whose loads are in flight
 // together.
-template <int D, bool IN_BF16, bool OUT_BF16, bool INTER, int kAtOnce>
-__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs r, QkArgs x, int run_len, float eps) {
+template <int D, bool IN_BF16, bool OUT_BF16, bool INTER, int kRun>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs r, QkArgs x, float eps) {
   constexpr int L = D / 16;
   const int lane = threadIdx.x % L;
   const HeadRuns<D, INTER> runs(lane, r.rotary_dim);
   const PairRates rates = pair_rates<D, INTER>(r, runs);
-  const int q_runs = (x.heads[0] + run_len - 1) / run_len;
-  const int n_runs = q_runs + (x.heads[1] + run_len - 1) / run_len;
+  const int q_runs = (x.heads[0] + kRun - 1) / kRun;
+  const int n_runs = q_runs + (x.heads[1] + kRun - 1) / kRun;
   const int64_t groups = r.n_tokens * n_runs;
   for (int64_t g = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L; g < groups;
        g += static_cast<int64_t>(gridDim.x) * kThreads / L) {
     const int64_t token = g / n_runs;
     const int run = static_cast<int>(g - token * n_runs);
     const int which = run >= q_runs;
-    const int h0 = (which ? run - q_runs : run) * run_len;
+    const int h0 = (which ? run - q_runs : run) * kRun;
     const int heads = which ? x.heads[1] : x.heads[0];
-    const int h1 = h0 + run_len < heads ? h0 + run_len : heads;
+    const int h1 = h0 + kRun < heads ? h0 + kRun : heads;
     const void* from = which ? x.in[1] : x.in[0];
     void* to = which ? x.out[1] : x.out[0];
     const float* w = which ? x.w[1] : x.w[0];
@@ -66,43 +66,43 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs r, QkAr
       load_n<false, 8>(w, runs.a, wa);
       load_n<false, 8>(w, runs.b, wb);
     }
-    for (int h = h0; h < h1; h += kAtOnce) {
-      float a[kAtOnce][8], b[kAtOnce][8];
+    float a[kRun][8], b[kRun][8];
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const size_t at = in0 + static_cast<size_t>(h + i < h1 ? h + i : h1 - 1) * D;
-        load_n<IN_BF16, 8>(from, at + runs.a, a[i]);
-        load_n<IN_BF16, 8>(from, at + runs.b, b[i]);
-      }
+    for (int i = 0; i < kRun; ++i) {
+      const size_t at = in0 + static_cast<size_t>(h0 + i < h1 ? h0 + i : h1 - 1) * D;
+      load_n<IN_BF16, 8>(from, at + runs.a, a[i]);
+      load_n<IN_BF16, 8>(from, at + runs.b, b[i]);
+    }
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        if (h + i >= h1) break;
-        if (w) {
-          float ss = 0.f;
+    for (int i = 0; i < kRun; ++i) {
+      if (h0 + i >= h1) break;
+      if (w) {
+        float ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(a[i][e], a[i][e], fmaf(b[i][e], b[i][e], ss));
-          const float inv = rsqrt_precise(dpp_group_sum<L>(ss) * (1.0f / D) + eps);
+        for (int e = 0; e < 8; ++e) ss = fmaf(a[i][e], a[i][e], fmaf(b[i][e], b[i][e], ss));
+        const float inv = rsqrt_precise(dpp_group_sum<L>(ss) * (1.0f / D) + eps);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[i][e] *= inv * wa[e];
-            b[i][e] *= inv * wb[e];
-          }
+        for (int e = 0; e < 8; ++e) {
+          a[i][e] *= inv * wa[e];
+          b[i][e] *= inv * wb[e];
         }
-        rotate<D, INTER>(runs, a[i], b[i], c, s);
-        const size_t at = out0 + static_cast<size_t>(h + i) * D;
-        store_n<OUT_BF16, 8>(to, at + runs.a, a[i]);
-        store_n<OUT_BF16, 8>(to, at + runs.b, b[i]);
       }
+      rotate<D, INTER>(runs, a[i], b[i], c, s);
+      const size_t at = out0 + static_cast<size_t>(h0 + i) * D;
+      store_n<OUT_BF16, 8>(to, at + runs.a, a[i]);
+      store_n<OUT_BF16, 8>(to, at + runs.b, b[i]);
     }
   }
 }
 
-// Groups take tokens and runs of heads as above, first all of q's and then all
-// of k's; a lane keeps its channels, so both weights' gradients gather in its
-// registers.  A workgroup joins its lanes in LDS and leaves one row of `part`,
-// [2][D].  Groups and the order of every sum depend on the sizes alone.
-template <int D, bool IN_BF16, bool OUT_BF16, bool INTER, int kPair>
-__global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, QkArgs x, int run_len, float eps,
+// Groups take a token's head at a time, first all of q's and then all of k's; a
+// lane keeps its channels, so both weights' gradients gather in its registers.  A
+// workgroup joins its lanes in LDS and leaves one row of `part`, [2][D].  Groups and
+// the order of every sum depend on the sizes alone.  (Runs of four heads whose sines
+// are formed once, with two heads' loads in flight, took 140 to 142 us where this
+// takes 124 to 138: 16384 tokens, 16 + 2 heads of 256 or 32 + 8 of 128.)
+template <int D, bool IN_BF16, bool OUT_BF16, bool INTER>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, QkArgs x, float eps,
                                                                     float* __restrict__ part) {
   constexpr int L = D / 16;
   __shared__ float red[4][kThreads][8];   // q's and k's weight, the two runs of each
@@ -118,61 +118,46 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, 
       load_n<false, 8>(w, runs.b, wb);
     }
     const int heads = x.heads[which];
-    const int n_runs = (heads + run_len - 1) / run_len;
-    const int64_t groups = r.n_tokens * n_runs;
+    const int64_t groups = r.n_tokens * heads;
     for (int64_t g = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L; g < groups;
          g += static_cast<int64_t>(gridDim.x) * kThreads / L) {
-      const int64_t token = g / n_runs;
-      const int h0 = static_cast<int>(g - token * n_runs) * run_len;
-      const int h1 = h0 + run_len < heads ? h0 + run_len : heads;
-      const size_t in0 = static_cast<size_t>(token) * x.stride[which];
-      const size_t out0 = static_cast<size_t>(token) * heads * D;
-      float c[8], s[8];
+      const int64_t token = g / heads;
+      const size_t in = static_cast<size_t>(token) * x.stride[which] + static_cast<size_t>(g - token * heads) * D;
+      const size_t out = static_cast<size_t>(g) * D;
+      float a[8], b[8], ga[8], gb[8];
+      load_n<IN_BF16, 8, true>(x.in[which], in + runs.a, a);
+      load_n<IN_BF16, 8, true>(x.in[which], in + runs.b, b);
+      load_n<OUT_BF16, 8, true>(x.dy[which], out + runs.a, ga);
+      load_n<OUT_BF16, 8, true>(x.dy[which], out + runs.b, gb);
       if (r.rotary_dim) {
+        float c[8], s[8];
         sines<D, INTER>(r, rates, token, c, s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = -s[e];   // back
+        rotate<D, INTER>(runs, ga, gb, c, s);
       }
-      for (int h = h0; h < h1; h += kPair) {
-        float a[kPair][8], b[kPair][8], ga[kPair][8], gb[kPair][8];
+      if (w) {
+        float ss = 0.f, sg = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPair; ++i) {
-          const int hi = h + i < h1 ? h + i : h1 - 1;
-          const size_t in = in0 + static_cast<size_t>(hi) * D, out = out0 + static_cast<size_t>(hi) * D;
-          load_n<IN_BF16, 8, true>(x.in[which], in + runs.a, a[i]);
-          load_n<IN_BF16, 8, true>(x.in[which], in + runs.b, b[i]);
-          load_n<OUT_BF16, 8, true>(x.dy[which], out + runs.a, ga[i]);
-          load_n<OUT_BF16, 8, true>(x.dy[which], out + runs.b, gb[i]);
+        for (int e = 0; e < 8; ++e) {
+          ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+          sg = fmaf(ga[e] * wa[e], a[e], fmaf(gb[e] * wb[e], b[e], sg));
         }
+        ss = dpp_group_sum<L>(ss);
+        sg = dpp_group_sum<L>(sg);
+        const float inv = rsqrt_precise(ss * (1.0f / D) + eps);
+        // n * mean(u n) = x * k; 0 where the squares pass fp32's range, as n is
+        const float k = inv == 0.f ? 0.f : sg * (1.0f / D) * inv * inv;
 #pragma unroll
-        for (int i = 0; i < kPair; ++i) {
-          if (h + i >= h1) break;
-          rotate<D, INTER>(runs, ga[i], gb[i], c, s);
-          if (w) {
-            float ss = 0.f, sg = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              ss = fmaf(a[i][e], a[i][e], fmaf(b[i][e], b[i][e], ss));
-              sg = fmaf(ga[i][e] * wa[e], a[i][e], fmaf(gb[i][e] * wb[e], b[i][e], sg));
-            }
-            ss = dpp_group_sum<L>(ss);
-            sg = dpp_group_sum<L>(sg);
-            const float inv = rsqrt_precise(ss * (1.0f / D) + eps);
-            // n * mean(u n) = x * k; 0 where the squares pass fp32's range, as n is
-            const float k = inv == 0.f ? 0.f : sg * (1.0f / D) * inv * inv;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              da[e] = fmaf(ga[i][e], a[i][e] * inv, da[e]);
-              db[e] = fmaf(gb[i][e], b[i][e] * inv, db[e]);
-              ga[i][e] = inv * fmaf(-a[i][e], k, ga[i][e] * wa[e]);
-              gb[i][e] = inv * fmaf(-b[i][e], k, gb[i][e] * wb[e]);
-            }
-          }
-          const size_t at = out0 + static_cast<size_t>(h + i) * D;
-          store_n<false, 8>(x.out[which], at + runs.a, ga[i]);
-          store_n<false, 8>(x.out[which], at + runs.b, gb[i]);
+        for (int e = 0; e < 8; ++e) {
+          da[e] = fmaf(ga[e], a[e] * inv, da[e]);
+          db[e] = fmaf(gb[e], b[e] * inv, db[e]);
+          ga[e] = inv * fmaf(-a[e], k, ga[e] * wa[e]);
+          gb[e] = inv * fmaf(-b[e], k, gb[e] * wb[e]);
         }
       }
+      store_n<false, 8>(x.out[which], out + runs.a, ga);
+      store_n<false, 8>(x.out[which], out + runs.b, gb);
     }
     store_n<false, 8>(&red[2 * which][threadIdx.x][0], 0, da);
     store_n<false, 8>(&red[2 * which + 1][threadIdx.x][0], 0, db);
@@ -192,13 +177,6 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, 
 }
 
 namespace {
-
-// Heads of a group's run: one while the groups are few (latency), then as many
-// as leave 8192 waves, 8 at most (the sines are formed once a run).
-int run_length(int D, int64_t n, int heads) {
-  const int64_t waves = n * heads * (D / 16) / 64;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, waves / 8192)));
-}
 
 template <class F>
 hipError_t with_shape(int D, bool in_bf16, bool out_bf16, bool inter, F&& f) {
@@ -223,22 +201,24 @@ hipError_t with_shape(int D, bool in_bf16, bool out_bf16, bool inter, F&& f) {
   }
 }
 
-int64_t groups_of(const QkArgs& x, int64_t n, int run) {
-  return n * ((x.heads[0] + run - 1) / run + (x.heads[1] + run - 1) / run);
-}
-
 }  // namespace
 
+// Four heads a group from 4096 waves of one head on (the sines are formed once,
+// and four heads' loads are in flight): 2000 tokens, 40 heads of 128: 11.1 us, with
+// one 15.0; 16384 tokens: 64, 75.  Below, latency counts: one token, 16 + 2 heads of
+// 256: 7.2, with one 6.3.
 hipError_t launch_qk_norm_rope(int D, const RopeArgs& r, const QkArgs& x, float eps, bool in_bf16, bool out_bf16,
                                hipStream_t st) {
-  const int run = run_length(D, r.n_tokens, x.heads[0] + x.heads[1]);
-  const int64_t blocks = (groups_of(x, r.n_tokens, run) * (D / 16) + kThreads - 1) / kThreads;
+  const int64_t lanes = r.n_tokens * (x.heads[0] + x.heads[1]) * (D / 16);
+  const int run = lanes / 64 >= 4096 ? 4 : 1;
+  const int64_t groups = r.n_tokens * ((x.heads[0] + run - 1) / run + (x.heads[1] + run - 1) / run);
+  const int64_t blocks = (groups * (D / 16) + kThreads - 1) / kThreads;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 256 * 16)));
   return with_shape(D, in_bf16, out_bf16, r.interleaved, [&](auto d, auto ib, auto ob, auto inter) {
     constexpr int kD = decltype(d)::value;
     constexpr bool kIn = decltype(ib)::value, kOut = decltype(ob)::value, kInter = decltype(inter)::value;
-    if (run == 1) qk_norm_rope_kernel<kD, kIn, kOut, kInter, 1><<<grid, kThreads, 0, st>>>(r, x, run, eps);
-    else qk_norm_rope_kernel<kD, kIn, kOut, kInter, 4><<<grid, kThreads, 0, st>>>(r, x, run, eps);
+    if (run == 1) qk_norm_rope_kernel<kD, kIn, kOut, kInter, 1><<<grid, kThreads, 0, st>>>(r, x, eps);
+    else qk_norm_rope_kernel<kD, kIn, kOut, kInter, 4><<<grid, kThreads, 0, st>>>(r, x, eps);
   });
 }
 
@@ -252,12 +232,9 @@ hipError_t launch_qk_norm_rope_bwd(int D, const RopeArgs& r, const QkArgs& x, fl
                                    bool in_bf16, bool out_bf16, hipStream_t st) {
   const int parts = qk_norm_rope_bwd_parts(D, r.n_tokens, x.heads[0] + x.heads[1]);
   if (parts > 0) {
-    const int run = run_length(D, r.n_tokens, x.heads[0] + x.heads[1]);
     const hipError_t e = with_shape(D, in_bf16, out_bf16, r.interleaved, [&](auto d, auto ib, auto ob, auto inter) {
-      constexpr int kD = decltype(d)::value;
-      constexpr bool kIn = decltype(ib)::value, kOut = decltype(ob)::value, kInter = decltype(inter)::value;
-      if (run == 1) qk_norm_rope_bwd_kernel<kD, kIn, kOut, kInter, 1><<<dim3(parts), kThreads, 0, st>>>(r, x, run, eps, part);
-      else qk_norm_rope_bwd_kernel<kD, kIn, kOut, kInter, 2><<<dim3(parts), kThreads, 0, st>>>(r, x, run, eps, part);
+      qk_norm_rope_bwd_kernel<decltype(d)::value, decltype(ib)::value, decltype(ob)::value, decltype(inter)::value>
+          <<<dim3(parts), kThreads, 0, st>>>(r, x, eps, part);
     });
     if (e != hipSuccess) return e;
   }

@@ -12,8 +12,26 @@ from tests.test_gpu_rope import kda, make_cfg, make_rope  # noqa: F401  (fixture
 pytestmark = pytest.mark.gpu
 
 
-def attend(kda, b, group, io=BF, out=BF, scale=None, every=1, **args):  # noqa: F811
-    """The call, its every'th sequence checked."""
+class Some:
+    """Some sequences and key heads of a batch, for a check."""
+
+    def __init__(self, b, every=1, heads=None):
+        self.b, self.cu = b, b.cu
+        self.seqs = [(t, n) if i % every == 0 else (0, n) for i, (t, n) in enumerate(b.seqs)]
+        self.of = range(b.heads) if heads is None else [h for h in heads if h < b.heads]
+        self.heads = len(self.of)
+
+    def held(self, i):
+        return [x[list(self.of)] for x in self.b.held(i)]
+
+    def check(self, o, lse, q, scale, max_q=0):
+        group = q.shape[1] // self.b.heads
+        rows = [h * group + x for h in self.of for x in range(group)]
+        check_attention(o[:, rows], None if lse is None else lse[:, rows], self, q[:, rows], scale, max_q)
+
+
+def attend(kda, b, group, io=BF, out=BF, scale=None, every=1, heads=None, **args):  # noqa: F811
+    """The call, every'th sequence and the heads given of it checked."""
     b.fill()
     q = Rand(3)(b.n, b.heads * group, b.d, dtype=io, scale=2)
     o, ok = guarded(q.shape, out)
@@ -21,41 +39,41 @@ def attend(kda, b, group, io=BF, out=BF, scale=None, every=1, **args):  # noqa: 
     cfg = make_cfg(kda, b.heads * group, b.d, io, out)
     kda.kda_paged_attention(cfg, b.cache, q, *b.where, scale, o=o, lse=lse, **args)
     assert ok() and ok2()
-    b.seqs = [(t, n) if i % every == 0 else (0, n) for i, (t, n) in enumerate(b.seqs)]
-    check_attention(o, lse, b, q, b.d ** -0.5 if scale is None else scale, args.get("max_q", 0))
+    Some(b, every, heads).check(o, lse, q, b.d ** -0.5 if scale is None else scale, args.get("max_q", 0))
 
 
-@pytest.mark.parametrize("d,tokens", [(64, 70), (128, 70), (256, 140)])
+@pytest.mark.parametrize("d,tokens", [(64, 100), (128, 170), (256, 140)])
 @pytest.mark.parametrize("io", [BF, F32])
 def test_more_tiles_than_units_of_the_card(kda, d, tokens, io):  # noqa: F811
     """So many that none is split, of ragged lengths, empty ones among them."""
     seqs = [(tokens - i % 3, tokens + i) if i % 5 else (i % 2, 0) for i in range(40)]
-    attend(kda, Batch(kda, seqs, 8, d, 64), 1, io, every=6, max_q=tokens)
+    attend(kda, Batch(kda, seqs, 8, d, 64), 1, io, every=6, heads=(0, 3, 7), max_q=tokens)
 
 
-@pytest.mark.parametrize("d,group", [(64, 4), (128, 8), (256, 16)])
-def test_a_table_with_room_for_more(kda, d, group):  # noqa: F811
+@pytest.mark.parametrize("d,heads,group", [(64, 1, 4), (128, 5, 24), (256, 1, 16)])
+def test_a_table_with_room_for_more(kda, d, heads, group):  # noqa: F811
     """The split goes by the table's room; sequences far shorter than it have fewer parts, or one; rows that see nothing."""
-    attend(kda, Batch(kda, [(90, 1500), (70, 71), (33, 0), (80, 50), (20, 300)], 1, d, 32, extra=300), group, max_q=90)
+    seqs = [(90, 1500), (70, 71), (33, 0), (80, 50), (20, 300)]
+    attend(kda, Batch(kda, seqs, heads, d, 32, extra=600), group, heads=(0, 4), max_q=90)
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("d,heads", [(64, 1), (128, 129), (256, 17)])
 @pytest.mark.parametrize("rows", [255, 256, 257, 300, 513])
-def test_rows_around_a_tile(kda, d, rows):  # noqa: F811
-    heads = 17 if d == 256 else 1
-    attend(kda, Batch(kda, [(rows, rows + 190)], heads, d, 64), 1, max_q=rows)
-    attend(kda, Batch(kda, [(rows, rows)], heads, d, 256), 1, max_q=0)
+def test_rows_around_a_tile(kda, d, heads, rows):  # noqa: F811
+    attend(kda, Batch(kda, [(rows, rows + 190)], heads, d, 64), 1, heads=(0, 5, 128), max_q=rows)
+    attend(kda, Batch(kda, [(rows, rows)], heads, d, 256), 1, heads=(0, 16), max_q=0)
 
 
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 0.5])
 def test_scales(kda, scale):  # noqa: F811
-    attend(kda, Batch(kda, [(90, 400)], 2, 128, 64), 1, scale=scale)
+    attend(kda, Batch(kda, [(90, 400)], 128, 128, 64), 4, scale=scale, heads=(0, 127))
+    attend(kda, Batch(kda, [(90, 400)], 2, 64, 64), 4, scale=scale)
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
-def test_pages_that_are_not_held(kda, d):  # noqa: F811
+@pytest.mark.parametrize("d,heads", [(64, 2), (128, 5), (256, 2)])
+def test_pages_that_are_not_held(kda, d, heads):  # noqa: F811
     """As for single tokens: their positions are left out, a length beyond the table counts to its end."""
-    heads, tokens = 2, 160
+    tokens = 160
     b = Batch(kda, [(tokens, 700), (tokens, 700), (tokens, 512)], heads, d, 64)
     b.fill()
     q = Rand(3)(b.n, 16 * heads, d, dtype=BF)
@@ -77,10 +95,10 @@ def test_pages_that_are_not_held(kda, d):  # noqa: F811
         check(o[2 * tokens + j][None].cpu(), e, m, ref.attention_rel(d, 512, top, BF, BF, 0)[0])
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
-def test_what_is_not_seen_has_no_effect(kda, d):  # noqa: F811
+@pytest.mark.parametrize("d,heads", [(64, 2), (128, 8), (256, 2)])
+def test_what_is_not_seen_has_no_effect(kda, d, heads):  # noqa: F811
     """NaN behind the lengths, in pages of no one and at later tokens; and one that is seen reaches those that see it."""
-    tokens, heads, group = 140, 2, 16
+    tokens, group = 140, 16
     b = Batch(kda, [(tokens, 450), (tokens, 140)], heads, d, 64, seed=2)
     b.fill()
     q = Rand(7)(b.n, heads * group, d, dtype=BF)
@@ -102,7 +120,8 @@ def test_what_is_not_seen_has_no_effect(kda, d):  # noqa: F811
             p, first = run(), at - (450 - tokens)
             assert torch.equal(p[:first], o[:first]) and torch.equal(p[tokens:], o[tokens:])
             assert torch.equal(p[first:tokens, :group], o[first:tokens, :group])
-            bad = p[first:tokens, group:].isnan()
+            assert torch.equal(p[first:tokens, 2 * group:], o[first:tokens, 2 * group:])
+            bad = p[first:tokens, group:2 * group].isnan()
             assert bad.all() if s is b.cache.k_scale else (bad[..., 32:64].all() and not bad[..., :32].any()
                                                            and not bad[..., 64:].any())
             s.copy_(keep)
@@ -119,22 +138,22 @@ def test_the_most_sequences(kda, io, out, max_q):  # noqa: F811
 def test_max_q_that_was_too_small(kda):  # noqa: F811
     """Only the choice of the kernel goes by it."""
     attend(kda, Batch(kda, [(70, 200), (1, 300), (5, 5)], 2, 128, 64), 2, max_q=1)
-    b = Batch(kda, [(150, 200), (150, 300), (150, 150)], 2, 64, 64)
-    attend(kda, b, 1, max_q=70)
+    b = Batch(kda, [(250, 300), (250, 400), (250, 250)], 2, 64, 64)
+    attend(kda, b, 1, max_q=100)
 
 
 def test_streams_and_graphs(kda):  # noqa: F811
     """The same bits on another stream and with rows behind the last sequence; two captured calls that share a workspace,
     one of them split and one not, replayed in turn while the lengths grow."""
-    d, heads, group = 128, 2, 2
-    b = Batch(kda, [(80, 700), (100, 2000)], heads, d, 64, extra=4)
+    d, heads, group = 128, 8, 24
+    b = Batch(kda, [(80, 700), (100, 2000)], heads, d, 64, extra=200)
     b.fill()
     cfg = make_cfg(kda, heads * group, d)
     q = Rand(5)(b.n + 7, heads * group, d, dtype=BF)
     o = torch.full_like(q, 7.0)
     kda.kda_paged_attention(cfg, b.cache, q, *b.where, max_q=100, o=o)
     assert (o[b.n:] == 7).all()
-    check_attention(o, None, b, q, d ** -0.5, 100)
+    Some(b, 2, (0,)).check(o, None, q, d ** -0.5, 100)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     s = kda.kda_paged_attention(cfg, b.cache, q, *b.where, max_q=100, stream=side)
@@ -186,12 +205,12 @@ def test_far_in_a_large_cache(kda):  # noqa: F811
     check_attention(kda.kda_paged_attention(cfg, far, q, b.cu, table, b.lengths), None, b, q, d ** -0.5)
 
 
-@pytest.mark.parametrize("tokens", [1, 80])
+@pytest.mark.parametrize("tokens", [1, 110])
 def test_sequences_that_share_pages(kda, tokens):  # noqa: F811
     """A prefix held once, and one page twice in a sequence."""
-    b = Batch(kda, [(tokens, 400), (tokens, 333), (tokens, 400)], 2, 128, 32)
+    b = Batch(kda, [(tokens, 400), (tokens, 333), (tokens, 400)], 2, 64, 32)
     b.fill()
     b.table[1, :7], b.table[2, 5] = b.table[0, :7], b.table[2, 1]
-    q = Rand(3)(b.n, 4, 128, dtype=BF)
-    o = kda.kda_paged_attention(make_cfg(kda, 4, 128), b.cache, q, *b.where, max_q=tokens)
-    check_attention(o, None, b, q, 128 ** -0.5, tokens)
+    q = Rand(3)(b.n, 4, 64, dtype=BF)
+    o = kda.kda_paged_attention(make_cfg(kda, 4, 64), b.cache, q, *b.where, max_q=tokens)
+    check_attention(o, None, b, q, 64 ** -0.5, tokens)
