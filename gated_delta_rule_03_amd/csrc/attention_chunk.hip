@@ -6,9 +6,10 @@
 // query heads of one key head) and walks the positions in blocks.  Everything
 // comes through LDS: keys and values go there from memory as they are, without
 // registers, three and four blocks ahead (all workgroups of an XCD touch a block
-// for the first time together, so a block's bytes come from far away); while a block is worked on, some of the
-// lanes widen the next one's values to bf16 and leave them in the order in which
-// the matrix cores' operands read them; one barrier a block.  Keys need no
+// for the first time together, so a block's bytes come from far away); while a
+// block is worked on, some of the lanes widen the next one's values to bf16 and
+// leave them in the order in which the matrix cores' operands read them; one
+// barrier a block.  Keys need no
 // widening: they are 4-bit operands of the 32x32x64 step, against the queries'
 // three 6-bit pieces (attention.h).  16-byte pieces of neighbouring keys lie
 // permuted, so that eight lanes' reads have no bank conflict.
@@ -18,7 +19,8 @@
 // 8 / NC of tile c's row r is r * NC + c (NC = D / 32 tiles): what a lane widens,
 // 8 neighbouring channels of 8 positions, then goes to 8 neighbouring rows' or
 // tiles' places.  Two waves a SIMD, so that one's softmax runs under the other's
-// products.
+// products.  Two chunks of 2048 tokens behind 16384 positions, 16 query heads on 2
+// key heads of 256: 904 us, 1.14 PFLOP/s; 32 on 8 of 128: 1.02; of 64: 0.86.
 //
 // A workgroup takes one (sequence, key head, row tile), the last tiles (which
 // see the most) first, or one of up to `splits` equal parts of its positions
@@ -144,14 +146,18 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   });
   if (splits > 1 && threadIdx.x == 0)   // (those that there are: by their first part)
     for (int64_t i = static_cast<int64_t>(before[c.N]) * c.heads + blockIdx.x; i < units; i += gridDim.x) joins[i].pieces = 0;
-  // the workgroup's unit and part: neighbouring ones on one XCD, which then share
-  // keys and values in its cache, each XCD its share of those there are
+  // the workgroup's unit and part.  Workgroups go to the XCDs in turn, and a
+  // sequence's units are numbered head by head, the last tiles (which see the most)
+  // of all heads first: an XCD has few heads, whose keys and values its workgroups
+  // share in its cache, as much to do as the others, and its short units at the end
+  // (one chunk of 8192 tokens, 2 key heads of 256: 505 us, with an eighth of the line
+  // of heads and tiles to each XCD 817; 8 of 128: 588 us, with the tiles of one head
+  // after the other over all XCDs 790).
   const int64_t there = static_cast<int64_t>(before[c.N]) * c.heads;
-  const int all = uniform(static_cast<int>(there < units ? there : units)) * splits;
-  const int per_xcd = (all + 7) >> 3;
-  const int place = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if (static_cast<int>(blockIdx.x >> 3) >= per_xcd || place >= all) return;
-  const int id = uniform(place / splits), part = place - id * splits;
+  const int n_units = uniform(static_cast<int>(there < units ? there : units));
+  const int place = blockIdx.x;
+  if (place >= n_units * splits) return;
+  const int part = uniform(place / n_units), id = uniform(place - part * n_units);
   int n = 0;
   for (int hi = c.N; hi - n > 1;) {   // the last with its tiles' first unit <= id
     const int mid = (n + hi) >> 1;
@@ -163,7 +169,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   const int rows = s.tokens * group;
   const int tiles = (rows + kRows - 1) / kRows;
   const int local = uniform(static_cast<int>(id - static_cast<int64_t>(before[n]) * c.heads));
-  const int head = uniform(local / tiles), tile = tiles - 1 - (local - head * tiles);
+  const int turn = uniform(local / c.heads), head = local - turn * c.heads, tile = tiles - 1 - turn;
   __syncthreads();   // (sm.wide held lay_out's sums)
 
   auto seen = [&](int row) {   // positions that a row sees
