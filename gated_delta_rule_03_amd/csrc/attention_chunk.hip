@@ -91,6 +91,9 @@ struct Pages {
     const int a = uniform(x0), b = uniform(x1), c = uniform(x2), d = uniform(x3);
     return step < 2 ? (step == 0 ? a : b) : (step == 2 ? c : d);
   }
+  __device__ __forceinline__ bool any_missing(int steps) const {
+    return uniform(steps == 2 ? x0 | x1 : x0 | x1 | x2 | x3) < 0;
+  }
 };
 
 // What a kernel of D channels keeps in LDS.
@@ -268,7 +271,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
 
   // values: a lane widens 8 neighbouring channels (a word) of the 8 positions
   // 16 u + 4 h + {0 .. 3, 8 .. 11} of one step
-  auto widen_words = [&](int b, int from_buf, int buf, int task_wave) {
+  auto widen_words = [&](const Pages& p, int b, int from_buf, int buf, int task_wave) {
     const int l = lane_anew();
     const int task = task_wave * 64 + l;
     const int step = task / S::kTaskLanes, in = task % S::kTaskLanes;
@@ -277,7 +280,8 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
     const uint8_t* words = sm.v[from_buf] + first * S::kRowBytes + col * 4;
     const uint8_t* scales = sm.vs[from_buf] + (col / 4) * S::kPos + first;
     uint8_t* const to = sm.wide[buf] + step * (kStep * D * 2) + (tu * 64 + th * 32) * 16;
-    const bool wary = static_cast<uint32_t>(b + 1) * S::kPos > least_all;
+    // (a page that is not held stands for page 0, whose bytes its weights of 0 meet)
+    const bool wary = static_cast<uint32_t>(b + 1) * S::kPos > least_all || p.any_missing(S::kSteps);
     bool bad = false;
     // kEach positions at a time: with 256 channels all 8 would not fit the registers beside the sums and the queries
     constexpr int kEach = D == 256 ? 4 : 8;
@@ -353,7 +357,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
       fetch(p4, b + 4, false, raw);
       const Pages p5 = pages_of(b + 5);
       const int task_wave = (wave + 4 * buf) & (W - 1);   // the other half of the waves each time
-      if (b + 1 >= b0 && b + 1 < b1 && task_wave < S::kTaskWaves) widen_words(b + 1, (raw + 1) & 3, buf ^ 1, task_wave);
+      if (b + 1 >= b0 && b + 1 < b1 && task_wave < S::kTaskWaves) widen_words(p1, b + 1, (raw + 1) & 3, buf ^ 1, task_wave);
 #pragma unroll 1
       for (int step = b < b0 ? S::kSteps : 0; step < S::kSteps; step += S::kAtOnce) {
         const uint32_t at = static_cast<uint32_t>(b) * S::kPos + step * kStep;

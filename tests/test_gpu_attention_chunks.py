@@ -214,3 +214,24 @@ def test_sequences_that_share_pages(kda, tokens):  # noqa: F811
     q = Rand(3)(b.n, 4, 64, dtype=BF)
     o = kda.kda_paged_attention(make_cfg(kda, 4, 64), b.cache, q, *b.where, max_q=tokens)
     check_attention(o, None, b, q, 64 ** -0.5, tokens)
+
+
+@pytest.mark.parametrize("d,heads", [(64, 2), (128, 16), (256, 2)])
+def test_missing_pages_beside_held_ones(kda, d, heads):  # noqa: F811
+    """Every third page of 32 positions is missing; NaN in all pages of no one, the first among them, has no effect."""
+    tokens = 160
+    b = next(b for b in (Batch(kda, [(tokens, 900)], heads, d, 32, seed=s) for s in range(50)) if not (b.table == 0).any())
+    b.fill()
+    q = Rand(3)(b.n, 16 * heads, d, dtype=BF)
+    k, v = b.held(0)
+    b.table[0, 1::3] = -1
+    others = [p for p in range(b.cache.k.shape[0]) if p not in b.table[0].tolist()]
+    assert 0 in others
+    b.cache.k_scale[others], b.cache.v_scale[others] = 255, 255
+    o, ok = guarded(q.shape, BF)
+    kda.kda_paged_attention(make_cfg(kda, 16 * heads, d), b.cache, q, *b.where, o=o, max_q=tokens)
+    assert ok()
+    for j in (0, 31, tokens - 1):
+        keep = torch.tensor([p for p in range(900 - tokens + j + 1) if p // 32 % 3 != 1])
+        e, _, m, top = ref.attention(q[j:j + 1].double().cpu(), k[:, keep], v[:, keep], len(keep), d ** -0.5)
+        check(o[j:j + 1].cpu(), e, m, ref.attention_rel(d, 900, top, BF, BF, 0)[0])
