@@ -558,7 +558,7 @@ hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int 
   const int parts = parts_of(D, c, units_by(c, group, max_rows));
   Split* joins = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(joins + units);
-  const dim3 grid(static_cast<unsigned>((units * parts + 7) / 8 * 8));
+  const dim3 grid(static_cast<unsigned>(units * parts));
   const size_t shared = (static_cast<size_t>(c.N) + 1) * 4;
   auto go = [&](auto d, auto ib) {
     constexpr int kD = decltype(d)::value;
