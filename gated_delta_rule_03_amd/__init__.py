@@ -724,7 +724,10 @@ class Rope:
         n, dev = self.inv_freq.numel(), self.inv_freq.device
         c = KdaRopeC(2 * n, int(self.interleaved), _int32(self.num_axes), _at("inv_freq", self.inv_freq, (n,), torch.float32, dev),
                      _at("axis", self.axis, (n,), torch.int32, dev))
-        object.__setattr__(self, "_c", c)     # (frozen: the tensors it points to stay)
+        # (frozen: the tensors it points to stay)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+        object.__setattr__(self, "_device", dev)
 
     @classmethod
     def build(cls, rotary_dim: int, theta: float = 10000.0, sections=None, interleaved: bool = False, device="cuda"):
@@ -802,11 +805,10 @@ def _rope_at(rope, positions, n, device):
     """(pointer to the struct or None, address of the positions)."""
     if rope is None:
         return None, None
-    if rope.inv_freq.device != device:
+    if rope._device != device:
         raise ValueError(f"rope must be on {device}")
-    if positions is not None and positions.dim() == 1 and rope.num_axes == 1:
-        positions = positions[None]
-    return ctypes.byref(rope._c), _at("positions", positions, (rope.num_axes, n), torch.int32, device)
+    shape = (n,) if rope.num_axes == 1 and positions is not None and positions.dim() == 1 else (rope.num_axes, n)
+    return rope._ref, _at("positions", positions, shape, torch.int32, device)
 
 
 def kda_qk_norm_rope(cfg: Config, rope: Optional[Rope], q, k, q_weight=None, k_weight=None, positions=None,
