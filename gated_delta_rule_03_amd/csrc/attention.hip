@@ -538,14 +538,17 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
 
 // Joins the pieces of units: PARTS: of the chunk kernel's, of `stride` places each;
 // otherwise of those that began in one of the `units` workgroups of the kernel
-// above.  A wave takes a row, eight pieces of it in flight, or four waves do where
+// above.  A wave takes a row, eight pieces of it in flight, or kWide waves do where
 // there are more than eight; the workgroups take the units of few pieces by their
-// own number, and find those of many by a count over all.
+// own number, and find those of many by a count over all.  us with 4, 8, 16 waves:
+// one row tile of 16384 positions, 2 key heads of 256: 9.3, 6.4, 5.9; 256 sequences
+// at 8192 (few pieces): 4.8, 4.8, 5.6; parts of 4 x 512 rows at 8192: 16.4, 23.3, -.
 template <int D, int ROWS, bool OUT_BF16, bool PARTS>
 __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group, void* __restrict__ o,
                                                            float* __restrict__ lse, const Split* __restrict__ splits,
                                                            const float* __restrict__ pieces, int units, int stride) {
   constexpr int E = D / 64, kTogether = 8;   // channels of a lane; pieces whose loads are in flight
+  constexpr int kWide = PARTS ? 4 : 8;         // waves of a row of many pieces
   __shared__ float meet[16][64][E], tops[16][2];
   __shared__ int counts[16], list[PARTS ? 1 : kMostWorkgroups];
   const int wave = uniform(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
@@ -598,16 +601,16 @@ __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group,
       }
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, tops[(wave & 12) + k][0]);
+      for (int k = 0; k < kWide; ++k) top = fmaxf(top, tops[(wave & ~(kWide - 1)) + k][0]);
       l = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float m = tops[(wave & 12) + k][0], f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-        l = fmaf(f, tops[(wave & 12) + k][1], l);
+      for (int k = 0; k < kWide; ++k) {
+        const float m = tops[(wave & ~(kWide - 1)) + k][0], f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        l = fmaf(f, tops[(wave & ~(kWide - 1)) + k][1], l);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(f, meet[(wave & 12) + k][lane][e], x[e]);
+        for (int e = 0; e < E; ++e) x[e] = fmaf(f, meet[(wave & ~(kWide - 1)) + k][lane][e], x[e]);
       }
       __syncthreads();
     }
@@ -621,14 +624,14 @@ __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group,
     }
   };
 
-  constexpr int kFew = ROWS / 16, kMany = ROWS / 4;   // a unit's jobs
+  constexpr int kFew = ROWS / 16, kMany = ROWS * kWide / 16;   // a unit's jobs
   if constexpr (PARTS) {
     const bool many = stride > kTogether;
     const int jobs = many ? kMany : kFew;
     for (int job = blockIdx.x; job < units * jobs; job += gridDim.x) {
       const int unit = job / jobs, own = job - unit * jobs;
       if (splits[unit].pieces == 0) continue;
-      if (many) join(unit, own * 4 + (wave >> 2), wave & 3, 4);
+      if (many) join(unit, own * (16 / kWide) + wave / kWide, wave % kWide, kWide);
       else join(unit, own * 16 + wave, 0, 1);
     }
   } else {
@@ -652,7 +655,7 @@ __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group,
     __syncthreads();
     todo = uniform(todo) * kMany;
     for (int job = blockIdx.x; job < todo; job += gridDim.x)
-      join(uniform(list[job / kMany]), job % kMany * 4 + (wave >> 2), wave & 3, 4);
+      join(uniform(list[job / kMany]), job % kMany * (16 / kWide) + wave / kWide, wave % kWide, kWide);
   }
 }
 
