@@ -23,7 +23,14 @@ __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u)
 struct Sequence {
   int first;          // its first row of q
   int tokens;         // new tokens
-  int length;         // positions held
+  int length;         // positions held: of its length, those that the table has room for
+  int base;           // positions of its length in front of the new tokens; below 0: that many tokens see nothing
+
+  // Positions that new token j sees.  (The limit comes from the length as given: beyond the table a token sees what is held.)
+  __device__ __forceinline__ uint32_t seen(int j) const {
+    const int x = base + j + 1;   // at most the length as given, since j is below the number of tokens
+    return static_cast<uint32_t>(x < 0 ? 0 : x < length ? x : length);
+  }
 };
 
 // A value that is the same in every lane, as the compiler cannot see.
@@ -42,6 +49,7 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& c, int n) {
   const int64_t most = static_cast<int64_t>(c.max_pages) << c.page_shift;
   const int len = c.lengths[n];
   s.length = len < 0 ? 0 : len < most ? len : static_cast<int>(most);
+  s.base = static_cast<int>((len < 0 ? 0 : len) - (end - s.first));
   return s;
 }
 

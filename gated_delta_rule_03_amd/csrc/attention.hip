@@ -412,10 +412,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
     // this lane's rows
     Queries<D, QK> qf[MT];
     uint32_t sees[MT];
-    auto seen = [&](int row) {   // positions that a row sees
-      const int x = s.length - s.tokens + row / group + 1;
-      return static_cast<uint32_t>(x < 0 ? 0 : x);
-    };
+    auto seen = [&](int row) { return s.seen(row / group); };   // positions that a row sees
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = tile * kRows + m * 16 + j;

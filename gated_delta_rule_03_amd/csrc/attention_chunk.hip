@@ -175,10 +175,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   const int turn = uniform(local / c.heads), head = local - turn * c.heads, tile = tiles - 1 - turn;
   __syncthreads();   // (sm.wide held lay_out's sums)
 
-  auto seen = [&](int row) {   // positions that a row sees
-    const int x = s.length - s.tokens + row / group + 1;
-    return static_cast<uint32_t>(x < 0 ? 0 : x);
-  };
+  auto seen = [&](int row) { return s.seen(row / group); };   // positions that a row sees
   auto seen_by = [&](int row) { return static_cast<uint32_t>(uniform(static_cast<int>(seen(row)))); };   // of a scalar
   const int wave_row = tile * kRows + wave * 32;
   const int row = wave_row + row32;

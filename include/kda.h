@@ -691,7 +691,8 @@ kda_status_t kda_read_kv(const kda_config_t *cfg, const kda_kv_cache_t *cache, i
 
 /*
  * Attention of each sequence's newest tokens over its cache, causal among them:
- *   token j of the q_n tokens of sequence n sees positions 0 .. lengths[n] - q_n + j
+ *   token j of the q_n tokens of sequence n sees positions 0 .. lengths[n] - q_n + j,
+ *   those of them that are held (also where lengths[n] passes the table)
  *   o = sum_p w_p v_p,  w = softmax over those positions of scale * q . k_p
  * where query head h reads key / value head h * num_kv_heads / num_heads.
  *   q              [n_tokens][Hq][d] io_dtype (16-byte aligned)

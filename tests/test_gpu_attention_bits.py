@@ -1,0 +1,55 @@
+"""What attention over the paged cache holds of its inputs: which positions a token sees where a length passes the table."""
+import pytest
+import torch
+
+from tests import attention_bounds as ref
+from tests.layer_reference import check
+from tests.test_gpu_kv_cache import Batch
+from tests.test_gpu_layer import BF, F32
+from tests.test_gpu_rope import kda, make_cfg  # noqa: F401  (fixture)
+
+pytestmark = pytest.mark.gpu
+
+# (d, key heads, query heads of each, tokens): rows of a key head of one sequence from one to a few hundred, so that every
+# kernel and every number of row tiles takes some
+SHAPES = [(64, 2, 4, 1), (64, 2, 4, 5), (64, 1, 5, 9), (64, 2, 2, 75), (128, 2, 4, 1), (128, 2, 3, 7), (128, 8, 26, 160),
+          (256, 2, 8, 1), (256, 2, 4, 6), (256, 2, 16, 130)]
+TYPES = [(BF, BF), (F32, BF), (BF, F32), (F32, F32)]
+
+
+def compare(kda, b, cfg, q, sees, scale, max_q, note=""):  # noqa: F811
+    """o and lse of the call against 64 bits; sees: a list of counts for each sequence."""
+    lse = torch.empty(q.shape[:2], device="cuda")
+    o = kda.kda_paged_attention(cfg, b.cache, q, *b.where, scale, max_q=max_q, lse=lse)
+    heads = sorted({0, 1, q.shape[1] // 2, q.shape[1] - 1} & set(range(q.shape[1])))
+    group = q.shape[1] // b.heads
+    cu = b.cu.tolist()
+    for i, s in enumerate(sees):
+        if not s:
+            continue
+        k, v = (x[[h // group for h in heads]] for x in b.held(i))
+        e, el, m, top = ref.attention(q[cu[i]:cu[i + 1]][:, heads].double().cpu(), k, v, s, scale)
+        rel, rl = ref.bounds(b.d, max(s + [1]), top, o.dtype)
+        check(o[cu[i]:cu[i + 1]][:, heads].cpu(), e, m, rel, f"{note} sequence {i}")
+        g = lse[cu[i]:cu[i + 1]][:, heads].double().cpu()
+        none = el.isinf()
+        assert torch.equal(g.isinf(), none) and (g[none] < 0).all()
+        ratio = ((g - el).abs() / (rl + 4 * 2.0 ** -24 * el.abs()))[~none]
+        assert (ratio <= 1).all(), f"{note} lse of sequence {i}: {float(ratio.max())} of the bound"
+
+
+@pytest.mark.parametrize("d,heads,group,tokens", SHAPES)
+@pytest.mark.parametrize("io,out", TYPES)
+def test_lengths_beyond_the_table(kda, d, heads, group, tokens, io, out):  # noqa: F811
+    """Token j sees positions 0 .. length - tokens + j, those of them that the table has room for: all of its pages are held,
+    lengths pass them by less than the tokens, by as much, and by far.  Queries of 0: the mean of what is seen, and the log of
+    its count."""
+    room = 256
+    b = Batch(kda, [(tokens, room)] * 5, heads, d, 64)
+    b.fill()
+    beyond = [0, max(1, tokens // 2), tokens, tokens + room, 2**31 - 1 - room]
+    b.lengths = torch.tensor([room + x for x in beyond], dtype=torch.int32, device="cuda")
+    q = torch.zeros(b.n, heads * group, d, dtype=io, device="cuda")
+    sees = [[min(room, room + x - tokens + j + 1) for j in range(tokens)] for x in beyond]
+    for max_q in (tokens, 0):
+        compare(kda, b, make_cfg(kda, heads * group, d, io, out), q, sees, d ** -0.5, max_q, f"max_q {max_q}")
