@@ -139,58 +139,18 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t w, float s) {
   return __builtin_bit_cast(bf16x8, make_uint4(widen<0>(w, s), widen<1>(w, s), widen<2>(w, s), widen<3>(w, s)));
 }
 
-typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x32 __attribute__((ext_vector_type(32)));
-
-// x as three 6-bit pieces.  With max|x| = 1.m 2^p the first's unit is 2^(p - 2)
-// where 1.m <= 1.875 (e2m3 reaches 7.5) and 2^(p - 1) above; what it leaves is at
-// most 4 units of 2^-4 of its own, and so on.
-__device__ __forceinline__ void split_e2m3(float (&x)[32], u32x6 (&v)[3], uint32_t& scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    const uint32_t b = __float_as_uint(x[e]) & 0x7fffffffu;
-    top = b > top ? b : top;
-  }
-  const int p = static_cast<int>(top >> 23);
-  int byte = p - 2 + ((top & 0x7fffffu) > 0x700000u);
-  byte = byte < 9 ? 9 : byte;
-  if (p == 255) {   // NaN, infinity: every product with the block is NaN
-    scale = 0xffffffu;
-    v[0] = v[1] = v[2] = u32x6{0, 0, 0, 0, 0, 0};
-    return;
-  }
-  scale = static_cast<uint32_t>(byte) | static_cast<uint32_t>(byte - 4) << 8 | static_cast<uint32_t>(byte - 8) << 16;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const float s = __uint_as_float(static_cast<uint32_t>(byte - 4 * i) << 23);
-    f32x16 even, odd;   // the conversion takes its elements from two vectors in turn
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      even[e] = x[2 * e];
-      odd[e] = x[2 * e + 1];
-    }
-    v[i] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, s);
-    if (i < 2) {
-      const f32x32 got = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(v[i], s);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x[e] -= got[e];
-    }
-  }
-}
 
 // The log of a row's sum of exponentials, from its running maximum (in base 2) and its weights' sum.
 __device__ __forceinline__ float row_lse(float m, float l) {
   return l == 0.0f ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// The chunk kernel (attention_chunk.hip), bf16 outputs: workspace, launch (scale
+// The chunk kernel (attention_chunk.hip), bf16 queries and outputs: workspace, launch (scale
 // in base 2) and the joining of its units' parts, `stride` pieces apart.
 size_t attention_chunk_ws(int D, const CacheArgs& c, int group, int64_t max_rows);
 hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale,
-                                  int64_t max_rows, void* o, float* lse, void* ws, bool in_bf16, hipStream_t st);
+                                  int64_t max_rows, void* o, float* lse, void* ws, hipStream_t st);
 hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, float* lse, const Split* joins,
                              float* pieces, int units, int stride, hipStream_t st);
 

@@ -17,16 +17,15 @@
 // weights then reach 256, which neither fp32 sums nor bf16 operands mind, and
 // the accumulators are rescaled a few times a row instead of at every step.
 //
-// Precision, by the output's type.  bf16: keys enter the matrix cores as they
-// lie in the cache (4-bit operands with their e8m0 scales), queries as the sum of
-// three 6-bit values (e2m3) with a scale for 32 channels, each the rounding of
-// what the last one left: every product and every sum of eight is exact, and a
-// query is off by at most 2^-14 of its block's largest (a bf16 one by nothing
-// above 2^-7 of it).  Next to widened keys that takes half the matrix cores'
-// time and none of the vector units'.  The weights are the sum of two bf16
-// values up to 16 rows, where the cache's bytes set the time, and one above; the
-// sum that divides is then of the rounded weights.  fp32: keys widened to bf16
-// (exact), queries as one or three bf16 values, weights as three.
+// Precision.  Keys are widened to bf16 (exact) and queries enter as they are: as
+// one bf16 value, or the three that an fp32 one is the sum of, so that scores have
+// the rounding of fp32 sums alone, whatever the channels' sizes.  (The matrix cores
+// would take the keys' 4 bits as they lie, next to queries of 6 or 8 bits.  A query
+// is then a sum of such values that share a power of two: what is small beside the
+// largest of its 32 channels loses bits that a key may turn into the whole score,
+// and 8-bit products are cut 2^13 below a step's largest.)  Weights, by the output's
+// type: fp32, three bf16 values; bf16, two up to 16 rows, where the cache's bytes
+// set the time, and one above; the sum that divides is then of the rounded weights.
 //
 // Work: all (sequence, key head, row tile) units are laid end to end in blocks
 // of 128 positions, and every workgroup takes an equal share of that line, so
@@ -54,19 +53,17 @@ __device__ __forceinline__ float* piece_at(float* pieces, int64_t slot) {
   return pieces + slot * (static_cast<int64_t>(ROWS) * (D + 2));
 }
 
-// How queries and keys meet: 6-bit pieces of queries and the keys' own 4 bits, or
-// one or three bf16 pieces and keys widened to bf16.
-enum class Qk { kF6 = 0, kBf16 = 1, kFp32 = 3 };
+// Waves a SIMD that the registers leave room for: those of the sums, and of fp32 queries' three pieces.
+constexpr int waves_of(int D, int mt, bool in_bf16) { return D / 16 * mt > 16 || (D == 256 && !in_bf16) ? 1 : 2; }
 
-// A wave's step of 32 positions as it lies in memory.  Of a position's key a lane
-// reads d / 4 channels (with 64 channels and 4-bit operands 32, lanes 32 and up
-// what lanes 0 and up do, against queries of 0).
-template <int D, Qk QK>
-constexpr int kKeyWords = QK == Qk::kF6 && D == 64 ? 4 : D / 32;
+// bf16 values that a query is held in, exactly: what it comes as, or the three of an fp32 one.
+template <bool IN_BF16>
+constexpr int kQueryPieces = IN_BF16 ? 1 : 3;
 
-template <int D, Qk QK>
+// A wave's step of 32 positions as it lies in memory.  Of a position's key a lane reads d / 4 channels.
+template <int D>
 struct RawKeys {
-  uint32_t w[2][kKeyWords<D, QK>];  // positions 2 (l % 16) and the next
+  uint32_t w[2][D / 32];            // positions 2 (l % 16) and the next
   uint32_t scale[D > 128 ? 2 : 1];  // their scale bytes, for each 32 channels of the lane
 };
 template <int D>
@@ -76,36 +73,33 @@ struct RawValues {
 };
 
 // Where a lane's bytes of a step are, from the step's first byte.
-template <int D, Qk QK>
+template <int D>
 struct LaneOffsets {
   uint32_t k, ks[D > 128 ? 2 : 1], v, vs;
 
   __device__ __forceinline__ explicit LaneOffsets(int page_shift) {
     const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-    const int part = QK == Qk::kF6 && D == 64 ? 2 * (g & 1) : g;   // quarter of the head
-    k = 2 * j * (D / 2) + part * (D / 8);
+    k = 2 * j * (D / 2) + g * (D / 8);
 #pragma unroll
-    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) ks[i] = ((part * D / 128 + i) << page_shift) + 2 * j;
+    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) ks[i] = ((g * D / 128 + i) << page_shift) + 2 * j;
     v = 8 * g * (D / 2) + j * (D / 32);
     vs = ((j * D / 512) << page_shift) + 8 * g;
   }
 };
 
-template <int D, Qk QK>
-__device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, const LaneOffsets<D, QK>& lane,
-                                          RawKeys<D, QK>& r) {
+template <int D>
+__device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, const LaneOffsets<D>& lane, RawKeys<D>& r) {
   const uint8_t* row = c.k + at.values;
   const uint8_t* scales = c.k_scale + at.scales;
-  constexpr int kWords = kKeyWords<D, QK>;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    if constexpr (kWords == 2) {
+    if constexpr (D == 64) {
       const uint2 w = *reinterpret_cast<const uint2*>(row + lane.k + t * (D / 2));
       r.w[t][0] = w.x;
       r.w[t][1] = w.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
+      for (int i = 0; i < D / 128; ++i) {
         const uint4 w = *reinterpret_cast<const uint4*>(row + lane.k + t * (D / 2) + 16 * i);
         r.w[t][4 * i] = w.x;
         r.w[t][4 * i + 1] = w.y;
@@ -118,8 +112,8 @@ __device__ __forceinline__ void load_keys(const CacheArgs& c, const StepAt& at, 
   for (int i = 0; i < (D > 128 ? 2 : 1); ++i) r.scale[i] = *reinterpret_cast<const uint16_t*>(scales + lane.ks[i]);
 }
 
-template <int D, Qk QK>
-__device__ __forceinline__ void load_values(const CacheArgs& c, const StepAt& at, const LaneOffsets<D, QK>& lane,
+template <int D>
+__device__ __forceinline__ void load_values(const CacheArgs& c, const StepAt& at, const LaneOffsets<D>& lane,
                                             RawValues<D>& r) {
   const uint8_t* row = c.v + at.values;
   r.scale = *reinterpret_cast<const uint2*>(c.v_scale + at.scales + lane.vs);
@@ -146,97 +140,47 @@ struct Rows {
 };
 
 // Queries of 16 rows as operands: a lane holds the channels of its keys.
-template <int D, Qk QK>
+template <int D, int QP>
 struct Queries {
-  SplitN<static_cast<int>(QK)> v[D / 32];
-};
-
-template <int D>
-struct Queries<D, Qk::kF6> {
-  static constexpr int kBlocks = D > 128 ? 2 : 1;
-  u32x6 v[kBlocks][3];         // 32 channels each
-  uint32_t scale[kBlocks];     // their e8m0 scales, a byte a piece
+  SplitN<QP> v[D / 32];
 };
 
 // row: the first element of the row's head; flip: 0x80008000 turns every sign.
-template <int D, Qk QK, bool BF16>
-__device__ __forceinline__ void load_queries(const void* q, size_t row, uint32_t flip, Queries<D, QK>& r) {
+template <int D, bool BF16>
+__device__ __forceinline__ void load_queries(const void* q, size_t row, uint32_t flip, Queries<D, kQueryPieces<BF16>>& r) {
   const int g = (threadIdx.x & 63) >> 4;
-  if constexpr (QK == Qk::kF6) {
 #pragma unroll
-    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) {
-      float x[32];
-      const size_t at = row + (D == 64 ? 32 * (g & 1) : g * (D / 4) + 32 * i);
+  for (int i = 0; i < D / 32; ++i) {
+    const size_t at = row + g * (D / 4) + 8 * i;
+    if constexpr (BF16) r.v[i].v[0] = load_bf16x8(static_cast<const uint16_t*>(q) + at);
+    else r.v[i] = load_split<3>(static_cast<const float*>(q) + at);
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        float y[8];
-        load_n<BF16, 8>(q, at + e, y);
-#pragma unroll
-        for (int z = 0; z < 8; ++z) x[e + z] = D == 64 && g >= 2 ? 0.0f : __uint_as_float(__float_as_uint(y[z]) ^ (flip & 0x80000000u));
-      }
-      split_e2m3(x, r.v[i], r.scale[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const size_t at = row + g * (D / 4) + 8 * i;
-      if constexpr (BF16) r.v[i].v[0] = load_bf16x8(static_cast<const uint16_t*>(q) + at);
-      else r.v[i] = load_split<3>(static_cast<const float*>(q) + at);
-#pragma unroll
-      for (int p = 0; p < static_cast<int>(QK); ++p) {
-        uint4 w = __builtin_bit_cast(uint4, r.v[i].v[p]);
-        w.x ^= flip;
-        w.y ^= flip;
-        w.z ^= flip;
-        w.w ^= flip;
-        r.v[i].v[p] = __builtin_bit_cast(bf16x8, w);
-      }
+    for (int p = 0; p < kQueryPieces<BF16>; ++p) {
+      uint4 w = __builtin_bit_cast(uint4, r.v[i].v[p]);
+      w.x ^= flip;
+      w.y ^= flip;
+      w.z ^= flip;
+      w.w ^= flip;
+      r.v[i].v[p] = __builtin_bit_cast(bf16x8, w);
     }
   }
-}
-
-// c += the keys of position t of each pair (4 bits) times piece P of the queries.
-template <int T, int P>
-__device__ __forceinline__ f32x4 mfma_f4f6(const uint32_t* k, uint32_t k_scale, const u32x6& q, uint32_t q_scale, f32x4 c) {
-  const i32x8 a = {static_cast<int>(k[0]), static_cast<int>(k[1]), static_cast<int>(k[2]), static_cast<int>(k[3]), 0, 0, 0, 0};
-  const i32x8 b = {static_cast<int>(q[0]), static_cast<int>(q[1]), static_cast<int>(q[2]), static_cast<int>(q[3]),
-                   static_cast<int>(q[4]), static_cast<int>(q[5]), 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 2, T, static_cast<int>(k_scale), P,
-                                                          static_cast<int>(q_scale));
 }
 
 // S^T of a step: element (position 8 g + e, row j) in s[.][e & 1][e >> 1].
-template <int D, int MT, Qk QK>
-__device__ __forceinline__ void scores(const RawKeys<D, QK>& r, const Queries<D, QK> (&q)[MT], f32x4 (&s)[MT][2]) {
+template <int D, int MT, int QP>
+__device__ __forceinline__ void scores(const RawKeys<D>& r, const Queries<D, QP> (&q)[MT], f32x4 (&s)[MT][2]) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) s[m][0] = s[m][1] = zero4();
-  if constexpr (QK == Qk::kF6) {
 #pragma unroll
-    for (int i = 0; i < (D > 128 ? 2 : 1); ++i) {
-      auto piece = [&](auto p) {
-        constexpr int P = decltype(p)::value;
+  for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          s[m][0] = mfma_f4f6<0, P>(&r.w[0][4 * i], r.scale[i], q[m].v[i][P], q[m].scale[i], s[m][0]);
-          s[m][1] = mfma_f4f6<1, P>(&r.w[1][4 * i], r.scale[i], q[m].v[i][P], q[m].scale[i], s[m][1]);
-        }
-      };
-      piece(std::integral_constant<int, 2>{});
-      piece(std::integral_constant<int, 1>{});
-      piece(std::integral_constant<int, 0>{});
+    for (int t = 0; t < 2; ++t) {
+      const bf16x8 k = widen8(r.w[t][i], scale_of(D > 128 && i >= 4 ? r.scale[D > 128 ? 1 : 0] : r.scale[0], t));
+#pragma unroll
+      for (int p = QP - 1; p >= 0; --p)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s[m][t] = mfma(k, q[m].v[i].v[p], s[m][t]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const bf16x8 k = widen8(r.w[t][i], scale_of(D > 128 && i >= 4 ? r.scale[D > 128 ? 1 : 0] : r.scale[0], t));
-#pragma unroll
-        for (int p = static_cast<int>(QK) - 1; p >= 0; --p)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) s[m][t] = mfma(k, q[m].v[i].v[p], s[m][t]);
-      }
-  }
 }
 
 // The step's weights, and its values' part of the sums.
@@ -352,11 +296,11 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
 
 }  // namespace
 
-template <int D, int MT, Qk QK, int PP, bool IN_BF16, bool OUT_BF16>
-__global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged_attention_kernel(
+template <int D, int MT, int PP, bool IN_BF16, bool OUT_BF16>
+__global__ __launch_bounds__(kWaves * 64, waves_of(D, MT, IN_BF16)) void paged_attention_kernel(
     CacheArgs c, const void* __restrict__ q, int group, float scale, void* __restrict__ o, float* __restrict__ lse,
     Split* __restrict__ splits, float* __restrict__ pieces) {
-  constexpr int kRows = 16 * MT;
+  constexpr int kRows = 16 * MT, QP = kQueryPieces<IN_BF16>;
   constexpr int kPitch = D + 4;
   __shared__ float meet[kWaves][16][kPitch];
   __shared__ float tops[kWaves][kRows][2];
@@ -376,7 +320,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
   const int64_t start = share * blockIdx.x;
   const int64_t end = start + share < total ? start + share : total;
   Split split = {0, 0, 0, 0, 0};
-  const LaneOffsets<D, QK> lanes(c.page_shift);
+  const LaneOffsets<D> lanes(c.page_shift);
   const int64_t page_bytes = static_cast<int64_t>(c.heads) * (D / 2) << c.page_shift;
 
   // sequences that hold nothing: their rows see nothing
@@ -410,7 +354,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
     const int b1 = end - cur < blocks - b0 ? b0 + static_cast<int>(end - cur) : blocks;
     const int head = static_cast<int>(unit / tiles), tile = static_cast<int>(unit - static_cast<int64_t>(head) * tiles);
     // this lane's rows
-    Queries<D, QK> qf[MT];
+    Queries<D, QP> qf[MT];
     uint32_t sees[MT];
     auto seen = [&](int row) { return s.seen(row / group); };   // positions that a row sees
 #pragma unroll
@@ -418,8 +362,7 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
       const int row = tile * kRows + m * 16 + j;
       const int r = row < rows ? row : rows - 1;
       const int t = r / group;
-      load_queries<D, QK, IN_BF16>(q, (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D, flip,
-                                      qf[m]);
+      load_queries<D, IN_BF16>(q, (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D, flip, qf[m]);
       sees[m] = seen(r);
     }
     // positions that every row sees, and that any does
@@ -443,17 +386,17 @@ __global__ __launch_bounds__(kWaves * 64, (D / 16) * MT > 16 ? 1 : 2) void paged
         return step_at<D>(c, n, page_bytes, head_bytes, static_cast<uint32_t>(b) * kBlockPos + first_pos, b < stop);
       };
       StepAt here = place(b0);
-      RawKeys<D, QK> keys;
-      load_keys<D, QK>(c, here, lanes, keys);
+      RawKeys<D> keys;
+      load_keys<D>(c, here, lanes, keys);
       StepAt next = place(b0 + 1);
       for (int b = b0; b < stop; ++b) {
         const uint32_t at = static_cast<uint32_t>(b) * kBlockPos + first_pos;
         RawValues<D> values;
-        load_values<D, QK>(c, here, lanes, values);
+        load_values<D>(c, here, lanes, values);
         f32x4 s4[MT][2];
-        scores<D, MT, QK>(keys, qf, s4);
+        scores<D, MT, QP>(keys, qf, s4);
         __builtin_amdgcn_sched_barrier(0);
-        load_keys<D, QK>(c, next, lanes, keys);
+        load_keys<D>(c, next, lanes, keys);
         const StepAt after = place(b + 2);
         if (here.held)
           weigh<D, MT, PP>(values, s4, scale, at + kStep <= least, at, sees, c.v_scale + here.scales, c.page_shift, acc);
@@ -663,9 +606,9 @@ namespace {
 // 144 (4 fill the registers: one wave a SIMD); d 64, 40 rows: 101, 81, 67; 30: 68, 45,
 // 66; d 256 (32 of 8192, 2 key heads), 24 rows: 54, 45.  Up to 16 rows one tile is enough,
 // and its weights keep a second piece.
-int row_tiles(int D, bool exact, int64_t rows) {
-  if (exact || rows <= 16) return 1;
-  return D == 64 && rows > 32 ? 4 : 2;
+int row_tiles(int D, bool in_bf16, bool out_bf16, int64_t rows) {
+  if (!out_bf16 || rows <= 16 || (!in_bf16 && D > 64)) return 1;
+  return D == 64 && in_bf16 && rows > 32 ? 4 : 2;
 }
 
 // Whether the chunk kernel takes a call: it reads keys and values once for 256
@@ -677,15 +620,15 @@ int row_tiles(int D, bool exact, int64_t rows) {
 //   d 256, 2 key heads, behind 8192: 32 x 256: 199, 241; 32 x 128: 154, 125; 4 x 512:
 //     83, 83; 1 x 512: 52, 36
 // (Its workgroups are the units, which have to fit a grid.)
-bool in_chunks(int D, const CacheArgs& c, int group, bool exact, int64_t rows) {
-  if (exact || (c.n_tokens * group / kChunkRows + c.N) * c.heads > kMostUnits) return false;
+bool in_chunks(int D, const CacheArgs& c, int group, bool bf16, int64_t rows) {
+  if (!bf16 || (c.n_tokens * group / kChunkRows + c.N) * c.heads > kMostUnits) return false;
   const int64_t all = c.n_tokens * c.heads * group;
   return D == 64 ? rows > 96 : D == 128 ? rows > 160 && all >= 32768 : rows > 128 && all >= 4096;
 }
 
 // Two a CU, or one where the registers leave room for one wave a SIMD (d 256, 24 rows
 // as above: 46 us, with two 63; d 128, 64 rows, where two fit: 112, with one 139).
-int workgroups(int D, int mt) { return D / 16 * mt > 16 ? kMostWorkgroups / 2 : kMostWorkgroups; }
+int workgroups(int D, int mt, bool in_bf16) { return kMostWorkgroups / 2 * waves_of(D, mt, in_bf16); }
 
 int64_t rows_of(const CacheArgs& c, int group, int max_q) {
   return (max_q > 0 ? std::min<int64_t>(max_q, c.n_tokens) : c.n_tokens) * group;
@@ -706,30 +649,32 @@ hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, floa
   return hipGetLastError();
 }
 
-size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, int max_q, bool exact) {
+size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, int max_q, bool in_bf16, bool out_bf16) {
   CacheArgs c{};
   c.n_tokens = n_tokens;
   c.N = N;
   c.heads = heads;
-  if (in_chunks(D, c, group, exact, rows_of(c, group, max_q))) return attention_chunk_ws(D, c, group, rows_of(c, group, max_q));
-  const int mt = row_tiles(D, exact, rows_of(c, group, max_q));
-  const size_t wgs = workgroups(D, mt);
+  const int64_t rows = rows_of(c, group, max_q);
+  if (in_chunks(D, c, group, in_bf16 && out_bf16, rows)) return attention_chunk_ws(D, c, group, rows);
+  const int mt = row_tiles(D, in_bf16, out_bf16, rows);
+  const size_t wgs = workgroups(D, mt, in_bf16);
   return wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4;
 }
 
 hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
                                   float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st) {
-  if (in_chunks(D, c, group, !out_bf16, rows_of(c, group, max_q)))
-    return launch_attention_chunk(D, c, q, group, scale * kLog2e, rows_of(c, group, max_q), o, lse, ws, in_bf16, st);
-  const int mt = row_tiles(D, !out_bf16, rows_of(c, group, max_q));
-  const int wgs = workgroups(D, mt);
+  const int64_t rows = rows_of(c, group, max_q);
+  if (in_chunks(D, c, group, in_bf16 && out_bf16, rows))
+    return launch_attention_chunk(D, c, q, group, scale * kLog2e, rows, o, lse, ws, st);
+  const int mt = row_tiles(D, in_bf16, out_bf16, rows);
+  const int wgs = workgroups(D, mt, in_bf16);
   Split* splits = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(splits + wgs);
   const size_t shared = (static_cast<size_t>(c.N) + 1) * 8;
-  auto go = [&](auto d, auto t, auto qk, auto pp, auto ib, auto ob) {
-    constexpr int kD = decltype(d)::value, kT = decltype(t)::value, kPP = decltype(pp)::value;
-    constexpr bool kIn = decltype(ib)::value, kOut = decltype(ob)::value;
-    paged_attention_kernel<kD, kT, decltype(qk)::value, kPP, kIn, kOut>
+  auto go = [&](auto d, auto t, auto pp, auto ib, auto ob) {
+    constexpr int kD = decltype(d)::value, kT = decltype(t)::value;
+    constexpr bool kOut = decltype(ob)::value;
+    paged_attention_kernel<kD, kT, decltype(pp)::value, decltype(ib)::value, kOut>
         <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -744,15 +689,16 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
   const integral_constant<int, 3> three;
   auto by_type = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    const integral_constant<Qk, Qk::kF6> f6;
-    if (!out_bf16) {
-      if (in_bf16) return go(d, one, integral_constant<Qk, Qk::kBf16>{}, three, true_type{}, false_type{});
-      return go(d, one, integral_constant<Qk, Qk::kFp32>{}, three, false_type{}, false_type{});
-    }
+    if (!out_bf16) return in_bf16 ? go(d, one, three, true_type{}, false_type{}) : go(d, one, three, false_type{}, false_type{});
     auto by_rows = [&](auto ib) {
-      if (mt == 1) return go(d, one, f6, two, ib, true_type{});
-      if (mt == 2) return go(d, two, f6, one, ib, true_type{});
-      if constexpr (kD == 64) return go(d, integral_constant<int, 4>{}, f6, one, ib, true_type{});
+      constexpr bool kIn = decltype(ib)::value;
+      if (mt == 1) return go(d, one, two, ib, true_type{});
+      if constexpr (kIn || kD == 64) {
+        if (mt == 2) return go(d, two, one, ib, true_type{});
+      }
+      if constexpr (kIn && kD == 64) {
+        if (mt == 4) return go(d, integral_constant<int, 4>{}, one, ib, true_type{});
+      }
       return hipErrorInvalidValue;
     };
     return in_bf16 ? by_rows(true_type{}) : by_rows(false_type{});

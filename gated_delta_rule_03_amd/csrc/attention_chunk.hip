@@ -1,6 +1,6 @@
 // Attention over the paged 4-bit cache for chunks of many new tokens, bf16
-// outputs.  The matrix cores' and vector units' time counts here, so values are
-// widened once for a whole workgroup:
+// queries and outputs.  The matrix cores' and vector units' time counts here, so
+// values are widened once for a whole workgroup:
 //
 // A workgroup has 8 waves of 32 rows (rows are a sequence's new tokens times the
 // query heads of one key head) and walks the positions in blocks.  Everything
@@ -9,11 +9,11 @@
 // for the first time together, so a block's bytes come from far away); while a
 // block is worked on, some of the lanes widen the next one's values to bf16 and
 // leave them in the order in which the matrix cores' operands read them; one
-// barrier a block.  Keys need no
-// widening: they are 4-bit operands of the 32x32x64 step, against the queries'
-// three 6-bit pieces (attention.h).  16-byte pieces of neighbouring keys lie
-// permuted, so that eight lanes' reads have no bank conflict.
-//   S^T = K Q^T   (32 positions x 32 rows), O^T += V^T P^T (32x32x16 steps)
+// barrier a block.  Keys stay in their 4 bits there, and each wave widens what it
+// multiplies (four conversions a step; shared in bf16 they would not fit the LDS at
+// 256 channels).  16-byte pieces of neighbouring keys lie permuted, so that eight lanes'
+// reads have no bank conflict.
+//   S^T = K Q^T, O^T += V^T P^T   (32 positions x 32 rows, 32x32x16 steps)
 // Lane l has row l % 32 of S^T at positions 8 b + 4 (l / 32) + i, and P^T's
 // operand takes them in that order, so weights stay in their lane.  Channel
 // 8 / NC of tile c's row r is r * NC + c (NC = D / 32 tiles): what a lane widens,
@@ -37,17 +37,6 @@ constexpr int kChunkWaves = kChunkRows / 32;
 
 __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
-// c += 32 positions' keys (4 bits) times piece P of 32 rows' queries, 64 channels.
-template <int P>
-__device__ __forceinline__ f32x16 mfma32_f4f6(const uint4& k, uint32_t k_scale, const u32x6& q, uint32_t q_scale,
-                                              const f32x16& c) {
-  const i32x8 a = {static_cast<int>(k.x), static_cast<int>(k.y), static_cast<int>(k.z), static_cast<int>(k.w), 0, 0, 0, 0};
-  const i32x8 b = {static_cast<int>(q[0]), static_cast<int>(q[1]), static_cast<int>(q[2]), static_cast<int>(q[3]),
-                   static_cast<int>(q[4]), static_cast<int>(q[5]), 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 2, 0, static_cast<int>(k_scale), P,
-                                                         static_cast<int>(q_scale));
 }
 
 // Loads from memory to LDS without registers: 16 bytes (4) a lane, lane l's to
@@ -125,7 +114,7 @@ struct ChunkShape {
 
 }  // namespace
 
-template <int D, bool IN_BF16>
+template <int D>
 __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(CacheArgs c, const void* __restrict__ q, int group,
                                                                     float scale, int splits, int units,
                                                                     void* __restrict__ o, float* __restrict__ lse,
@@ -135,13 +124,13 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   constexpr int W = kChunkWaves;
   constexpr int kRows = kChunkRows;
   constexpr int NC = D / 32;              // channel tiles
-  constexpr int kBlocks = D / 64;         // 64-channel steps of the scores
+  constexpr int kBlocks = D / 64;         // blocks of 32 channels of a lane's half of a head
   static_assert(S::kChunks <= W && 2 * S::kScaleLoads <= W && S::kTaskWaves <= W, "a load, a word a wave");
   __shared__ alignas(1024) S sm;
   extern __shared__ int32_t before[];     // [N + 1]: tiles in front of each sequence
   const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x >> 6)), row32 = lane & 31, h = lane >> 5;
   const int Hq = c.heads * group;
-  const uint32_t flip = scale < 0.0f ? 0x80000000u : 0u;
+  const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
   scale = fminf(fmaxf(fabsf(scale), 1.17549435e-38f), 3.4028235e38f);
 
   lay_out<W * 64>(c.N, before, reinterpret_cast<int64_t*>(sm.wide), [&](int n) {
@@ -187,23 +176,19 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
   const uint32_t least_all = seen_by(tile * kRows);
   const uint32_t most_all = seen_by(((tile + 1) * kRows < rows ? (tile + 1) * kRows : rows) - 1);
 
-  // queries: 64-channel step i takes channels 32 (h * D / 64 + i) ..
-  u32x6 qv[kBlocks][3];
-  uint32_t qs[kBlocks];
+  // queries: step i takes channels h * D / 2 + 8 i ..
+  bf16x8 qv[D / 16];
   {
     const int t = r / group;
     const size_t from = (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D + h * (D / 2);
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
-      float x[32];
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        float y[8];
-        load_n<IN_BF16, 8>(q, from + 32 * i + e, y);
-#pragma unroll
-        for (int z = 0; z < 8; ++z) x[e + z] = __uint_as_float(__float_as_uint(y[z]) ^ flip);
-      }
-      split_e2m3(x, qv[i], qs[i]);
+    for (int i = 0; i < D / 16; ++i) {
+      uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(q) + from + 8 * i);
+      w.x ^= flip;
+      w.y ^= flip;
+      w.z ^= flip;
+      w.w ^= flip;
+      qv[i] = __builtin_bit_cast(bf16x8, w);
     }
   }
 
@@ -374,18 +359,17 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
           uint4 kw[S::kAtOnce];
-          uint32_t ks[S::kAtOnce];
+          float ks[S::kAtOnce];
 #pragma unroll
           for (int z = 0; z < S::kAtOnce; ++z) {
             kw[z] = *reinterpret_cast<const uint4*>(keys + z * (kStep * S::kRowBytes) + S::piece(row32, h * (D / 64) + i) * 16);
-            ks[z] = scales[i * S::kPos + z * kStep];
+            ks[z] = scale_of(scales[i * S::kPos + z * kStep], 0);
           }
 #pragma unroll
-          for (int z = 0; z < S::kAtOnce; ++z) sc[z] = mfma32_f4f6<2>(kw[z], ks[z], qv[i][2], qs[i], sc[z]);
+          for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int z = 0; z < S::kAtOnce; ++z) sc[z] = mfma32_f4f6<1>(kw[z], ks[z], qv[i][1], qs[i], sc[z]);
-#pragma unroll
-          for (int z = 0; z < S::kAtOnce; ++z) sc[z] = mfma32_f4f6<0>(kw[z], ks[z], qv[i][0], qs[i], sc[z]);
+            for (int z = 0; z < S::kAtOnce; ++z)
+              sc[z] = mfma32(widen8(y == 0 ? kw[z].x : y == 1 ? kw[z].y : y == 2 ? kw[z].z : kw[z].w, ks[z]), qv[4 * i + y], sc[z]);
         }
         if (at + S::kAtOnce * kStep > least || !(held[0] && held[S::kAtOnce - 1])) {
           // (against constants: the positions of 16 elements would be kept in registers throughout)
@@ -550,26 +534,25 @@ size_t attention_chunk_ws(int D, const CacheArgs& c, int group, int64_t max_rows
 }
 
 hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale,
-                                  int64_t max_rows, void* o, float* lse, void* ws, bool in_bf16, hipStream_t st) {
+                                  int64_t max_rows, void* o, float* lse, void* ws, hipStream_t st) {
   const int64_t units = most_units(c, group);
   const int parts = parts_of(D, c, units_by(c, group, max_rows));
   Split* joins = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(joins + units);
   const dim3 grid(static_cast<unsigned>(units * parts));
   const size_t shared = (static_cast<size_t>(c.N) + 1) * 4;
-  auto go = [&](auto d, auto ib) {
+  auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    attention_chunk_kernel<kD, decltype(ib)::value><<<grid, kChunkWaves * 64, shared, st>>>(
-        c, q, group, scale, parts, static_cast<int>(units), o, lse, joins, pieces);
+    attention_chunk_kernel<kD><<<grid, kChunkWaves * 64, shared, st>>>(c, q, group, scale, parts, static_cast<int>(units), o,
+                                                                     lse, joins, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1) return e;
     return launch_join_parts(kD, c, group, o, lse, joins, pieces, static_cast<int>(units), parts, st);
   };
-  auto by_type = [&](auto d) { return in_bf16 ? go(d, std::true_type{}) : go(d, std::false_type{}); };
   switch (D) {
-    case 64: return by_type(std::integral_constant<int, 64>{});
-    case 128: return by_type(std::integral_constant<int, 128>{});
-    case 256: return by_type(std::integral_constant<int, 256>{});
+    case 64: return go(std::integral_constant<int, 64>{});
+    case 128: return go(std::integral_constant<int, 128>{});
+    case 256: return go(std::integral_constant<int, 256>{});
     default: return hipErrorInvalidValue;
   }
 }

@@ -211,7 +211,7 @@ size_t kda_paged_attention_workspace_bytes(const kda_config_t* cfg, int32_t num_
                                            int32_t max_q) {
   if (check_attention(cfg, num_kv_heads, N, n_tokens, max_q) != KDA_OK) return 0;
   return align_up(kda::paged_attention_ws(cfg->head_k_dim, N, num_kv_heads, cfg->num_heads / num_kv_heads, n_tokens, max_q,
-                                          cfg->out_dtype == KDA_FP32));
+                                          cfg->io_dtype == KDA_BF16, cfg->out_dtype == KDA_BF16));
 }
 
 kda_status_t kda_paged_attention(const kda_config_t* cfg, const kda_kv_cache_t* cache, int32_t N, int64_t n_tokens,

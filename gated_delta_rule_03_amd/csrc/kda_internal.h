@@ -222,8 +222,8 @@ hipError_t launch_append_kv(int D, const RopeArgs& r, const CacheArgs& cache, co
                             hipStream_t st);
 hipError_t launch_read_kv(int D, const CacheArgs& cache, void* k_out, void* v_out, bool out_bf16, hipStream_t st);
 
-// Attention over the cache; `exact`: fp32 outputs; max_q 0: not known.
-size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, int max_q, bool exact);
+// Attention over the cache; max_q 0: not known.
+size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, int max_q, bool in_bf16, bool out_bf16);
 hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
                                   float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st);
 

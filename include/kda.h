@@ -705,11 +705,10 @@ kda_status_t kda_read_kv(const kda_config_t *cfg, const kda_kv_cache_t *cache, i
  *   workspace      kda_paged_attention_workspace_bytes(); calls that overlap in
  *                  time need one each.  Nothing in it is kept between calls
  * Positions that a token does not see, whatever their bytes, have no effect on
- * it.  Sums and the softmax are fp32.  For bf16 outputs a query enters the
- * matrix cores as a sum of 6-bit values, within 2^-14 of the largest of its 32
- * neighbouring channels, and a weight as two bf16 values, or one where a key
- * head has more than 16 rows in a sequence (max_q * num_heads / num_kv_heads);
- * for fp32 outputs both enter as sums of bf16 values that leave fp32's
+ * it.  Sums and the softmax are fp32, queries and keys exact.  For bf16 outputs a
+ * weight enters the matrix cores as two bf16 values, or one where a key head has
+ * more than 16 rows in a sequence (max_q * num_heads / num_kv_heads); for fp32
+ * outputs as three, which leave fp32's
  * rounding.  N up to 4096 (else KDA_ERR_UNSUPPORTED).  Nothing aliases.  The
  * same inputs give the same bits on every run.
  */

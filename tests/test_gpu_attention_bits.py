@@ -1,11 +1,12 @@
-"""What attention over the paged cache holds of its inputs: which positions a token sees where a length passes the table."""
+"""What attention over the paged cache holds of its inputs: which positions a token sees where a length passes the table, and
+small channels beside large ones."""
 import pytest
 import torch
 
 from tests import attention_bounds as ref
 from tests.layer_reference import check
 from tests.test_gpu_kv_cache import Batch
-from tests.test_gpu_layer import BF, F32
+from tests.test_gpu_layer import BF, F32, Rand
 from tests.test_gpu_rope import kda, make_cfg  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
@@ -17,8 +18,9 @@ SHAPES = [(64, 2, 4, 1), (64, 2, 4, 5), (64, 1, 5, 9), (64, 2, 2, 75), (128, 2, 
 TYPES = [(BF, BF), (F32, BF), (BF, F32), (F32, F32)]
 
 
-def compare(kda, b, cfg, q, sees, scale, max_q, note=""):  # noqa: F811
-    """o and lse of the call against 64 bits; sees: a list of counts for each sequence."""
+def compare(kda, b, cfg, q, sees, scale, max_q, note="", weight=0):  # noqa: F811
+    """o and lse of the call against 64 bits; sees: a list of counts for each sequence; weight: what a weight may be off by, in
+    o (with the sum that divides) and lse."""
     lse = torch.empty(q.shape[:2], device="cuda")
     o = kda.kda_paged_attention(cfg, b.cache, q, *b.where, scale, max_q=max_q, lse=lse)
     heads = sorted({0, 1, q.shape[1] // 2, q.shape[1] - 1} & set(range(q.shape[1])))
@@ -30,6 +32,8 @@ def compare(kda, b, cfg, q, sees, scale, max_q, note=""):  # noqa: F811
         k, v = (x[[h // group for h in heads]] for x in b.held(i))
         e, el, m, top = ref.attention(q[cu[i]:cu[i + 1]][:, heads].double().cpu(), k, v, s, scale)
         rel, rl = ref.bounds(b.d, max(s + [1]), top, o.dtype)
+        if o.dtype == BF:
+            rel, rl = rel + 2 * weight, rl + weight
         check(o[cu[i]:cu[i + 1]][:, heads].cpu(), e, m, rel, f"{note} sequence {i}")
         g = lse[cu[i]:cu[i + 1]][:, heads].double().cpu()
         none = el.isinf()
@@ -53,3 +57,17 @@ def test_lengths_beyond_the_table(kda, d, heads, group, tokens, io, out):  # noq
     sees = [[min(room, room + x - tokens + j + 1) for j in range(tokens)] for x in beyond]
     for max_q in (tokens, 0):
         compare(kda, b, make_cfg(kda, heads * group, d, io, out), q, sees, d ** -0.5, max_q, f"max_q {max_q}")
+
+
+@pytest.mark.parametrize("d,heads,group,tokens", SHAPES)
+@pytest.mark.parametrize("io,out", TYPES)
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 20, 2.0 ** 60])
+def test_small_channels_beside_large_ones(kda, d, heads, group, tokens, io, out, ratio):  # noqa: F811
+    """One channel in 32 of the queries is `ratio` times the others, and the keys are 0 there: scores are the others'."""
+    b = Batch(kda, [(tokens, tokens + 90)], heads, d, 64)
+    b.fill()
+    b.cache.k[..., ::16] &= 0xf0       # the even channel of the first byte of each 32
+    q = Rand(5)(b.n, heads * group, d, dtype=io, scale=2)
+    q[..., ::32] *= ratio
+    sees = [[91 + j for j in range(tokens)]]
+    compare(kda, b, make_cfg(kda, heads * group, d, io, out), q, sees, d ** -0.5, tokens, weight=2.0 ** -8 if tokens * group > 16 else 0)
