@@ -23,9 +23,11 @@
 // would take the keys' 4 bits as they lie, next to queries of 6 or 8 bits.  A query
 // is then a sum of such values that share a power of two: what is small beside the
 // largest of its 32 channels loses bits that a key may turn into the whole score,
-// and 8-bit products are cut 2^13 below a step's largest.)  Weights, by the output's
-// type: fp32, three bf16 values; bf16, two up to 16 rows, where the cache's bytes
-// set the time, and one above; the sum that divides is then of the rounded weights.
+// and 8-bit products are cut 2^13 below a step's largest.)  Weights enter as two
+// bf16 values for bf16 outputs (off by 2^-16; one is off by 2^-8, which moves an
+// output by as much as its own rounding) and as three for fp32 ones; their sum is of
+// the weights before that, so that a token's result is the same to that precision
+// whatever else is in the call, and lse has fp32's.
 //
 // Work: all (sequence, key head, row tile) units are laid end to end in blocks
 // of 128 positions, and every workgroup takes an equal share of that line, so
@@ -221,15 +223,8 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
 #pragma unroll
     for (int e = 0; e < 4; ++e) split_pair<PP>(x[2 * e], x[2 * e + 1], w[m][e]);
     float sum = 0.f;
-    if constexpr (PP == 1) {   // of the weights as they are used
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[m][e][0]),
-                                              __builtin_bit_cast(bf16x2, sreg(0x3f803f80u)), sum, false);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += x[e];
-    }
+    for (int e = 0; e < 8; ++e) sum += x[e];
     acc.l[m] += sum;
   }
   float vs[8];
@@ -296,11 +291,11 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
 
 }  // namespace
 
-template <int D, int MT, int PP, bool IN_BF16, bool OUT_BF16>
+template <int D, int MT, bool IN_BF16, bool OUT_BF16>
 __global__ __launch_bounds__(kWaves * 64, waves_of(D, MT, IN_BF16)) void paged_attention_kernel(
     CacheArgs c, const void* __restrict__ q, int group, float scale, void* __restrict__ o, float* __restrict__ lse,
     Split* __restrict__ splits, float* __restrict__ pieces) {
-  constexpr int kRows = 16 * MT, QP = kQueryPieces<IN_BF16>;
+  constexpr int kRows = 16 * MT, QP = kQueryPieces<IN_BF16>, PP = OUT_BF16 ? 2 : 3;
   constexpr int kPitch = D + 4;
   __shared__ float meet[kWaves][16][kPitch];
   __shared__ float tops[kWaves][kRows][2];
@@ -604,8 +599,7 @@ namespace {
 // Row tiles of 16 that a workgroup takes.  us with 1, 2, 4 (64 sequences of 4096
 // positions, 8 key heads): d 128, 20 rows each: 102, 58, 140; 64 rows: 188, 110,
 // 144 (4 fill the registers: one wave a SIMD); d 64, 40 rows: 101, 81, 67; 30: 68, 45,
-// 66; d 256 (32 of 8192, 2 key heads), 24 rows: 54, 45.  Up to 16 rows one tile is enough,
-// and its weights keep a second piece.
+// 66; d 256 (32 of 8192, 2 key heads), 24 rows: 54, 45.
 int row_tiles(int D, bool in_bf16, bool out_bf16, int64_t rows) {
   if (!out_bf16 || rows <= 16 || (!in_bf16 && D > 64)) return 1;
   return D == 64 && in_bf16 && rows > 32 ? 4 : 2;
@@ -671,10 +665,10 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
   Split* splits = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(splits + wgs);
   const size_t shared = (static_cast<size_t>(c.N) + 1) * 8;
-  auto go = [&](auto d, auto t, auto pp, auto ib, auto ob) {
+  auto go = [&](auto d, auto t, auto ib, auto ob) {
     constexpr int kD = decltype(d)::value, kT = decltype(t)::value;
     constexpr bool kOut = decltype(ob)::value;
-    paged_attention_kernel<kD, kT, decltype(pp)::value, decltype(ib)::value, kOut>
+    paged_attention_kernel<kD, kT, decltype(ib)::value, kOut>
         <<<dim3(wgs), kWaves * 64, shared, st>>>(c, q, group, scale * kLog2e, o, lse, splits, pieces);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -686,18 +680,18 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
   using std::true_type;
   const integral_constant<int, 1> one;
   const integral_constant<int, 2> two;
-  const integral_constant<int, 3> three;
+  const integral_constant<int, 4> four;
   auto by_type = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    if (!out_bf16) return in_bf16 ? go(d, one, three, true_type{}, false_type{}) : go(d, one, three, false_type{}, false_type{});
+    if (!out_bf16) return in_bf16 ? go(d, one, true_type{}, false_type{}) : go(d, one, false_type{}, false_type{});
     auto by_rows = [&](auto ib) {
       constexpr bool kIn = decltype(ib)::value;
-      if (mt == 1) return go(d, one, two, ib, true_type{});
+      if (mt == 1) return go(d, one, ib, true_type{});
       if constexpr (kIn || kD == 64) {
-        if (mt == 2) return go(d, two, one, ib, true_type{});
+        if (mt == 2) return go(d, two, ib, true_type{});
       }
       if constexpr (kIn && kD == 64) {
-        if (mt == 4) return go(d, integral_constant<int, 4>{}, one, ib, true_type{});
+        if (mt == 4) return go(d, four, ib, true_type{});
       }
       return hipErrorInvalidValue;
     };

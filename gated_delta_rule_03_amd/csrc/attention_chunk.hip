@@ -14,13 +14,15 @@
 // 256 channels).  16-byte pieces of neighbouring keys lie permuted, so that eight lanes'
 // reads have no bank conflict.
 //   S^T = K Q^T, O^T += V^T P^T   (32 positions x 32 rows, 32x32x16 steps)
+// A weight is two bf16 values (attention.hip), the smaller one multiplied first.
 // Lane l has row l % 32 of S^T at positions 8 b + 4 (l / 32) + i, and P^T's
 // operand takes them in that order, so weights stay in their lane.  Channel
 // 8 / NC of tile c's row r is r * NC + c (NC = D / 32 tiles): what a lane widens,
 // 8 neighbouring channels of 8 positions, then goes to 8 neighbouring rows' or
 // tiles' places.  Two waves a SIMD, so that one's softmax runs under the other's
 // products.  Two chunks of 2048 tokens behind 16384 positions, 16 query heads on 2
-// key heads of 256: 904 us, 1.14 PFLOP/s; 32 on 8 of 128: 1.02; of 64: 0.86.
+// key heads of 256: 1270 us, 0.81 PFLOP/s of the formula's products (half as many
+// again are made for the second halves of the weights).
 //
 // A workgroup takes one (sequence, key head, row tile), the last tiles (which
 // see the most) first, or one of up to `splits` equal parts of its positions
@@ -401,20 +403,32 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
         const float base = top_of_row == neg_inf() ? 0.0f : top_of_row;
 #pragma unroll
         for (int z = 0; z < S::kAtOnce; ++z) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            w[e] = pack_bf16x2(__builtin_amdgcn_exp2f(fmaf(sc[z][2 * e], scale, -base)),
-                               __builtin_amdgcn_exp2f(fmaf(sc[z][2 * e + 1], scale, -base)));
-            sum_of_row = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[e]),
-                                                         __builtin_bit_cast(bf16x2, sreg(0x3f803f80u)), sum_of_row, false);
-          }
           const uint8_t* from = sm.wide[buf] + (step + z) * (kStep * D * 2) + lane * 16;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const bf16x8 pw = __builtin_bit_cast(bf16x8, make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
+            uint32_t w[4][2];
+            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) acc[i] = mfma32(load_bf16x8(from + (i * 2 + u) * 1024), pw, acc[i]);
+            for (int e = 0; e < 4; ++e) {
+              const float a = __builtin_amdgcn_exp2f(fmaf(sc[z][8 * u + 2 * e], scale, -base));
+              const float b = __builtin_amdgcn_exp2f(fmaf(sc[z][8 * u + 2 * e + 1], scale, -base));
+              sum += a + b;
+              split_pair<2>(a, b, w[e]);
+            }
+            sum_of_row += sum;
+            bf16x8 pw[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) pw[p] = __builtin_bit_cast(bf16x8, make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]));
+            // (two tiles in turn, since a product waits for the one before it on the same sums: 1270 us of the call above, tile
+            // by tile 1335; weights formed for 16 positions at a time, or some would be put aside at 256 channels)
+#pragma unroll
+            for (int i = 0; i < NC; i += 2) {
+              const bf16x8 v0 = load_bf16x8(from + (i * 2 + u) * 1024), v1 = load_bf16x8(from + (i * 2 + 2 + u) * 1024);
+              acc[i] = mfma32(v0, pw[1], acc[i]);
+              acc[i + 1] = mfma32(v1, pw[1], acc[i + 1]);
+              acc[i] = mfma32(v0, pw[0], acc[i]);
+              acc[i + 1] = mfma32(v1, pw[0], acc[i + 1]);
+            }
           }
         }
         int bad = 0;   // the waves that widened these steps

@@ -705,10 +705,9 @@ kda_status_t kda_read_kv(const kda_config_t *cfg, const kda_kv_cache_t *cache, i
  *   workspace      kda_paged_attention_workspace_bytes(); calls that overlap in
  *                  time need one each.  Nothing in it is kept between calls
  * Positions that a token does not see, whatever their bytes, have no effect on
- * it.  Sums and the softmax are fp32, queries and keys exact.  For bf16 outputs a
- * weight enters the matrix cores as two bf16 values, or one where a key head has
- * more than 16 rows in a sequence (max_q * num_heads / num_kv_heads); for fp32
- * outputs as three, which leave fp32's
+ * it, and a token's precision does not go by what else is in the call.  Sums and
+ * the softmax are fp32, queries and keys exact.  Weights meet the values to within
+ * 2^-16 of themselves for bf16 outputs, and for fp32 outputs to within fp32's
  * rounding.  N up to 4096 (else KDA_ERR_UNSUPPORTED).  Nothing aliases.  The
  * same inputs give the same bits on every run.
  */

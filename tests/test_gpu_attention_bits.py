@@ -1,5 +1,5 @@
-"""What attention over the paged cache holds of its inputs: which positions a token sees where a length passes the table, and
-small channels beside large ones."""
+"""What attention over the paged cache holds of its inputs: which positions a token sees where a length passes the table,
+small channels beside large ones, weights, and the log of their sum."""
 import pytest
 import torch
 
@@ -18,9 +18,8 @@ SHAPES = [(64, 2, 4, 1), (64, 2, 4, 5), (64, 1, 5, 9), (64, 2, 2, 75), (128, 2, 
 TYPES = [(BF, BF), (F32, BF), (BF, F32), (F32, F32)]
 
 
-def compare(kda, b, cfg, q, sees, scale, max_q, note="", weight=0):  # noqa: F811
-    """o and lse of the call against 64 bits; sees: a list of counts for each sequence; weight: what a weight may be off by, in
-    o (with the sum that divides) and lse."""
+def compare(kda, b, cfg, q, sees, scale, max_q, note=""):  # noqa: F811
+    """o and lse of the call against 64 bits; sees: a list of counts for each sequence."""
     lse = torch.empty(q.shape[:2], device="cuda")
     o = kda.kda_paged_attention(cfg, b.cache, q, *b.where, scale, max_q=max_q, lse=lse)
     heads = sorted({0, 1, q.shape[1] // 2, q.shape[1] - 1} & set(range(q.shape[1])))
@@ -32,8 +31,6 @@ def compare(kda, b, cfg, q, sees, scale, max_q, note="", weight=0):  # noqa: F81
         k, v = (x[[h // group for h in heads]] for x in b.held(i))
         e, el, m, top = ref.attention(q[cu[i]:cu[i + 1]][:, heads].double().cpu(), k, v, s, scale)
         rel, rl = ref.bounds(b.d, max(s + [1]), top, o.dtype)
-        if o.dtype == BF:
-            rel, rl = rel + 2 * weight, rl + weight
         check(o[cu[i]:cu[i + 1]][:, heads].cpu(), e, m, rel, f"{note} sequence {i}")
         g = lse[cu[i]:cu[i + 1]][:, heads].double().cpu()
         none = el.isinf()
@@ -70,4 +67,33 @@ def test_small_channels_beside_large_ones(kda, d, heads, group, tokens, io, out,
     q = Rand(5)(b.n, heads * group, d, dtype=io, scale=2)
     q[..., ::32] *= ratio
     sees = [[91 + j for j in range(tokens)]]
-    compare(kda, b, make_cfg(kda, heads * group, d, io, out), q, sees, d ** -0.5, tokens, weight=2.0 ** -8 if tokens * group > 16 else 0)
+    compare(kda, b, make_cfg(kda, heads * group, d, io, out), q, sees, d ** -0.5, tokens)
+
+
+@pytest.mark.parametrize("d,heads,group,tokens", SHAPES)
+@pytest.mark.parametrize("io,out", TYPES)
+def test_weights_and_their_sum(kda, d, heads, group, tokens, io, out):  # noqa: F811
+    """Scores that rise by a little at a time, so that a row's running maximum lags behind, and outputs far smaller than
+    their terms."""
+    n = tokens + 400
+    b = Batch(kda, [(tokens, n)], heads, d, 64)
+    b.fill()
+    q = Rand(7)(b.n, heads * group, d, dtype=io)
+    # half of a row's weight on one key: the scores' slope along the positions comes from the scales
+    for p in range(n):
+        b.cache.k_scale[int(b.table[0, p // 64]), :, :, p % 64] = 124 + (p * 5 // n)
+    sees = [[401 + j for j in range(tokens)]]
+    compare(kda, b, make_cfg(kda, heads * group, d, io, out), q, sees, 0.7 * d ** -0.5, tokens)
+
+
+@pytest.mark.parametrize("io,out", TYPES)
+@pytest.mark.parametrize("d,heads,group", [(64, 2, 4), (128, 2, 4), (256, 2, 8)])
+def test_a_token_beside_others(kda, d, heads, group, io, out):  # noqa: F811
+    """A decoding token is as near to 64 bits beside drafts and chunks as alone."""
+    for tokens in (1, 5, 60):
+        b = Batch(kda, [(1, 700), (tokens, 300)], heads, d, 64)
+        b.fill()
+        q = Rand(9)(b.n, heads * group, d, dtype=io, scale=2)
+        sees = [[700], [301 - tokens + j for j in range(tokens)]]
+        for max_q in (tokens, 0):
+            compare(kda, b, make_cfg(kda, heads * group, d, io, out), q, sees, d ** -0.5, max_q, f"{tokens} tokens")
