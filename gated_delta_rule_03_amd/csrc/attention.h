@@ -148,7 +148,8 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // The chunk kernel (attention_chunk.hip), bf16 queries and outputs: workspace, launch (scale
 // in base 2) and the joining of its units' parts, `stride` pieces apart.
-size_t attention_chunk_ws(int D, const CacheArgs& c, int group, int64_t max_rows);
+int64_t most_chunk_units(const CacheArgs& c, int group);   // that a call can have
+size_t attention_chunk_ws(int D, int64_t units);
 hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale,
                                   int64_t max_rows, void* o, float* lse, void* ws, hipStream_t st);
 hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, float* lse, const Split* joins,

@@ -613,11 +613,10 @@ int row_tiles(int D, bool in_bf16, bool out_bf16, int64_t rows) {
 //     1 x 4096 behind 16384: 293, 306; 1 x 1024: 99, 91; 1 x 2048 behind 512: 29, 18
 //   d 256, 2 key heads, behind 8192: 32 x 256: 199, 241; 32 x 128: 154, 125; 4 x 512:
 //     83, 83; 1 x 512: 52, 36
-// (Its workgroups are the units, which have to fit a grid.)
-bool in_chunks(int D, const CacheArgs& c, int group, bool bf16, int64_t rows) {
-  if (!bf16 || (c.n_tokens * group / kChunkRows + c.N) * c.heads > kMostUnits) return false;
+// (Its workgroups are the units, which have to fit a grid: kMostUnits.)
+bool for_chunks(int D, const CacheArgs& c, int group, bool bf16, int64_t rows) {
   const int64_t all = c.n_tokens * c.heads * group;
-  return D == 64 ? rows > 96 : D == 128 ? rows > 160 && all >= 32768 : rows > 128 && all >= 4096;
+  return bf16 && (D == 64 ? rows > 96 : D == 128 ? rows > 160 && all >= 32768 : rows > 128 && all >= 4096);
 }
 
 // Two a CU, or one where the registers leave room for one wave a SIMD (d 256, 24 rows
@@ -643,22 +642,27 @@ hipError_t launch_join_parts(int D, const CacheArgs& c, int group, void* o, floa
   return hipGetLastError();
 }
 
+// At least what every call of fewer tokens, sequences or rows needs, whichever kernel it goes to.
 size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, int max_q, bool in_bf16, bool out_bf16) {
   CacheArgs c{};
   c.n_tokens = n_tokens;
   c.N = N;
   c.heads = heads;
   const int64_t rows = rows_of(c, group, max_q);
-  if (in_chunks(D, c, group, in_bf16 && out_bf16, rows)) return attention_chunk_ws(D, c, group, rows);
-  const int mt = row_tiles(D, in_bf16, out_bf16, rows);
-  const size_t wgs = workgroups(D, mt, in_bf16);
-  return wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4;
+  size_t bytes = 0;
+  for (int mt = row_tiles(D, in_bf16, out_bf16, rows); mt > 0; mt /= 2) {
+    const size_t wgs = workgroups(D, mt, in_bf16);
+    bytes = std::max(bytes, wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4);
+  }
+  if (for_chunks(D, c, group, in_bf16 && out_bf16, rows))
+    bytes = std::max(bytes, attention_chunk_ws(D, std::min(most_chunk_units(c, group), kMostUnits)));
+  return bytes;
 }
 
 hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int group, float scale, int max_q, void* o,
                                   float* lse, void* ws, bool in_bf16, bool out_bf16, hipStream_t st) {
   const int64_t rows = rows_of(c, group, max_q);
-  if (in_chunks(D, c, group, in_bf16 && out_bf16, rows))
+  if (for_chunks(D, c, group, in_bf16 && out_bf16, rows) && most_chunk_units(c, group) <= kMostUnits)
     return launch_attention_chunk(D, c, q, group, scale * kLog2e, rows, o, lse, ws, st);
   const int mt = row_tiles(D, in_bf16, out_bf16, rows);
   const int wgs = workgroups(D, mt, in_bf16);

@@ -502,16 +502,24 @@ __global__ __launch_bounds__(kChunkWaves * 64, 2) void attention_chunk_kernel(Ca
 
 namespace {
 
-constexpr int kMostParts = 128, kMostPieces = 768;
+constexpr int kMostParts = 128;
 
-// The most units that a call can have: every sequence's last tile may be a short one.
-int64_t most_units(const CacheArgs& c, int group) { return (c.n_tokens * group / kChunkRows + c.N) * c.heads; }
+// Places for the sums of parts (256 rows each: 264 KB at 256 channels).  Up to 85
+// units, of which one round of workgroups takes three parts each, as many as one
+// round (one a CU; at 64 and 128 channels, where a place is smaller, three and two
+// rounds); above, where shares that come out even are worth a second and a third
+// round, 768: 203 MB, 103 or 52.  (One chunk behind 8192 positions, 2 key heads of
+// 256, with 256 and 768 places: 64 units 217 us both, 94 units 401 and 353.)
+int64_t most_pieces(int D, int64_t units) {
+  if (units > 85) return 768;
+  return D == 256 ? 256 : D == 128 ? 512 : 768;
+}
 
 // Units to be expected: no sequence has more than max_rows rows.  (The results
 // do not rest on it.)
 int64_t units_by(const CacheArgs& c, int group, int64_t max_rows) {
   const int64_t tiles = std::max(c.n_tokens * group / kChunkRows, (max_rows + kChunkRows - 1) / kChunkRows * c.N);
-  return std::min(tiles * c.heads, most_units(c, group));
+  return std::min(tiles * c.heads, most_chunk_units(c, group));
 }
 
 // Equal parts of each unit's positions at most, of the blocks that the page table
@@ -520,11 +528,11 @@ int64_t units_by(const CacheArgs& c, int group, int64_t max_rows) {
 // one and a half, and a part's sums, written and read again, a thirtieth on all
 // CUs.  The kernel takes fewer where the positions are few.
 template <int D>
-int parts_of(const CacheArgs& c, int64_t units) {
+int parts_of(const CacheArgs& c, int64_t units, int64_t most_units) {
   const int64_t room = (static_cast<int64_t>(c.max_pages) << c.page_shift) / ChunkShape<D>::kPos + 1;
   int best = 1;
   double least = 1e30;
-  for (int s = 1; s <= kMostParts && units * s <= kMostPieces; ++s) {
+  for (int s = 1; s <= kMostParts && (s == 1 || most_units * s <= most_pieces(D, most_units)); ++s) {
     const double cost = static_cast<double>((units * s + 255) / 256) * (static_cast<double>((room + s - 1) / s) + 2.5) +
                         (s > 1 ? 1.5 + 0.033 * static_cast<double>(units * s) : 0.0);
     if (cost < least) {
@@ -535,22 +543,26 @@ int parts_of(const CacheArgs& c, int64_t units) {
   return best;
 }
 
-int parts_of(int D, const CacheArgs& c, int64_t units) {
-  return D == 64 ? parts_of<64>(c, units) : D == 128 ? parts_of<128>(c, units) : parts_of<256>(c, units);
+int parts_of(int D, const CacheArgs& c, int64_t units, int64_t most_units) {
+  return D == 64 ? parts_of<64>(c, units, most_units) : D == 128 ? parts_of<128>(c, units, most_units) : parts_of<256>(c, units, most_units);
 }
 
 }  // namespace
 
-size_t attention_chunk_ws(int D, const CacheArgs& c, int group, int64_t max_rows) {
-  const int64_t units = units_by(c, group, max_rows), parts = units > 0 ? std::min<int64_t>(kMostParts, kMostPieces / units) : 1;
-  if (parts <= 1) return 16;
-  return most_units(c, group) * (sizeof(Split) + static_cast<size_t>(parts) * kChunkRows * (D + 2) * 4);
+// Every sequence's last tile may be a short one.
+int64_t most_chunk_units(const CacheArgs& c, int group) {
+  return (c.n_tokens * group + (kChunkRows - 1) * std::min<int64_t>(c.N, c.n_tokens)) / kChunkRows * c.heads;
+}
+
+// What any call of at most so many units needs.
+size_t attention_chunk_ws(int D, int64_t units) {
+  return units * sizeof(Split) + std::min(kMostParts * units, most_pieces(D, units)) * (static_cast<size_t>(kChunkRows) * (D + 2) * 4);
 }
 
 hipError_t launch_attention_chunk(int D, const CacheArgs& c, const void* q, int group, float scale,
                                   int64_t max_rows, void* o, float* lse, void* ws, hipStream_t st) {
-  const int64_t units = most_units(c, group);
-  const int parts = parts_of(D, c, units_by(c, group, max_rows));
+  const int64_t units = most_chunk_units(c, group);
+  const int parts = parts_of(D, c, units_by(c, group, max_rows), units);
   Split* joins = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(joins + units);
   const dim3 grid(static_cast<unsigned>(units * parts));
