@@ -6,9 +6,12 @@
 //
 // HBM-bound: each head is read once and kept in the registers of D / 16 lanes
 // (rope.h).  Such a group of lanes takes a token and a run of its heads, whose
-// sines it forms once (in fp32 from an angle reduced in 64 bits: v_sin_f32 and
-// v_cos_f32 take turns and were at most 1.2e-7 off over one turn).  32768 tokens of
-// 40 heads of 128 in bf16: 125 us (5.4 TB/s); backward, of 18 heads of 256: 242 (5.0).
+// sines it forms once, from an angle reduced in 64 bits: for bf16 outputs (in the
+// backward, bf16 gradients) with v_sin_f32 and v_cos_f32, which take turns in fp32
+// and are at most 1.2e-7 and the angle's rounding off, absolutely; for fp32 ones to
+// fp32's own rounding, by a series in 64 bits.  32768 tokens of
+// 40 heads of 128 in bf16: 125 us (5.4 TB/s); backward, of 18 heads of 256: 242 (5.0);
+// 16384 of 40 of 128 in fp32: 129 (5.2) and 140 (with the hardware's sines 128, 136).
 #include <algorithm>
 
 #include "kda_device.h"
@@ -22,15 +25,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <int D, bool INTER>
+template <int D, bool INTER, bool BF16>
 __device__ __forceinline__ void sines(const RopeArgs& r, const PairRates& p, int64_t token, float (&c)[8],
                                       float (&s)[8]) {
   const Places at(r, token);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = static_cast<float>(turns(p, at, e));
-    c[e] = __builtin_amdgcn_cosf(t);
-    s[e] = __builtin_amdgcn_sinf(t);
+    const double t = turns(p, at, e);
+    if constexpr (BF16) {
+      c[e] = __builtin_amdgcn_cosf(static_cast<float>(t));
+      s[e] = __builtin_amdgcn_sinf(static_cast<float>(t));
+    } else {
+      sincos_turns32(t, s[e], c[e]);
+    }
   }
 }
 
@@ -62,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs r, QkAr
     const size_t in0 = static_cast<size_t>(token) * (which ? x.stride[1] : x.stride[0]);
     const size_t out0 = static_cast<size_t>(token) * heads * D;
     float c[8], s[8], wa[8], wb[8];
-    if (r.rotary_dim) sines<D, INTER>(r, rates, token, c, s);
+    if (r.rotary_dim) sines<D, INTER, OUT_BF16>(r, rates, token, c, s);
     if (w) {
       load_n<false, 8>(w, runs.a, wa);
       load_n<false, 8>(w, runs.b, wb);
@@ -132,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(RopeArgs r, 
       load_n<OUT_BF16, 8, true>(x.dy[which], out + runs.b, gb);
       if (r.rotary_dim) {
         float c[8], s[8];
-        sines<D, INTER>(r, rates, token, c, s);
+        sines<D, INTER, OUT_BF16>(r, rates, token, c, s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = -s[e];   // back
         rotate<D, INTER>(runs, ga, gb, c, s);

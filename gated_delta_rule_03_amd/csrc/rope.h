@@ -92,15 +92,40 @@ struct Places {
   }
 };
 
-// Pair e's angle at the token, in turns within half a turn.  The product of a
-// 31-bit position and a 24-bit frequency is exact in 64 bits but for the one
-// rounding of the rate: 1e-10 turns at position 10^6.
+// Pair e's angle at the token, in turns within half a turn.  Three roundings in 64
+// bits, of 1 / (2 pi), of the rate and of its product with the position: together
+// within 1e-10 turns at position 10^6.
 __device__ __forceinline__ double turns(double rate, int32_t position) {
   const double t = static_cast<double>(position) * rate;
   return t - rint(t);
 }
 __device__ __forceinline__ double turns(const PairRates& p, const Places& at, int e) {
   return turns(p.rate[e], at.on((p.axes >> (2 * e)) & 3));
+}
+
+// Sine and cosine of t turns, |t| <= 1/2, to fp32's rounding also next to 0: to the
+// nearest quarter turn, then the Taylor series within an eighth in 64 bits (the
+// terms left out are below 2e-10 of the result).
+__device__ __forceinline__ void sincos_turns32(double t, float& s, float& c) {
+  const double q = rint(4.0 * t);
+  const double x = (t - 0.25 * q) * 6.283185307179586476925;
+  const double z = x * x;
+  double a = -1.0 / 39916800.0;                 // 1 / 11!
+  a = fma(a, z, 1.0 / 362880.0);
+  a = fma(a, z, -1.0 / 5040.0);
+  a = fma(a, z, 1.0 / 120.0);
+  a = fma(a, z, -1.0 / 6.0);
+  a = fma(a * z, x, x);
+  double b = -1.0 / 3628800.0;                  // 1 / 10!
+  b = fma(b, z, 1.0 / 40320.0);
+  b = fma(b, z, -1.0 / 720.0);
+  b = fma(b, z, 1.0 / 24.0);
+  b = fma(b, z, -0.5);
+  b = fma(b, z, 1.0);
+  const int n = static_cast<int>(q) & 3;
+  const float u = static_cast<float>(n & 1 ? b : a), v = static_cast<float>(n & 1 ? a : b);
+  s = n & 2 ? -u : u;
+  c = (n + 1) & 2 ? -v : v;
 }
 
 // (a, b) rotated by the pairs' sines: the runs of one lane, T float or double.
