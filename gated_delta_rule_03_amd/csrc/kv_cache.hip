@@ -82,12 +82,12 @@ __device__ __forceinline__ double rsqrt64(double x) {
   return x == __longlong_as_double(0x7ff0000000000000ll) ? 0.0 : r;
 }
 
-// y rounded to fp32, to odd.
+// y rounded to fp32, to odd: cut (the nearest value, or the one below its
+// magnitude), the last bit set where y is not that; subnormal values likewise.
 __device__ __forceinline__ float round_odd(double y) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(y));
-  constexpr uint64_t kCut = (1ull << 29) - 1;   // bits that fp32 does not have
-  const float f = static_cast<float>(__longlong_as_double(static_cast<long long>(b & ~kCut)));
-  return __uint_as_float(__float_as_uint(f) | ((b & kCut) != 0));
+  const float f = static_cast<float>(y);
+  const double near = f;
+  return __uint_as_float((__float_as_uint(f) - (fabs(near) > fabs(y))) | (near != y));
 }
 
 __device__ __forceinline__ uint32_t max_bits(const float (&x)[8]) {
