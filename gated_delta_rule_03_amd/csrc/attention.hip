@@ -597,9 +597,10 @@ __global__ __launch_bounds__(1024) void join_pieces_kernel(int heads, int group,
 namespace {
 
 // Row tiles of 16 that a workgroup takes.  us with 1, 2, 4 (64 sequences of 4096
-// positions, 8 key heads): d 128, 20 rows each: 102, 58, 140; 64 rows: 188, 110,
-// 144 (4 fill the registers: one wave a SIMD); d 64, 40 rows: 101, 81, 67; 30: 68, 45,
-// 66; d 256 (32 of 8192, 2 key heads), 24 rows: 54, 45.
+// positions, 8 key heads): d 128, 20 rows each: 93, 70, 162; 64 rows: 183, 134, 166
+// (4 fill the registers: one wave a SIMD); d 64, 30 rows: 66, 49, 78; 40: 95, 90,
+// 79; 64: 126, 91, 80; d 256 (32 of 8192, 2 key heads), 24 rows: 54, 49.  The three
+// pieces of fp32 queries leave room for two at 64 channels and one above.
 int row_tiles(int D, bool in_bf16, bool out_bf16, int64_t rows) {
   if (!out_bf16 || rows <= 16 || (!in_bf16 && D > 64)) return 1;
   return D == 64 && in_bf16 && rows > 32 ? 4 : 2;
@@ -608,21 +609,23 @@ int row_tiles(int D, bool in_bf16, bool out_bf16, int64_t rows) {
 // Whether the chunk kernel takes a call: it reads keys and values once for 256
 // rows, but computes for 256 where there are fewer, and takes longer to begin.  us
 // there and here (sequences x rows of a key head behind 4096 positions unless said):
-//   d 64, 8 key heads: 64 x 100: 123, 128; 64 x 40: 123, 73; 8 x 100 behind 1000: 30, 34
-//   d 128, 8 key heads: 64 x 256: 307, 411; 64 x 160: 285, 276; 64 x 68: 229, 157;
-//     1 x 4096 behind 16384: 293, 306; 1 x 1024: 99, 91; 1 x 2048 behind 512: 29, 18
-//   d 256, 2 key heads, behind 8192: 32 x 256: 199, 241; 32 x 128: 154, 125; 4 x 512:
-//     83, 83; 1 x 512: 52, 36
+//   d 64, 8 key heads: 64 x 192: 296, 232; 64 x 256: 295, 302; 1 x 4096: 114, 96;
+//     1 x 8192: 211, 213; 4 x 2048: 162, 164
+//   d 128, 8 key heads: 64 x 192: 419, 398; 64 x 256: 441, 519; 16 x 256: 137, 129;
+//     1 x 4096: 155, 144; 1 x 8192: 302, 329; 4 x 2048: 234, 256
+//   d 256, 2 key heads: 64 x 128: 153, 157; 64 x 160: 197, 212; 16 x 256: 115, 82;
+//     1 x 4096: 94, 87, behind 16384 213, 281; 4 x 1024: 95, 82, behind 16384 251, 277
 // (Its workgroups are the units, which have to fit a grid: kMostUnits.)
 bool for_chunks(int D, const CacheArgs& c, int group, bool bf16, int64_t rows) {
   const int64_t all = c.n_tokens * c.heads * group;
-  return bf16 && (D == 64 ? rows > 96 : D == 128 ? rows > 160 && all >= 32768 : rows > 128 && all >= 4096);
+  return bf16 && (D == 256 ? rows > 128 && all >= 8192 : rows > 192 && all >= 65536);
 }
 
 // Two a CU, or one where the registers leave room for one wave a SIMD (d 256, 24 rows
-// as above: 46 us, with two 63; d 128, 64 rows, where two fit: 112, with one 139).
+// as above: 49 us, with two 65; d 128, 64 rows, where two fit: 134, with one 173).
 int workgroups(int D, int mt, bool in_bf16) { return kMostWorkgroups / 2 * waves_of(D, mt, in_bf16); }
 
+// The rows of a key head of the longest sequence; where max_q is not known, the most that they can be.
 int64_t rows_of(const CacheArgs& c, int group, int max_q) {
   return (max_q > 0 ? std::min<int64_t>(max_q, c.n_tokens) : c.n_tokens) * group;
 }

@@ -11,10 +11,10 @@ from tests.test_gpu_rope import kda, make_cfg  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
 
-# (d, key heads, query heads of each, tokens): rows of a key head of one sequence from one to a few hundred, so that every
+# (d, key heads, query heads of each, tokens): rows of a key head of one sequence from one to thousands, so that every
 # kernel and every number of row tiles takes some
-SHAPES = [(64, 2, 4, 1), (64, 2, 4, 5), (64, 1, 5, 9), (64, 2, 2, 75), (128, 2, 4, 1), (128, 2, 3, 7), (128, 8, 26, 160),
-          (256, 2, 8, 1), (256, 2, 4, 6), (256, 2, 16, 130)]
+SHAPES = [(64, 2, 4, 1), (64, 2, 4, 5), (64, 1, 5, 9), (64, 2, 2, 75), (64, 8, 52, 160), (128, 2, 4, 1), (128, 2, 3, 7),
+          (128, 8, 52, 160), (256, 2, 8, 1), (256, 2, 4, 6), (256, 2, 16, 130), (256, 4, 16, 130)]
 TYPES = [(BF, BF), (F32, BF), (BF, F32), (F32, F32)]
 
 
