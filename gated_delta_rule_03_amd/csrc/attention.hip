@@ -55,8 +55,8 @@ __device__ __forceinline__ float* piece_at(float* pieces, int64_t slot) {
   return pieces + slot * (static_cast<int64_t>(ROWS) * (D + 2));
 }
 
-// Waves a SIMD that the registers leave room for: those of the sums, and of fp32 queries' three pieces.
-constexpr int waves_of(int D, int mt, bool in_bf16) { return D / 16 * mt > 16 || (D == 256 && !in_bf16) ? 1 : 2; }
+// Waves a SIMD that the registers leave room for.
+constexpr int waves_of(int D, int mt) { return D / 16 * mt > 16 ? 1 : 2; }
 
 // bf16 values that a query is held in, exactly: what it comes as, or the three of an fp32 one.
 template <bool IN_BF16>
@@ -141,28 +141,42 @@ struct Rows {
   float m[MT], l[MT];    // running maximum (of the row), sum of this lane's weights
 };
 
-// Queries of 16 rows as operands: a lane holds the channels of its keys.
+// Queries of 16 rows as operands: a lane holds the channels of its keys.  The
+// smallest of the three pieces of 256 channels waits in LDS (every wave's is the
+// same), or two waves a SIMD would not fit the registers.
+template <int D, int QP>
+constexpr bool kThirdInLds = D == 256 && QP == 3;
+
 template <int D, int QP>
 struct Queries {
-  SplitN<QP> v[D / 32];
+  SplitN<kThirdInLds<D, QP> ? 2 : QP> v[D / 32];
 };
 
 // row: the first element of the row's head; flip: 0x80008000 turns every sign.
 template <int D, bool BF16>
-__device__ __forceinline__ void load_queries(const void* q, size_t row, uint32_t flip, Queries<D, kQueryPieces<BF16>>& r) {
-  const int g = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ void load_queries(const void* q, size_t row, uint32_t flip, Queries<D, kQueryPieces<BF16>>& r,
+                                             uint4 (*third)[64]) {
+  constexpr int QP = kQueryPieces<BF16>;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const size_t at = row + g * (D / 4) + 8 * i;
-    if constexpr (BF16) r.v[i].v[0] = load_bf16x8(static_cast<const uint16_t*>(q) + at);
-    else r.v[i] = load_split<3>(static_cast<const float*>(q) + at);
+    SplitN<QP> x;
+    if constexpr (BF16) x.v[0] = load_bf16x8(static_cast<const uint16_t*>(q) + at);
+    else x = load_split<3>(static_cast<const float*>(q) + at);
 #pragma unroll
-    for (int p = 0; p < kQueryPieces<BF16>; ++p) {
-      uint4 w = __builtin_bit_cast(uint4, r.v[i].v[p]);
+    for (int p = 0; p < QP; ++p) {
+      uint4 w = __builtin_bit_cast(uint4, x.v[p]);
       w.x ^= flip;
       w.y ^= flip;
       w.z ^= flip;
       w.w ^= flip;
+      if constexpr (kThirdInLds<D, QP>) {
+        if (p == 2) {
+          third[i][lane] = w;
+          continue;
+        }
+      }
       r.v[i].v[p] = __builtin_bit_cast(bf16x8, w);
     }
   }
@@ -170,7 +184,11 @@ __device__ __forceinline__ void load_queries(const void* q, size_t row, uint32_t
 
 // S^T of a step: element (position 8 g + e, row j) in s[.][e & 1][e >> 1].
 template <int D, int MT, int QP>
-__device__ __forceinline__ void scores(const RawKeys<D>& r, const Queries<D, QP> (&q)[MT], f32x4 (&s)[MT][2]) {
+__device__ __forceinline__ void scores(const RawKeys<D>& r, const Queries<D, QP> (&q)[MT], const uint4 (*third)[64],
+                                       f32x4 (&s)[MT][2]) {
+  constexpr bool kThird = kThirdInLds<D, QP>;
+  int lane = threadIdx.x & 63;
+  if constexpr (kThird) asm volatile("" : "+v"(lane));   // read anew in every step, not kept across them
 #pragma unroll
   for (int m = 0; m < MT; ++m) s[m][0] = s[m][1] = zero4();
 #pragma unroll
@@ -178,8 +196,9 @@ __device__ __forceinline__ void scores(const RawKeys<D>& r, const Queries<D, QP>
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const bf16x8 k = widen8(r.w[t][i], scale_of(D > 128 && i >= 4 ? r.scale[D > 128 ? 1 : 0] : r.scale[0], t));
+      if constexpr (kThird) s[0][t] = mfma(k, load_bf16x8(&third[i][lane]), s[0][t]);
 #pragma unroll
-      for (int p = QP - 1; p >= 0; --p)
+      for (int p = (kThird ? 2 : QP) - 1; p >= 0; --p)
 #pragma unroll
         for (int m = 0; m < MT; ++m) s[m][t] = mfma(k, q[m].v[i].v[p], s[m][t]);
     }
@@ -292,13 +311,15 @@ __device__ __forceinline__ void weigh(const RawValues<D>& r, const f32x4 (&s)[MT
 }  // namespace
 
 template <int D, int MT, bool IN_BF16, bool OUT_BF16>
-__global__ __launch_bounds__(kWaves * 64, waves_of(D, MT, IN_BF16)) void paged_attention_kernel(
+__global__ __launch_bounds__(kWaves * 64, waves_of(D, MT)) void paged_attention_kernel(
     CacheArgs c, const void* __restrict__ q, int group, float scale, void* __restrict__ o, float* __restrict__ lse,
     Split* __restrict__ splits, float* __restrict__ pieces) {
   constexpr int kRows = 16 * MT, QP = kQueryPieces<IN_BF16>, PP = OUT_BF16 ? 2 : 3;
   constexpr int kPitch = D + 4;
   __shared__ float meet[kWaves][16][kPitch];
   __shared__ float tops[kWaves][kRows][2];
+  __shared__ uint4 third[kThirdInLds<D, QP> ? D / 32 : 1][64];
+  static_assert(!kThirdInLds<D, QP> || MT == 1, "one tile's");
   extern __shared__ int64_t before[];   // [N + 1]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 15, g = lane >> 4;
   const int Hq = c.heads * group;
@@ -357,7 +378,8 @@ __global__ __launch_bounds__(kWaves * 64, waves_of(D, MT, IN_BF16)) void paged_a
       const int row = tile * kRows + m * 16 + j;
       const int r = row < rows ? row : rows - 1;
       const int t = r / group;
-      load_queries<D, IN_BF16>(q, (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D, flip, qf[m]);
+      load_queries<D, IN_BF16>(q, (static_cast<size_t>(s.first + t) * Hq + head * group + (r - t * group)) * D, flip, qf[m],
+                               third);
       sees[m] = seen(r);
     }
     // positions that every row sees, and that any does
@@ -389,7 +411,7 @@ __global__ __launch_bounds__(kWaves * 64, waves_of(D, MT, IN_BF16)) void paged_a
         RawValues<D> values;
         load_values<D>(c, here, lanes, values);
         f32x4 s4[MT][2];
-        scores<D, MT, QP>(keys, qf, s4);
+        scores<D, MT, QP>(keys, qf, third, s4);
         __builtin_amdgcn_sched_barrier(0);
         load_keys<D>(c, next, lanes, keys);
         const StepAt after = place(b + 2);
@@ -623,7 +645,7 @@ bool for_chunks(int D, const CacheArgs& c, int group, bool bf16, int64_t rows) {
 
 // Two a CU, or one where the registers leave room for one wave a SIMD (d 256, 24 rows
 // as above: 49 us, with two 65; d 128, 64 rows, where two fit: 134, with one 173).
-int workgroups(int D, int mt, bool in_bf16) { return kMostWorkgroups / 2 * waves_of(D, mt, in_bf16); }
+int workgroups(int D, int mt) { return kMostWorkgroups / 2 * waves_of(D, mt); }
 
 // The rows of a key head of the longest sequence; where max_q is not known, the most that they can be.
 int64_t rows_of(const CacheArgs& c, int group, int max_q) {
@@ -654,7 +676,7 @@ size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, 
   const int64_t rows = rows_of(c, group, max_q);
   size_t bytes = 0;
   for (int mt = row_tiles(D, in_bf16, out_bf16, rows); mt > 0; mt /= 2) {
-    const size_t wgs = workgroups(D, mt, in_bf16);
+    const size_t wgs = workgroups(D, mt);
     bytes = std::max(bytes, wgs * sizeof(Split) + 2 * wgs * (16 * mt) * (D + 2) * 4);
   }
   if (for_chunks(D, c, group, in_bf16 && out_bf16, rows))
@@ -668,7 +690,7 @@ hipError_t launch_paged_attention(int D, const CacheArgs& c, const void* q, int 
   if (for_chunks(D, c, group, in_bf16 && out_bf16, rows) && most_chunk_units(c, group) <= kMostUnits)
     return launch_attention_chunk(D, c, q, group, scale * kLog2e, rows, o, lse, ws, st);
   const int mt = row_tiles(D, in_bf16, out_bf16, rows);
-  const int wgs = workgroups(D, mt, in_bf16);
+  const int wgs = workgroups(D, mt);
   Split* splits = static_cast<Split*>(ws);
   float* pieces = reinterpret_cast<float*>(splits + wgs);
   const size_t shared = (static_cast<size_t>(c.N) + 1) * 8;
