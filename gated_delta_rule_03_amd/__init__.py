@@ -945,7 +945,7 @@ def kda_paged_attention(cfg: Config, cache: KvCache, q, cu_seqlens, page_table, 
     (io dtype), over its cache (their own keys and values among it), causal:
     token j of q_n sees positions up to lengths[n] - q_n + j.  scale: 1 /
     sqrt(d) by default; max_q: at least the most tokens of one sequence (0: not
-    known; cu_seqlens None: one each).  lse: fp32 [n_tokens, num_heads], filled
+    known, the kernel is then chosen by the mean; cu_seqlens None: one each).  lse: fp32 [n_tokens, num_heads], filled
     with the log of the sum of exponentials.  Returns o, out dtype; rows behind
     cu_seqlens[N] are not written."""
     c, N, dev = _cache_at(cfg, cache, cu_seqlens, page_table, lengths)

@@ -647,9 +647,12 @@ bool for_chunks(int D, const CacheArgs& c, int group, bool bf16, int64_t rows) {
 // as above: 49 us, with two 65; d 128, 64 rows, where two fit: 134, with one 173).
 int workgroups(int D, int mt) { return kMostWorkgroups / 2 * waves_of(D, mt); }
 
-// The rows of a key head of the longest sequence; where max_q is not known, the most that they can be.
+// Rows of a key head of the longest sequence; where max_q is not known, those of
+// the mean (256 sequences of one token at 8192 positions, 2 key heads of 256: 202
+// us, and 906 when all tokens were counted as one sequence's, in the chunk kernel;
+// one long chunk among many sequences goes to the first kernel for it).
 int64_t rows_of(const CacheArgs& c, int group, int max_q) {
-  return (max_q > 0 ? std::min<int64_t>(max_q, c.n_tokens) : c.n_tokens) * group;
+  return (max_q > 0 ? std::min<int64_t>(max_q, c.n_tokens) : (c.n_tokens + c.N - 1) / c.N) * group;
 }
 
 }  // namespace
@@ -673,7 +676,7 @@ size_t paged_attention_ws(int D, int N, int heads, int group, int64_t n_tokens, 
   c.n_tokens = n_tokens;
   c.N = N;
   c.heads = heads;
-  const int64_t rows = rows_of(c, group, max_q);
+  const int64_t rows = rows_of(c, group, max_q > 0 ? max_q : static_cast<int>(std::max<int64_t>(n_tokens, 1)));
   size_t bytes = 0;
   for (int mt = row_tiles(D, in_bf16, out_bf16, rows); mt > 0; mt /= 2) {
     const size_t wgs = workgroups(D, mt);

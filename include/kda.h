@@ -698,7 +698,8 @@ kda_status_t kda_read_kv(const kda_config_t *cfg, const kda_kv_cache_t *cache, i
  *   q              [n_tokens][Hq][d] io_dtype (16-byte aligned)
  *   scale          finite, e.g. 1 / sqrt(d)
  *   max_q          at least the largest q_n, or 0 if not known: only the choice
- *                  of the kernel and of the workspace goes by it
+ *                  of the kernel (0: by the mean n_tokens / N) and the workspace
+ *                  (0: of the most that it can be) go by it
  *   o              [n_tokens][Hq][d] out_dtype; 0 for a token that sees nothing
  *   lse            [n_tokens][Hq] fp32: log(sum exp(scale * q . k_p)), -infinity
  *                  for a token that sees nothing; or NULL

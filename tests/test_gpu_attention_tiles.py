@@ -132,3 +132,15 @@ def test_far_in_a_large_cache(kda):  # noqa: F811
 @pytest.mark.parametrize("d,heads", [(64, 260), (128, 260), (256, 40)])
 def test_the_other_types_at_these_sizes(kda, d, heads, io, out):  # noqa: F811
     chunks.attend(kda, Batch(kda, [(257, 300)], heads, d, 64), 1, io, out, heads=(0, heads - 1), max_q=257)
+
+
+@pytest.mark.parametrize("d,heads,group", [(64, 8, 32), (128, 8, 32), (256, 2, 16)])
+def test_single_tokens_where_max_q_is_not_known(kda, d, heads, group):  # noqa: F811
+    """The kernel of single tokens takes them: the same bits."""
+    b = Batch(kda, [(1, 30 + i) for i in range(260)], heads, d, 64)
+    b.fill()
+    q = Rand(5)(b.n, heads * group, d, dtype=BF)
+    cfg = make_cfg(kda, heads * group, d)
+    o = kda.kda_paged_attention(cfg, b.cache, q, *b.where, max_q=1)
+    assert torch.equal(kda.kda_paged_attention(cfg, b.cache, q, *b.where), o)
+    assert torch.equal(kda.kda_paged_attention(cfg, b.cache, q, None, b.table, b.lengths), o)
