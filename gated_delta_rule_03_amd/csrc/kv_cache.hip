@@ -11,8 +11,8 @@
 // between two codes, and no power of two or 1.5 times one, is then crossed or
 // reached by that rounding, so every key is held as the nearest value.
 //
-// 65536 tokens of 2 heads of 256, 64 channels of them rotated: 61 us to append (174
-// MB, 2.9 TB/s: a token begins with five dependent loads, and 64-bit values leave
+// 65536 tokens of 2 heads of 256, 64 channels of them rotated: 51 us back to back (174
+// MB, 3.4 TB/s: a token begins with five dependent loads, and 64-bit values leave
 // registers for two waves a SIMD), 30 to read (6.1 TB/s).
 #include <algorithm>
 
@@ -362,10 +362,11 @@ dim3 grid_of(int D, int64_t groups) {
 
 hipError_t launch_append_kv(int D, const RopeArgs& r, const CacheArgs& c, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, const float* w, float eps, bool in_bf16, hipStream_t st) {
-  // heads of a group: one while the groups are few (256 tokens, 2 heads of 256: 12.0 us with the reading, with both 13.6),
-  // then as many as leave 8192 waves (the sines are formed once: 65536 tokens 94 us, with one 116)
+  // heads of a group: as many as leave 2048 waves, what the card holds of them at once (the sines are formed once).  us
+  // with 1, 2, 4, 8: 65536 tokens, 2 heads of 256: 71, 51; 16384: 20.5, 15.7; 4096: 9.5, 9.5; 16384 tokens, 8 heads of 128:
+  // 40, 30, 25, 21; 4096: 11.7, 9.5, 9.6, 14.4; 32768, 8 of 64: 50, 35, 28, 24
   const int64_t waves = c.n_tokens * c.heads * (D / 16) / 64;
-  const int run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c.heads, waves / 8192)));
+  const int run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c.heads, waves / 2048)));
   const dim3 grid = grid_of(D, c.n_tokens * ((c.heads + run - 1) / run));
   return with_head(D, in_bf16, [&](auto d, auto ib) {
     if (r.interleaved)
