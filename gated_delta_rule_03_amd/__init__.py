@@ -815,8 +815,8 @@ def kda_qk_norm_rope(cfg: Config, rope: Optional[Rope], q, k, q_weight=None, k_w
                      eps: float = 1e-6, *, q_out=None, k_out=None, stream=None):
     """y = rotate(x / sqrt(mean(x^2) + eps) * weight) per head: q [n, num_heads,
     d], k [n, kv heads, d] or None, io dtype (their tokens may be strided:
-    views into a wider projection); weights [d] fp32 or None (no norm); rope
-    None rotates nothing; positions int32 [num_axes, n] (or [n]).  Returns
+    views into a wider projection); weights [d] fp32 (of a zero-centred norm 1 +
+    its weight) or None (no norm); rope None rotates nothing; positions int32 [num_axes, n] (or [n]).  Returns
     (q_out, k_out), out dtype.  q_out=q and k_out=k work in place for
     contiguous tensors of one type."""
     dev, d, H = q.device, cfg.head_k_dim, cfg.num_heads

@@ -585,7 +585,10 @@ typedef struct kda_rope {
  *                  (a multiple of 8, >= Hq * d: a view into a wider projection)
  *   k              [n_tokens] rows of [num_kv_heads][d], k_stride apart; unused
  *                  with num_kv_heads == 0
- *   q_weight, k_weight  [d] fp32, or NULL: no norm of q / of k, the rotation alone
+ *   q_weight, k_weight  [d] fp32, or NULL: no norm of q / of k, the rotation alone.
+ *                  They multiply as they are: of a zero-centred norm, as the page's,
+ *                  whose factor is 1 + w, 1 + w is what goes here (here, in the
+ *                  backward, where the gradient is the same, and in kda_append_kv)
  *   eps            >= 0 (NaN or negative: KDA_ERR_INVALID_ARGUMENT); with 0 a row
  *                  of zeros gives NaN.  A row whose squares sum to more than
  *                  3.4e38 gives 0
