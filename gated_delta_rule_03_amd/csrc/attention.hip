@@ -633,16 +633,16 @@ int row_tiles(int D, bool in_bf16, bool out_bf16, int64_t rows) {
 // Whether the chunk kernel takes a call: it reads keys and values once for 256
 // rows, but computes for 256 where there are fewer, and takes longer to begin.  us
 // there and here (sequences x rows of a key head behind 4096 positions unless said):
-//   d 64, 8 key heads: 64 x 192: 296, 232; 64 x 256: 295, 302; 1 x 4096: 114, 96;
-//     1 x 8192: 211, 213; 4 x 2048: 162, 164
-//   d 128, 8 key heads: 64 x 192: 419, 398; 64 x 256: 441, 519; 16 x 256: 137, 129;
-//     1 x 4096: 155, 144; 1 x 8192: 302, 329; 4 x 2048: 234, 256
-//   d 256, 2 key heads: 64 x 128: 153, 157; 64 x 160: 197, 212; 16 x 256: 115, 82;
-//     1 x 4096: 94, 87, behind 16384 213, 281; 4 x 1024: 95, 82, behind 16384 251, 277
+//   d 64, 8 key heads: 64 x 160: 198, 226; 64 x 256: 232, 298; 16 x 256: 97, 80;
+//     1 x 4096: 112, 94; 1 x 8192: 208, 211; 4 x 2048: 159, 164
+//   d 128, 8 key heads: 64 x 160: 384, 327; 64 x 224: 395, 463; 16 x 256: 130, 143;
+//     1 x 4096: 146, 141; 1 x 8192: 284, 327; 4 x 2048: 219, 255
+//   d 256, 2 key heads: 64 x 128: 148, 155; 64 x 160: 193, 209; 16 x 256: 113, 80;
+//     1 x 4096: 90, 85, behind 16384 213, 281; 4 x 1024: 91, 80, behind 16384 251, 277
 // (Its workgroups are the units, which have to fit a grid: kMostUnits.)
 bool for_chunks(int D, const CacheArgs& c, int group, bool bf16, int64_t rows) {
   const int64_t all = c.n_tokens * c.heads * group;
-  return bf16 && (D == 256 ? rows > 128 && all >= 8192 : rows > 192 && all >= 65536);
+  return bf16 && rows > (D == 128 ? 192 : 128) && all >= (D == 256 ? 8192 : 65536);
 }
 
 // Two a CU, or one where the registers leave room for one wave a SIMD (d 256, 24 rows

@@ -1,5 +1,5 @@
-"""Attention of chunks at the sizes that the kernel of 256-row tiles takes (bf16; rows of a key head above 192 and 65536 of all
-heads, at 256 channels above 128 and 8192): tiles, parts, missing pages, NaN, scales, graphs, what lies far in a cache."""
+"""Attention of chunks at the sizes that the kernel of 256-row tiles takes (bf16; rows of a key head above 128, 192 at 128
+channels, and 65536 of all heads, at 256 channels 8192): tiles, parts, missing pages, NaN, scales, graphs, what lies far in a cache."""
 import pytest
 import torch
 
