@@ -19,10 +19,12 @@
 // operand takes them in that order, so weights stay in their lane.  Channel
 // 8 / NC of tile c's row r is r * NC + c (NC = D / 32 tiles): what a lane widens,
 // 8 neighbouring channels of 8 positions, then goes to 8 neighbouring rows' or
-// tiles' places.  Two waves a SIMD, so that one's softmax runs under the other's
-// products.  Two chunks of 2048 tokens behind 16384 positions, 16 query heads on 2
-// key heads of 256: 1270 us, 0.81 PFLOP/s of the formula's products (half as many
-// again are made for the second halves of the weights).
+// tiles' places.  Two waves a SIMD (four at 64 channels, two workgroups), so that
+// one's softmax runs under the other's products.  Two chunks of 2048 tokens of 16384
+// positions, 16 query heads on 2 key heads of 256: 1270 us, 0.81 PFLOP/s of the
+// formula's products (half as many again are made for the second halves of the
+// weights; matrix cores 51% busy, vector units 40); 32 on 8 of 128: 1398, 0.73; of
+// 64: 860, 0.60.
 //
 // A workgroup takes one (sequence, key head, row tile), the last tiles (which
 // see the most) first, or one of up to `splits` equal parts of its positions
@@ -146,9 +148,9 @@ __global__ __launch_bounds__(kChunkWaves * 64, D == 64 ? 4 : 2) void attention_c
   // sequence's units are numbered head by head, the last tiles (which see the most)
   // of all heads first: an XCD has few heads, whose keys and values its workgroups
   // share in its cache, as much to do as the others, and its short units at the end
-  // (one chunk of 8192 tokens, 2 key heads of 256: 505 us, with an eighth of the line
-  // of heads and tiles to each XCD 817; 8 of 128: 588 us, with the tiles of one head
-  // after the other over all XCDs 790).
+  // (one chunk of 8192 tokens, 2 key heads of 256: 690 us, 8 of 128: 790.  In a form
+  // with cheaper products 505, with an eighth of the line of heads and tiles to each
+  // XCD 817; 588, with the tiles of one head after the other over all XCDs 790.)
   const int64_t there = static_cast<int64_t>(before[c.N]) * c.heads;
   const int n_units = uniform(static_cast<int>(there < units ? there : units));
   const int place = blockIdx.x;
@@ -527,10 +529,12 @@ int64_t units_by(const CacheArgs& c, int group, int64_t max_rows) {
 }
 
 // Equal parts of each unit's positions at most, of the blocks that the page table
-// has room for: what takes the CUs (a workgroup each) the least time, counted in
-// blocks of 256 rows: a workgroup costs two and a half besides its own, the join
-// one and a half, and a part's sums, written and read again, a thirtieth on all
-// CUs.  The kernel takes fewer where the positions are few.
+// has room for: what takes the CUs (a workgroup each; the second that fits at 64
+// channels is not counted) the least time, in blocks of 256 rows: a workgroup costs
+// two and a half besides its own, the join one and a half, and a part's sums,
+// written and read again, a thirtieth on all CUs (with a quarter to a third less of
+// each, chunks of 512 to 6000 tokens behind 0 to 32768 positions took the same).
+// The kernel takes fewer where the positions are few.
 template <int D>
 int parts_of(const CacheArgs& c, int64_t units, int64_t most_units) {
   const int64_t room = (static_cast<int64_t>(c.max_pages) << c.page_shift) / ChunkShape<D>::kPos + 1;
