@@ -712,7 +712,7 @@ kda_status_t kda_read_kv(const kda_config_t *cfg, const kda_kv_cache_t *cache, i
  *                  one that is right for a call is enough for every smaller one
  *                  of the same heads and types.  At most 18 MB without, and 204
  *                  MB (103 at d 128, 52 at 64) with chunks of many rows, plus 32
- *                  bytes for each 256 rows of a key head
+ *                  bytes for each tile of up to 256 rows of a sequence and key head
  * Positions that a token does not see, whatever their bytes, have no effect on
  * it, and a token's precision does not go by what else is in the call.  Sums and
  * the softmax are fp32, queries and keys exact.  Weights meet the values to within
